@@ -28,6 +28,8 @@ GQ_WORKSPACE_ZEROED = 2
 GQ_TWO_PHASE = 4
 GQ_MX_FLOOR = 0
 GQ_MX_RCEIL = 1
+GQ_DTYPE_BF16 = 0
+GQ_DTYPE_F32 = 1
 
 # Every symbol the header declares, with its ctypes signature.
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
@@ -42,6 +44,13 @@ SIGNATURES = {
     "gq_mxfp8_dim0": (ctypes.c_int, [_P, _I64, _I64, _P, _P, ctypes.c_int, _P]),
     "gq_grouped_wgrad": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _I32, _P, _P]),
     "gq_fp8_rowwise_t_ex": (ctypes.c_int, [_P, _I64, _I64, _P, _I32, _P, _P, ctypes.c_uint32, _P, _SZ, _P]),
+    "gq_moe_sort": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I32, _I32, _P, _P, _P, _P]),
+    "gq_moe_dispatch": (ctypes.c_int, [_P, _I64, _I64, _I64, _P, _I32, _I64, _P, _P]),
+    "gq_moe_combine": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _P, _P, _I64, _I32, _P, _P]),
+    "gq_moe_combine_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _I64, _I64, _P, _P, _I64, _I32, _P, _P, _P]),
+    "gq_fp8_block_rows": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _I32, _I64, _P, _P, ctypes.c_uint32, _P]),
+    "gq_fp8_block_tiles": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_uint32, _P]),
+    "gq_grouped_mm": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, ctypes.c_int, _P, _I32, _P, _P]),
     "gq_check_device_error": (ctypes.c_int, [_P]),
     "gq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gq_last_error": (ctypes.c_char_p, []),

@@ -1,6 +1,6 @@
 // gq_api.cu -- the C ABI of libgqfp8 (declared in include/gq_fp8.h):
 // argument validation, per-device set-up, TMA descriptor encoding, the
-// per-device error word, and dispatch to the two kernels.
+// per-device error word, and dispatch to the kernels.
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -80,6 +80,10 @@ void setup_device(int dev) {
   st = wgrad::setup(info);
   if (st != GQ_OK) return;
   st = rows::setup(info);
+  if (st != GQ_OK) return;
+  st = moe::setup(info);
+  if (st != GQ_OK) return;
+  st = gmm::setup(info);
 }
 
 // Set-up for the current device (once per device per process).
@@ -216,6 +220,37 @@ gq_status validate_ws(void* ws, size_t ws_bytes, size_t need, const char* name) 
                 name, need, ws_bytes, ws == nullptr ? ", NULL" : "");
   if (!aligned(ws, 256))
     return fail(GQ_ERR_INVALID_ARG, "%s: workspace not 256-byte aligned", name);
+  return GQ_OK;
+}
+
+constexpr int64_t kMaxWidth = int64_t(1) << 22;  // columns of the MoE-layer operators' rows
+
+// Element size of a GQ_DTYPE_* code; 0 if unknown.
+int dtype_bytes(int dtype) {
+  return dtype == GQ_DTYPE_BF16 ? 2 : dtype == GQ_DTYPE_F32 ? 4 : 0;
+}
+
+// Token and slot counts of the sort, dispatch and combine calls.
+gq_status validate_slots(int64_t tokens, int32_t top_k, const char* name) {
+  if (tokens < 0 || top_k < 1)
+    return fail(GQ_ERR_INVALID_ARG, "%s: %lld tokens with %d slots each", name,
+                static_cast<long long>(tokens), top_k);
+  if (tokens > kMaxExtent || tokens * top_k > kMaxExtent)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: 2^31 slots or more", name);
+  return GQ_OK;
+}
+
+// A row buffer of `width` columns of `bytes` each, rows in 16-byte chunks.
+gq_status validate_rows(int64_t rows, int64_t width, int bytes, const char* name) {
+  if (bytes == 0) return fail(GQ_ERR_INVALID_ARG, "%s: unknown data type", name);
+  if (rows < 0 || width < 0)
+    return fail(GQ_ERR_INVALID_ARG, "%s: negative size (%lld, %lld)", name,
+                static_cast<long long>(rows), static_cast<long long>(width));
+  if (rows > kMaxExtent || width > kMaxWidth)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: 2^31 rows or more, or more than 2^22 columns", name);
+  if (width * bytes % 16 != 0)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: rows of %lld bytes are not a multiple of 16", name,
+                static_cast<long long>(width * bytes));
   return GQ_OK;
 }
 
@@ -449,6 +484,212 @@ gq_status gq_grouped_wgrad(const void* qa_t, const float* sa, const void* qx, co
                        static_cast<int32_t>(N), static_cast<int32_t>(K), offs, n_groups, out, s);
 }
 
+gq_status gq_fp8_block_rows(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld,
+                            const int32_t* pos, int32_t top_k, int64_t out_rows, void* out,
+                            float* scales, uint32_t flags, gq_stream_t stream) {
+  const char* name = "gq_fp8_block_rows";
+  if (flags & ~static_cast<uint32_t>(GQ_SCALE_POW2))
+    return fail(GQ_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name,
+                flags & ~static_cast<uint32_t>(GQ_SCALE_POW2));
+  const int size = dtype_bytes(dtype);
+  gq_status st = validate_rows(rows, K, size, name);
+  if (st != GQ_OK) return st;
+  if (pos != nullptr) {
+    st = validate_slots(rows, top_k, name);
+    if (st != GQ_OK) return st;
+    if (out_rows < 0) return fail(GQ_ERR_INVALID_ARG, "%s: negative output rows", name);
+    if (!aligned(pos, 4)) return fail(GQ_ERR_INVALID_ARG, "%s: pos not 4-byte aligned", name);
+  }
+  if (K % 16 != 0)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: K = %lld is not a multiple of 16", name,
+                static_cast<long long>(K));
+  if (ld < K || ld > kMaxExtent || ld * size % 16 != 0)
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: row pitch %lld below K = %lld or not a multiple of 16 bytes", name,
+                static_cast<long long>(ld), static_cast<long long>(K));
+  if (rows == 0 || K == 0 || (pos != nullptr && out_rows == 0)) return GQ_OK;
+  if (x == nullptr || out == nullptr || scales == nullptr)
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(scales, 4))
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: input and output must be 16-byte aligned, scales 4-byte aligned", name);
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return block::launch_rows(*info, x, dtype == GQ_DTYPE_F32, rows, K, ld, pos, top_k, out_rows, out,
+                            scales, (flags & GQ_SCALE_POW2) != 0,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_fp8_block_tiles(const void* w, int dtype, int64_t E, int64_t N, int64_t K, void* out,
+                             float* scales, uint32_t flags, gq_stream_t stream) {
+  const char* name = "gq_fp8_block_tiles";
+  if (flags & ~static_cast<uint32_t>(GQ_SCALE_POW2))
+    return fail(GQ_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name,
+                flags & ~static_cast<uint32_t>(GQ_SCALE_POW2));
+  const int size = dtype_bytes(dtype);
+  if (size == 0) return fail(GQ_ERR_INVALID_ARG, "%s: unknown data type", name);
+  if (E < 1 || N < 0 || K < 0)
+    return fail(GQ_ERR_INVALID_ARG, "%s: bad sizes (%lld, %lld, %lld)", name,
+                static_cast<long long>(E), static_cast<long long>(N), static_cast<long long>(K));
+  if (E > kMaxExtent || N > kMaxExtent || K > kMaxExtent)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: extent >= 2^31", name);
+  if (K % 16 != 0)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: K = %lld is not a multiple of 16", name,
+                static_cast<long long>(K));
+  if (N == 0 || K == 0) return GQ_OK;
+  const int64_t per = ((N + 127) / 128) * ((K + 127) / 128);  // both below 2^24: no overflow
+  if (per > kMaxExtent || E * per > kMaxExtent)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: 2^31 blocks or more", name);
+  if (w == nullptr || out == nullptr || scales == nullptr)
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(w, 16) || !aligned(out, 16) || !aligned(scales, 4))
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: input and output must be 16-byte aligned, scales 4-byte aligned", name);
+  const DeviceInfo* info = nullptr;
+  gq_status st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return block::launch_tiles(w, dtype == GQ_DTYPE_F32, E, N, K, out, scales,
+                             (flags & GQ_SCALE_POW2) != 0, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_moe_sort(const void* ids, int id_bytes, int64_t tokens, int32_t top_k,
+                      int32_t n_experts, int32_t* offs, int32_t* pos, int32_t* token,
+                      gq_stream_t stream) {
+  const char* name = "gq_moe_sort";
+  gq_status st = validate_slots(tokens, top_k, name);
+  if (st != GQ_OK) return st;
+  if (id_bytes != 4 && id_bytes != 8)
+    return fail(GQ_ERR_INVALID_ARG, "%s: ids of %d bytes (4 or 8)", name, id_bytes);
+  if (n_experts < 1)
+    return fail(GQ_ERR_INVALID_ARG, "%s: n_experts must be >= 1 (got %d)", name, n_experts);
+  if (n_experts > GQ_MAX_GROUPS)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: n_experts %d > %d", name, n_experts, GQ_MAX_GROUPS);
+  if (offs == nullptr || !aligned(offs, 4))
+    return fail(GQ_ERR_INVALID_ARG, "%s: offs NULL or misaligned", name);
+  if (tokens > 0) {
+    if (ids == nullptr || pos == nullptr || token == nullptr)
+      return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+    if (!aligned(ids, id_bytes) || !aligned(pos, 4) || !aligned(token, 4))
+      return fail(GQ_ERR_INVALID_ARG, "%s: misaligned pointer", name);
+  }
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return moe::launch_sort(ids, id_bytes == 8, tokens, top_k, n_experts, offs, pos, token,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_moe_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_t ld_bytes,
+                          const int32_t* pos, int32_t top_k, int64_t out_rows, void* out,
+                          gq_stream_t stream) {
+  const char* name = "gq_moe_dispatch";
+  gq_status st = validate_slots(tokens, top_k, name);
+  if (st != GQ_OK) return st;
+  st = validate_rows(out_rows, row_bytes, 1, name);
+  if (st != GQ_OK) return st;
+  if (ld_bytes < row_bytes || ld_bytes % 16 != 0)
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: row pitch of %lld bytes below the row or not a multiple of 16", name,
+                static_cast<long long>(ld_bytes));
+  if (tokens == 0 || row_bytes == 0 || out_rows == 0) return GQ_OK;
+  if (x == nullptr || pos == nullptr || out == nullptr)
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(x, 16) || !aligned(out, 16) || !aligned(pos, 4))
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: input and output must be 16-byte aligned, pos 4-byte aligned", name);
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return moe::launch_dispatch(x, tokens, row_bytes, ld_bytes, pos, top_k, out_rows, out,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_moe_combine(const void* y, int dtype, int64_t rows, int64_t H, const int32_t* pos,
+                         const float* weights, int64_t tokens, int32_t top_k, void* out,
+                         gq_stream_t stream) {
+  const char* name = "gq_moe_combine";
+  gq_status st = validate_slots(tokens, top_k, name);
+  if (st != GQ_OK) return st;
+  st = validate_rows(rows, H, dtype_bytes(dtype), name);
+  if (st != GQ_OK) return st;
+  if (tokens == 0 || H == 0) return GQ_OK;
+  if ((y == nullptr && rows > 0) || pos == nullptr || out == nullptr)
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(y, 16) || !aligned(out, 16) || !aligned(pos, 4) || !aligned(weights, 4))
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: rows must be 16-byte aligned, pos and weights 4-byte aligned", name);
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return moe::launch_combine(y, dtype == GQ_DTYPE_F32, rows, H, pos, weights, tokens, top_k, out,
+                             reinterpret_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_moe_combine_backward(const void* g, const void* y, int dtype, int64_t rows, int64_t H,
+                                  const int32_t* pos, const float* weights, int64_t tokens,
+                                  int32_t top_k, void* dy, float* dweights, gq_stream_t stream) {
+  const char* name = "gq_moe_combine_backward";
+  gq_status st = validate_slots(tokens, top_k, name);
+  if (st != GQ_OK) return st;
+  st = validate_rows(rows, H, dtype_bytes(dtype), name);
+  if (st != GQ_OK) return st;
+  if (tokens == 0) return GQ_OK;
+  if (pos == nullptr || weights == nullptr || dweights == nullptr)
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(pos, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+    return fail(GQ_ERR_INVALID_ARG, "%s: pos, weights and dweights must be 4-byte aligned", name);
+  if (rows > 0 && H > 0 && (g == nullptr || y == nullptr || dy == nullptr))
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(g, 16) || !aligned(y, 16) || !aligned(dy, 16))
+    return fail(GQ_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", name);
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return moe::launch_combine_backward(g, y, dtype == GQ_DTYPE_F32, rows, H, pos, weights, tokens,
+                                      top_k, dy, dweights, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_grouped_mm(const void* qa, const float* sa, int64_t M, const void* qb, const float* sb,
+                        int64_t N, int64_t K, int transpose_b, const int32_t* offs,
+                        int32_t n_groups, void* out, gq_stream_t stream) {
+  const char* name = "gq_grouped_mm";
+  if (M < 0 || N < 0 || K < 0)
+    return fail(GQ_ERR_INVALID_ARG, "%s: negative size (%lld, %lld, %lld)", name,
+                static_cast<long long>(M), static_cast<long long>(N), static_cast<long long>(K));
+  if (transpose_b != 0 && transpose_b != 1)
+    return fail(GQ_ERR_INVALID_ARG, "%s: transpose_b = %d", name, transpose_b);
+  if (n_groups < 1)
+    return fail(GQ_ERR_INVALID_ARG, "%s: n_groups must be >= 1 (got %d)", name, n_groups);
+  if (n_groups > GQ_MAX_GROUPS)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: n_groups %d > %d", name, n_groups, GQ_MAX_GROUPS);
+  if (M > kMaxExtent || N > kMaxWidth || K > kMaxWidth || n_groups * N > kMaxExtent)
+    return fail(GQ_ERR_UNSUPPORTED,
+                "%s: 2^31 rows or more, or N or K above 2^22, or n_groups * N >= 2^31", name);
+  if (N % 16 != 0 || K % 16 != 0)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: N = %lld and K = %lld must be multiples of 16", name,
+                static_cast<long long>(N), static_cast<long long>(K));
+  const int64_t inner = transpose_b ? N : K, outer = transpose_b ? K : N;
+  if (M == 0 || outer == 0) return GQ_OK;
+  if (offs == nullptr || out == nullptr)
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(offs, 4) || !aligned(out, 16))
+    return fail(GQ_ERR_INVALID_ARG, "%s: misaligned offsets or output", name);
+  if (inner == 0)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: the contraction has no columns", name);
+  if (qa == nullptr || sa == nullptr || qb == nullptr || sb == nullptr)
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL operand", name);
+  if (!aligned(qa, 16) || !aligned(qb, 16) || !aligned(sa, 4) || !aligned(sb, 4))
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: operands must be 16-byte aligned, scales 4-byte aligned", name);
+  const DeviceInfo* info = nullptr;
+  gq_status st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return gmm::launch(*info, g_dbg, qa, sa, M, qb, sb, static_cast<int32_t>(N),
+                     static_cast<int32_t>(K), transpose_b != 0, offs, n_groups, out,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
 gq_status gq_check_device_error(gq_stream_t stream) {
   const DeviceInfo* info = nullptr;
   gq_status st = current_device(&info);
@@ -488,7 +729,7 @@ const char* gq_status_string(gq_status status) {
 
 const char* gq_last_error(void) { return g_msg; }
 
-int gq_version(void) { return 200; }  // 0.2.0: mxfp8_dim0, grouped_wgrad, GQ_WORKSPACE_ZEROED
+int gq_version(void) { return 300; }  // 0.3.0: moe_sort, dispatch, combine, block scaling, grouped_mm
 
 gq_status gq_set_lag(int kind, int32_t lag) {
   if (kind != GQ_KIND_COLWISE && kind != GQ_KIND_ROWWISE_T)

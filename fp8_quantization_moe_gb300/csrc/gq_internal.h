@@ -95,6 +95,36 @@ gq_status launch(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa_t
                  const int32_t* offs, int32_t G, void* out, cudaStream_t stream);
 }  // namespace wgrad
 
+namespace block {
+gq_status launch_rows(const DeviceInfo& info, const void* x, bool f32, int64_t rows, int64_t K,
+                      int64_t ld, const int32_t* pos, int32_t top_k, int64_t out_rows, void* out,
+                      float* scales, bool pow2, cudaStream_t stream);
+gq_status launch_tiles(const void* w, bool f32, int64_t E, int64_t N, int64_t K, void* out,
+                       float* scales, bool pow2, cudaStream_t stream);
+}  // namespace block
+
+namespace moe {
+gq_status setup(DeviceInfo& info);
+gq_status launch_sort(const void* ids, bool i64, int64_t tokens, int32_t top_k, int32_t experts,
+                      int32_t* offs, int32_t* pos, int32_t* token, cudaStream_t stream);
+gq_status launch_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_t ld_bytes,
+                          const int32_t* pos, int32_t top_k, int64_t out_rows, void* out,
+                          cudaStream_t stream);
+gq_status launch_combine(const void* y, bool f32, int64_t rows, int64_t H, const int32_t* pos,
+                         const float* weights, int64_t tokens, int32_t top_k, void* out,
+                         cudaStream_t stream);
+gq_status launch_combine_backward(const void* g, const void* y, bool f32, int64_t rows, int64_t H,
+                                  const int32_t* pos, const float* weights, int64_t tokens,
+                                  int32_t top_k, void* dy, float* dweights, cudaStream_t stream);
+}  // namespace moe
+
+namespace gmm {
+gq_status setup(DeviceInfo& info);
+gq_status launch(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa, const float* sa,
+                 int64_t M, const void* qb, const float* sb, int32_t N, int32_t K, bool transposed,
+                 const int32_t* offs, int32_t E, void* out, cudaStream_t stream);
+}  // namespace gmm
+
 // Writes the scale of an empty group -- 448 / 1e-12 (fp32), or its power
 // of two below with GQ_SCALE_POW2 -- into n scales: every group is empty
 // when the token extent is 0.

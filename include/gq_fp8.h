@@ -290,6 +290,155 @@ gq_status gq_grouped_wgrad(const void* qa_t, const float* sa, const void* qx, co
                            int32_t n_groups, void* out, gq_stream_t stream);
 
 /*
+ * The operators of an fp8 MoE layer around the grouped products: tokens into
+ * expert order and back, quantization with one scale per block of 128, and
+ * the grouped product of such operands.
+ *
+ * Data types of the calls that take more than one.
+ */
+#define GQ_DTYPE_BF16 0
+#define GQ_DTYPE_F32 1
+
+/*
+ * Stable sort of the tokens' expert choices.  Slot p = t * top_k + j is
+ * token t's j-th choice; a slot whose id lies outside [0, n_experts) is
+ * dropped (an expert of another GPU, a slot over capacity).  The live slots
+ * are numbered by (id, p): "sorted rows", expert e's being
+ * [offs[e-1], offs[e]).
+ *
+ *   ids      int32 (id_bytes = 4) or int64 (8) [tokens, top_k].  (input)
+ *   tokens, top_k   tokens >= 0, top_k >= 1, tokens * top_k < 2^31.
+ *   n_experts 1 .. GQ_MAX_GROUPS.
+ *   offs     int32 [n_experts], END offsets as the other calls take them;
+ *            offs[n_experts-1] is the number of live slots.       (output)
+ *   pos      int32 [tokens, top_k]: the slot's sorted row, -1 for a dropped
+ *            slot.                                                (output)
+ *   token    int32 [tokens * top_k]: the token of each sorted row, -1 behind
+ *            the last one.                                        (output)
+ *   stream   the CUDA stream to run on.  No workspace.
+ */
+gq_status gq_moe_sort(const void* ids, int id_bytes, int64_t tokens, int32_t top_k,
+                      int32_t n_experts, int32_t* offs, int32_t* pos, int32_t* token,
+                      gq_stream_t stream);
+
+/*
+ * Token rows copied into sorted order: out[pos[t][j]] = x[t].  Positions
+ * outside [0, out_rows) are dropped slots; output rows that no slot names
+ * are left untouched.  The copy does not look at the elements: any type
+ * whose rows are multiples of 16 bytes.
+ *
+ *   x        [tokens] rows of row_bytes bytes, ld_bytes apart; 16-byte
+ *            aligned, ld_bytes >= row_bytes, both multiples of 16; row_bytes
+ *            at most 2^22.                                        (input)
+ *   pos      int32 [tokens, top_k], device.                       (input)
+ *   out      [out_rows] rows of row_bytes bytes, 16-byte aligned. (output)
+ *   stream   the CUDA stream to run on.  No workspace.
+ */
+gq_status gq_moe_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_t ld_bytes,
+                          const int32_t* pos, int32_t top_k, int64_t out_rows, void* out,
+                          gq_stream_t stream);
+
+/*
+ * The way back: out[t] = sum over j of weights[t][j] * y[pos[t][j]], in fp32,
+ * j ascending, rounded once to y's type.  Dropped slots (positions outside
+ * [0, rows)) add nothing, whatever their weight; a token with no live slot
+ * gets zeros.  Without weights (NULL) every live slot counts once: the
+ * gradient of gq_moe_dispatch.
+ *
+ *   y        bf16 or fp32 (dtype) [rows, H], 16-byte aligned.     (input)
+ *   H        a row is a multiple of 16 bytes; H <= 2^22.
+ *   pos      int32 [tokens, top_k], device.                       (input)
+ *   weights  fp32 [tokens, top_k] or NULL.                        (input)
+ *   out      y's type [tokens, H], 16-byte aligned.               (output)
+ *   stream   the CUDA stream to run on.  No workspace.
+ */
+gq_status gq_moe_combine(const void* y, int dtype, int64_t rows, int64_t H, const int32_t* pos,
+                         const float* weights, int64_t tokens, int32_t top_k, void* out,
+                         gq_stream_t stream);
+
+/*
+ * The gradients of gq_moe_combine with weights, for g = d loss / d out:
+ *   dy[pos[t][j]]  = weights[t][j] * g[t]      rounded once to g's type;
+ *   dweights[t][j] = <g[t], y[pos[t][j]]>      summed in fp32, 0 for a
+ *                                              dropped slot.
+ * Rows of dy that no slot names are left untouched.  (Without weights the
+ * gradient of gq_moe_combine is gq_moe_dispatch of g.)  Types, sizes and
+ * alignment as there; g is [tokens, H], dy [rows, H], dweights fp32
+ * [tokens, top_k].
+ */
+gq_status gq_moe_combine_backward(const void* g, const void* y, int dtype, int64_t rows, int64_t H,
+                                  const int32_t* pos, const float* weights, int64_t tokens,
+                                  int32_t top_k, void* dy, float* dweights, gq_stream_t stream);
+
+/*
+ * Quantization of rows with one scale per 1x128 block: columns [128 b,
+ * 128 b + 128) of a row (the last block of a row may be shorter) share
+ *     scale = 448 / max(amax, 1e-12)   (its power of two below with
+ *                                       GQ_SCALE_POW2)
+ * and q = e4m3(fp32(x * scale)), as in the per-group calls.  With pos the
+ * quantized row t and its scales go to the sorted rows pos[t][j] (the
+ * quantized form of gq_moe_dispatch; untouched and dropped rows as there),
+ * without it (NULL) to row t.
+ *
+ *   x        bf16 or fp32 (dtype) [rows, K], rows ld elements apart, 16-byte
+ *            aligned, a row pitch multiple of 16 bytes.           (input)
+ *   K        K % 16 == 0, K <= 2^22.
+ *   pos, top_k, out_rows   int32 [rows, top_k] or NULL (top_k and out_rows
+ *            are then ignored).                                   (input)
+ *   out      e4m3 bytes [out_rows or rows, K], 16-byte aligned.   (output)
+ *   scales   fp32 [out_rows or rows, ceil(K / 128)].              (output)
+ *   flags    0 or GQ_SCALE_POW2.
+ *   stream   the CUDA stream to run on.  No workspace.
+ */
+gq_status gq_fp8_block_rows(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld,
+                            const int32_t* pos, int32_t top_k, int64_t out_rows, void* out,
+                            float* scales, uint32_t flags, gq_stream_t stream);
+
+/*
+ * Quantization of stacked weights with one scale per 128x128 block of each
+ * expert's (N, K) matrix (the last blocks along N and K may be smaller);
+ * scale and cast as in gq_fp8_block_rows.  A transposed block is a block of
+ * the transposed matrix, so one quantized copy serves the forward and the
+ * grad_input product.
+ *
+ *   w        bf16 or fp32 (dtype) [E, N, K] row-major, 16-byte aligned. (input)
+ *   E, N, K  E >= 1, N >= 0, K >= 0, K % 16 == 0; fewer than 2^31 blocks.
+ *   out      e4m3 bytes [E, N, K], 16-byte aligned.               (output)
+ *   scales   fp32 [E, ceil(N / 128), ceil(K / 128)].              (output)
+ *   flags    0 or GQ_SCALE_POW2.
+ *   stream   the CUDA stream to run on.  No workspace.
+ */
+gq_status gq_fp8_block_tiles(const void* w, int dtype, int64_t E, int64_t N, int64_t K, void* out,
+                             float* scales, uint32_t flags, gq_stream_t stream);
+
+/*
+ * The grouped product of block-quantized rows with block-quantized stacked
+ * weights, one expert per token group.  With A = qa / sa and W = qb / sb
+ * (each block of 128 columns, or 128x128 values, divided by its scale):
+ *   transpose_b = 0:  out[m][n] = bf16( sum over k of A[m][k] * W[g][n][k] )
+ *   transpose_b = 1:  out[m][k] = bf16( sum over n of A[m][n] * W[g][n][k] )
+ * for every row m of group g: the layer's forward product and, with the same
+ * stored weights, its grad_input.  The e4m3 products of one 128-block of the
+ * contraction are summed in fp32 on the tensor cores (order unspecified),
+ * that sum is multiplied by fp32(fp32(1/sa) * fp32(1/sb)) and added in fp32.
+ *
+ *   qa       e4m3 [M, K] (transpose_b: [M, N]), 16-byte aligned.  (input)
+ *   sa       fp32 [M, ceil(columns of qa / 128)].                 (input)
+ *   qb       e4m3 [n_groups, N, K], 16-byte aligned.              (input)
+ *   sb       fp32 [n_groups, ceil(N / 128), ceil(K / 128)].       (input)
+ *   M, N, K  M < 2^31; N and K multiples of 16, at most 2^22, the one that
+ *            is summed over at least 16; n_groups * N < 2^31.
+ *   offs     int32 [n_groups] END offsets along M (as for the other calls);
+ *            rows behind the last end are left untouched.         (input)
+ *   n_groups 1 .. GQ_MAX_GROUPS.
+ *   out      bf16 [M, N] (transpose_b: [M, K]), 16-byte aligned.  (output)
+ *   stream   the CUDA stream to run on.  No workspace.
+ */
+gq_status gq_grouped_mm(const void* qa, const float* sa, int64_t M, const void* qb, const float* sb,
+                        int64_t N, int64_t K, int transpose_b, const int32_t* offs,
+                        int32_t n_groups, void* out, gq_stream_t stream);
+
+/*
  * Colwise scaling with no allocation at all, not even a caller workspace.
  * The pytorch/ao pages have no counterpart to this entry point; it exists for
  * callers that cannot obtain device memory at the point where they quantize
