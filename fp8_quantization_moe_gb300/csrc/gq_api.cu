@@ -149,6 +149,27 @@ gq_status encode_tiled_2d(CUtensorMap* map, CUtensorMapDataType dtype,
   return GQ_OK;
 }
 
+gq_status encode_tiled_3d(CUtensorMap* map, CUtensorMapDataType dtype,
+                          void* base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
+                          uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0,
+                          uint32_t box1, CUtensorMapSwizzle swizzle) {
+  std::call_once(g_encode_once, load_encode_fn);
+  if (g_encode == nullptr) return g_encode_status;
+  const cuuint64_t dims[3] = {dim0, dim1, dim2};
+  const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
+  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, dtype, 3, base, dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(GQ_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %llux%llux%llu",
+                static_cast<int>(r), static_cast<unsigned long long>(dim0),
+                static_cast<unsigned long long>(dim1), static_cast<unsigned long long>(dim2));
+  return GQ_OK;
+}
+
 WorkspaceLayout colwise_workspace(int64_t K, int64_t G) {
   auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
   WorkspaceLayout L;

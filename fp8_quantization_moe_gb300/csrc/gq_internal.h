@@ -20,6 +20,7 @@ struct DeviceInfo {
   int rowwise_ctas_per_sm = 0;
   int mx_ctas_per_sm = 0;
   int rows_ctas_per_sm = 0;
+  int mm_pairs = 0;  // block pairs of grouped_mm that are resident at once
 };
 
 // Launch-time knobs (test hooks).
@@ -34,6 +35,12 @@ struct DebugKnobs {
 gq_status encode_tiled_2d(CUtensorMap* map, CUtensorMapDataType dtype,
                           void* base, uint64_t dim0, uint64_t dim1,
                           uint64_t row_stride_bytes, uint32_t box0,
+                          uint32_t box1, CUtensorMapSwizzle swizzle);
+
+// Encodes a 3-D tiled tensor map whose boxes are one deep along dim2.
+gq_status encode_tiled_3d(CUtensorMap* map, CUtensorMapDataType dtype,
+                          void* base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
+                          uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0,
                           uint32_t box1, CUtensorMapSwizzle swizzle);
 
 // Records a message for gq_last_error() and returns `st`.

@@ -18,6 +18,7 @@
 
 #include "gq_device.cuh"
 #include "gq_internal.h"
+#include "gq_tcgen05.cuh"
 
 namespace gq {
 namespace moe {
@@ -42,35 +43,6 @@ struct SortParams {
   int64_t per_warp;  // slots of a warp's segment, a multiple of 32
   int32_t top_k, experts;
 };
-
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// The word at shared address `addr` of block `rank` of this cluster.
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr, uint32_t rank) {
-  uint32_t v;
-  asm volatile(
-      "{\n\t.reg .b32 a;\n\t"
-      "mapa.shared::cluster.u32 a, %1, %2;\n\t"
-      "ld.shared::cluster.u32 %0, [a];\n\t}"
-      : "=r"(v)
-      : "r"(addr), "r"(rank)
-      : "memory");
-  return v;
-}
 
 // The expert of slot p, or -1.
 template <bool kI64>
@@ -125,7 +97,7 @@ __global__ void __launch_bounds__(kSortWarpsMax * 32) sort_kernel(const SortPara
     uint32_t before = 0, all = 0;
     if (e < E) {
       for (uint32_t c = 0; c < nblocks; ++c) {
-        const uint32_t v = ld_cluster_u32(smem_addr(total + e), c);
+        const uint32_t v = ld_cluster_u32(map_cluster(smem_addr(total + e), c));
         if (c < rank) before += v;
         all += v;
       }

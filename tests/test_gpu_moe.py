@@ -462,3 +462,22 @@ def test_binding_refuses_bad_arguments(gq):
         gq.sort_tokens(pos, 0)
     with pytest.raises(gq.GQError):
         gq.block_rows(torch.zeros(4, 40, dtype=torch.bfloat16, device=DEV))
+
+
+def test_grouped_mm_timeout_is_reported_not_hung(gq):
+    """A withheld accumulator release makes the first pair's MMAs wait in
+    vain: every role leaves its loop after the (shortened) limit, the call
+    reports GQ_ERR_TIMEOUT, and the next call is fine."""
+    M, N, K = 64, 256, 1024
+    qa, sa = gq.block_rows(activations(1, M, K, torch.bfloat16))
+    qb, sb = gq.block_tiles(activations(2, N, K, torch.bfloat16)[None])
+    o = torch.tensor([M], dtype=torch.int32, device=DEV)
+    try:
+        gq.debug_set(skip_arrival=True, wait_timeout_ns=5_000_000)
+        gq.grouped_mm(qa, sa, qb, sb, o)
+        with pytest.raises(gq.GQError) as e:
+            gq.check_device_error()
+        assert e.value.status == 4
+    finally:
+        gq.debug_set(False, 0)
+    check_product(gq, M, N, K, [M], False)
