@@ -1,0 +1,91 @@
+// gq_grouped_mm.cuh -- what the two kernels of the grouped block-scaled
+// product share: parameters, and the list of tiles that the group ends give.
+// A tile is (group, `rows` rows of it, `cols` output columns); within a group
+// the row tiles run fastest, so that blocks at work at the same time share
+// the weights of a column tile.
+#pragma once
+
+#include "gq_device.cuh"
+#include "gq_internal.h"
+
+namespace gq {
+namespace gmm {
+
+constexpr int kBlock = 128;  // contraction columns per scale, and per stage
+constexpr int kSubK = 32;    // contraction columns per MMA (kind::f8f6f4)
+
+struct Params {
+  const float* sa;
+  const float* sb;
+  const int32_t* offs;
+  uint16_t* out;
+  unsigned* err;
+  int32_t M, E, inner, outer;
+  int32_t kbs;           // 128-blocks of the contraction
+  int32_t tiles_c;       // tiles along the output columns
+  int64_t sb_expert;     // scales per expert
+  int32_t sb_c, sb_k;    // scale strides along output and contraction blocks
+  int32_t sb_last;       // last output block
+  bool sa_vec;           // rows of sa are 16-byte aligned
+  bool transposed;
+  uint64_t timeout_ns;
+  int32_t skip_arrival;  // test hook: block 0 never frees its first accumulator
+};
+
+// The table of tiles, in shared memory.
+struct TileTable {
+  int32_t ends[kMaxGroups];
+  int32_t first[kMaxGroups + 1];  // row tiles before each group
+};
+
+// Fills the table (one warp).
+__device__ __forceinline__ void build_tiles(const Params& p, int32_t rows, TileTable& s, int lane) {
+  build_ends(p.offs, 0, p.E, p.M, s.ends, lane);
+  __syncwarp();
+  int32_t carry = 0;
+  for (int base = 0; base < p.E; base += 32) {
+    const int g = base + lane;
+    int32_t v = 0;
+    if (g < p.E) v = (s.ends[g] - (g > 0 ? s.ends[g - 1] : 0) + rows - 1) / rows;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= d) v += o;
+    }
+    if (g < p.E) s.first[g + 1] = carry + v;
+    carry += __shfl_sync(0xffffffffu, v, 31);
+  }
+  if (lane == 0) s.first[0] = 0;
+}
+
+struct Tile {
+  int32_t g, c0, m0, rows;  // group, first column, first row, rows of the group from there
+};
+
+__device__ __forceinline__ Tile tile_of(const Params& p, const TileTable& s, int32_t i,
+                                        int32_t rows, int32_t cols) {
+  // the last group whose first tile is at or before i
+  int32_t lo = 0, hi = p.E;
+  while (hi - lo > 1) {
+    const int32_t mid = (lo + hi) >> 1;
+    if (s.first[mid] * p.tiles_c <= i) lo = mid; else hi = mid;
+  }
+  Tile t;
+  t.g = lo;
+  const int32_t tt = s.first[lo + 1] - s.first[lo];
+  const int32_t r = i - s.first[lo] * p.tiles_c;
+  const int32_t start = lo > 0 ? s.ends[lo - 1] : 0;
+  t.c0 = (r / tt) * cols;
+  t.m0 = start + (r % tt) * rows;
+  t.rows = s.ends[lo] - t.m0;
+  return t;
+}
+
+// The product of many rows per group (gq_grouped_mm.cu) and of few
+// (gq_grouped_mm_few.cu).
+gq_status setup_few(DeviceInfo& info);
+gq_status launch_few(const DeviceInfo& info, Params p, const void* qa, const void* qb, int32_t N,
+                     int32_t K, cudaStream_t stream);
+
+}  // namespace gmm
+}  // namespace gq
