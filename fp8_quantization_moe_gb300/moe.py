@@ -21,8 +21,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._binding import (GQ_DTYPE_BF16, GQ_DTYPE_F32, GQ_SCALE_POW2, _check, _ptr, _stream_handle,
-                       lib)
+from ._binding import GQ_DTYPE_BF16, GQ_DTYPE_F32, GQ_SCALE_POW2, _check, lib
 
 BLOCK = 128
 _DTYPES = {torch.bfloat16: GQ_DTYPE_BF16, torch.float32: GQ_DTYPE_F32}
@@ -42,30 +41,42 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
-def _call(name: str, dev: torch.device, fn, *args):
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args)
+# A call on small sizes is as long as its host side: the current stream and
+# device are asked for directly (0.1 us each; torch.cuda.current_stream takes
+# 2 us), and an argument's checks are one expression.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device = torch._C._cuda_getDevice
+
+
+def _call(name: str, index: int, stream, fn, *args):
+    """Calls the library on device ``index``; the stream is its last argument."""
+    sh = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _get_device() == index:
+        st = fn(*args, sh)
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args)
+        with torch.cuda.device(index):
+            st = fn(*args, sh)
     if st:
         _check(st, name)
 
 
-def _cuda(t, what: str, ndim: int, dtypes, dev: Optional[torch.device] = None, shape=None,
-          contiguous: bool = True):
-    """Raises unless t is a CUDA tensor of that rank, type, device and shape."""
+def _need(t, what: str, ndim: int, dtypes, index: int = -1, shape=None, contiguous: bool = True):
+    """Raises ValueError unless t is a CUDA tensor of that rank, type and, where
+    given, device and shape."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == ndim
+            and (t.get_device() == index if index >= 0 else t.is_cuda)
+            and (shape is None or t.shape == shape) and (not contiguous or t.is_contiguous())):
+        return
     if not (isinstance(t, torch.Tensor) and t.is_cuda):
         raise ValueError(f"{what} must be a CUDA tensor")
     if t.dtype not in dtypes or t.dim() != ndim:
         raise ValueError(f"{what} must be a {ndim}-D tensor of "
                          + " or ".join(str(d).removeprefix("torch.") for d in dtypes))
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, not {tuple(t.shape)}")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{what} must be on {dev}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if index >= 0 and t.get_device() != index:
+        raise ValueError(f"{what} must be on cuda:{index}")
+    raise ValueError(f"{what} must be contiguous")
 
 
 _INT = (torch.int32, torch.int64)
@@ -92,15 +103,14 @@ def sort_tokens(ids: torch.Tensor, n_experts: int, *, stream=None) -> TokenOrder
     outside [0, n_experts) is dropped.  Live slots of one expert keep their
     order (token, then choice).  Returns a TokenOrder.
     """
-    _cuda(ids, "sort_tokens: ids", 2, _INT)
+    _need(ids, "sort_tokens: ids", 2, _INT)
     T, k = ids.shape
     dev = ids.device
     offs = torch.empty(n_experts if n_experts > 0 else 0, dtype=torch.int32, device=dev)
     pos = torch.empty((T, k), dtype=torch.int32, device=dev)
     token = torch.empty(T * k, dtype=torch.int32, device=dev)
-    _call("gq_moe_sort", dev, lib().gq_moe_sort, ids.data_ptr(), ids.element_size(), T, k,
-          n_experts, offs.data_ptr(), pos.data_ptr(), token.data_ptr(),
-          _stream_handle(stream, dev))
+    _call("gq_moe_sort", dev.index, stream, lib().gq_moe_sort, ids.data_ptr(), ids.element_size(),
+          T, k, n_experts, offs.data_ptr(), pos.data_ptr(), token.data_ptr())
     return TokenOrder(offs, pos, token)
 
 
@@ -119,43 +129,45 @@ def dispatch(x: torch.Tensor, pos: torch.Tensor, *, out=None, stream=None) -> to
     T, H = x.shape
     dev = x.device
     pitch = _pitch(x, "dispatch: x")
-    _cuda(pos, "dispatch: pos", 2, _I32, dev)
+    _need(pos, "dispatch: pos", 2, _I32, dev.index)
     if pos.shape[0] != T:
         raise ValueError("dispatch: pos must have a row for each row of x")
     k = pos.shape[1]
     if out is None:
         out = torch.empty((T * k, H), dtype=x.dtype, device=dev)
     else:
-        _cuda(out, "dispatch: out", 2, (x.dtype,), dev, (out.shape[0], H))
+        _need(out, "dispatch: out", 2, (x.dtype,), dev.index)
+        if out.shape[1] != H:
+            raise ValueError(f"dispatch: out must have rows of {H} columns")
     size = x.element_size()
-    _call("gq_moe_dispatch", dev, lib().gq_moe_dispatch, x.data_ptr(), T, H * size, pitch * size,
-          pos.data_ptr(), k, out.shape[0], out.data_ptr(), _stream_handle(stream, dev))
+    _call("gq_moe_dispatch", dev.index, stream, lib().gq_moe_dispatch, x.data_ptr(), T, H * size,
+          pitch * size, pos.data_ptr(), k, out.shape[0], out.data_ptr())
     return out
 
 
 def _block_rows(name, x, pos, out, scales, pow2_scales, stream):
-    _cuda(x, f"{name}: x", 2, _FLOAT, contiguous=False)
+    _need(x, name + ": x", 2, _FLOAT, contiguous=False)
     T, K = x.shape
     dev = x.device
-    pitch = _pitch(x, f"{name}: x")
+    pitch = _pitch(x, name + ": x")
     k, rows = 1, T
     if pos is not None:
-        _cuda(pos, f"{name}: pos", 2, _I32, dev)
+        _need(pos, name + ": pos", 2, _I32, dev.index)
         if pos.shape[0] != T:
             raise ValueError(f"{name}: pos must have a row for each row of x")
         k = pos.shape[1]
-        rows = T * k if out is None else out.shape[0]
+        rows = T * k if out is None else len(out)
     if out is None:
         out = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=dev)
     else:
-        _cuda(out, f"{name}: out", 2, _FP8, dev, (rows, K))
+        _need(out, name + ": out", 2, _FP8, dev.index, (rows, K))
     if scales is None:
         scales = torch.empty((rows, _blocks(K)), dtype=torch.float32, device=dev)
     else:
-        _cuda(scales, f"{name}: scales", 2, _F32, dev, (rows, _blocks(K)))
-    _call("gq_fp8_block_rows", dev, lib().gq_fp8_block_rows, x.data_ptr(), _DTYPES[x.dtype], T, K,
-          pitch, _ptr(pos), k, rows, out.data_ptr(), scales.data_ptr(),
-          GQ_SCALE_POW2 if pow2_scales else 0, _stream_handle(stream, dev))
+        _need(scales, name + ": scales", 2, _F32, dev.index, (rows, _blocks(K)))
+    _call("gq_fp8_block_rows", dev.index, stream, lib().gq_fp8_block_rows, x.data_ptr(),
+          _DTYPES[x.dtype], T, K, pitch, None if pos is None else pos.data_ptr(), k, rows,
+          out.data_ptr(), scales.data_ptr(), GQ_SCALE_POW2 if pow2_scales else 0)
     return out, scales
 
 
@@ -182,20 +194,20 @@ def block_tiles(w: torch.Tensor, *, out=None, scales=None, pow2_scales: bool = F
     bf16 or float32 (E, N, K) CUDA tensor, K % 16 == 0.  Returns (q
     float8_e4m3fn (E, N, K), scales float32 (E, ceil(N / 128),
     ceil(K / 128)))."""
-    _cuda(w, "block_tiles: w", 3, _FLOAT)
+    _need(w, "block_tiles: w", 3, _FLOAT)
     E, N, K = w.shape
     dev = w.device
     if out is None:
         out = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=dev)
     else:
-        _cuda(out, "block_tiles: out", 3, _FP8, dev, (E, N, K))
+        _need(out, "block_tiles: out", 3, _FP8, dev.index, (E, N, K))
     if scales is None:
         scales = torch.empty((E, _blocks(N), _blocks(K)), dtype=torch.float32, device=dev)
     else:
-        _cuda(scales, "block_tiles: scales", 3, _F32, dev, (E, _blocks(N), _blocks(K)))
-    _call("gq_fp8_block_tiles", dev, lib().gq_fp8_block_tiles, w.data_ptr(), _DTYPES[w.dtype], E, N,
-          K, out.data_ptr(), scales.data_ptr(), GQ_SCALE_POW2 if pow2_scales else 0,
-          _stream_handle(stream, dev))
+        _need(scales, "block_tiles: scales", 3, _F32, dev.index, (E, _blocks(N), _blocks(K)))
+    _call("gq_fp8_block_tiles", dev.index, stream, lib().gq_fp8_block_tiles, w.data_ptr(),
+          _DTYPES[w.dtype], E, N, K, out.data_ptr(), scales.data_ptr(),
+          GQ_SCALE_POW2 if pow2_scales else 0)
     return out, scales
 
 
@@ -212,24 +224,25 @@ def grouped_mm(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.T
     (M, N) and out (M, K) = A @ W[g]: grad_input with the same weights.  Rows
     behind the last end keep ``out``.
     """
-    _cuda(qb, "grouped_mm: qb", 3, _FP8)
+    _need(qb, "grouped_mm: qb", 3, _FP8)
     E, N, K = qb.shape
     dev = qb.device
+    index = dev.index
     inner, outer = (N, K) if transpose_b else (K, N)
-    _cuda(qa, "grouped_mm: qa", 2, _FP8, dev)
+    _need(qa, "grouped_mm: qa", 2, _FP8, index)
     M = qa.shape[0]
     if qa.shape[1] != inner:
         raise ValueError(f"grouped_mm: qa must have {inner} columns, not {qa.shape[1]}")
-    _cuda(sa, "grouped_mm: sa", 2, _F32, dev, (M, _blocks(inner)))
-    _cuda(sb, "grouped_mm: sb", 3, _F32, dev, (E, _blocks(N), _blocks(K)))
-    _cuda(offs, "grouped_mm: offs", 1, _I32, dev, (E,))
+    _need(sa, "grouped_mm: sa", 2, _F32, index, (M, _blocks(inner)))
+    _need(sb, "grouped_mm: sb", 3, _F32, index, (E, _blocks(N), _blocks(K)))
+    _need(offs, "grouped_mm: offs", 1, _I32, index, (E,))
     if out is None:
         out = torch.empty((M, outer), dtype=torch.bfloat16, device=dev)
     else:
-        _cuda(out, "grouped_mm: out", 2, (torch.bfloat16,), dev, (M, outer))
-    _call("gq_grouped_mm", dev, lib().gq_grouped_mm, qa.data_ptr(), sa.data_ptr(), M,
+        _need(out, "grouped_mm: out", 2, (torch.bfloat16,), index, (M, outer))
+    _call("gq_grouped_mm", index, stream, lib().gq_grouped_mm, qa.data_ptr(), sa.data_ptr(), M,
           qb.data_ptr(), sb.data_ptr(), N, K, 1 if transpose_b else 0, offs.data_ptr(), E,
-          out.data_ptr(), _stream_handle(stream, dev))
+          out.data_ptr())
     return out
 
 
@@ -244,19 +257,21 @@ def combine(y: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] 
     [0, rows)) add nothing; a token without live slots gets zeros.  Returns
     out (tokens, H) of y's type.
     """
-    _cuda(y, "combine: y", 2, _FLOAT)
+    _need(y, "combine: y", 2, _FLOAT)
     rows, H = y.shape
     dev = y.device
-    _cuda(pos, "combine: pos", 2, _I32, dev)
+    index = dev.index
+    _need(pos, "combine: pos", 2, _I32, index)
     T, k = pos.shape
     if weights is not None:
-        _cuda(weights, "combine: weights", 2, _F32, dev, (T, k))
+        _need(weights, "combine: weights", 2, _F32, index, (T, k))
     if out is None:
         out = torch.empty((T, H), dtype=y.dtype, device=dev)
     else:
-        _cuda(out, "combine: out", 2, (y.dtype,), dev, (T, H))
-    _call("gq_moe_combine", dev, lib().gq_moe_combine, y.data_ptr(), _DTYPES[y.dtype], rows, H,
-          pos.data_ptr(), _ptr(weights), T, k, out.data_ptr(), _stream_handle(stream, dev))
+        _need(out, "combine: out", 2, (y.dtype,), index, (T, H))
+    _call("gq_moe_combine", index, stream, lib().gq_moe_combine, y.data_ptr(), _DTYPES[y.dtype],
+          rows, H, pos.data_ptr(), None if weights is None else weights.data_ptr(), T, k,
+          out.data_ptr())
     return out
 
 
@@ -267,22 +282,23 @@ def combine_backward(g: torch.Tensor, y: torch.Tensor, pos: torch.Tensor, weight
     weights[t, j] * g[t] at row pos[t, j], dweights float32 (tokens, top_k) =
     <g[t], y[pos[t, j]]>, 0 for a dropped slot).  Rows of dy that no slot
     names keep ``dy``."""
-    _cuda(y, "combine_backward: y", 2, _FLOAT)
+    _need(y, "combine_backward: y", 2, _FLOAT)
     rows, H = y.shape
     dev = y.device
-    _cuda(pos, "combine_backward: pos", 2, _I32, dev)
+    index = dev.index
+    _need(pos, "combine_backward: pos", 2, _I32, index)
     T, k = pos.shape
-    _cuda(g, "combine_backward: g", 2, (y.dtype,), dev, (T, H))
-    _cuda(weights, "combine_backward: weights", 2, _F32, dev, (T, k))
+    _need(g, "combine_backward: g", 2, (y.dtype,), index, (T, H))
+    _need(weights, "combine_backward: weights", 2, _F32, index, (T, k))
     if dy is None:
         dy = torch.empty((rows, H), dtype=y.dtype, device=dev)
     else:
-        _cuda(dy, "combine_backward: dy", 2, (y.dtype,), dev, (rows, H))
+        _need(dy, "combine_backward: dy", 2, (y.dtype,), index, (rows, H))
     if dweights is None:
         dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
     else:
-        _cuda(dweights, "combine_backward: dweights", 2, _F32, dev, (T, k))
-    _call("gq_moe_combine_backward", dev, lib().gq_moe_combine_backward, g.data_ptr(), y.data_ptr(),
-          _DTYPES[y.dtype], rows, H, pos.data_ptr(), weights.data_ptr(), T, k, dy.data_ptr(),
-          dweights.data_ptr(), _stream_handle(stream, dev))
+        _need(dweights, "combine_backward: dweights", 2, _F32, index, (T, k))
+    _call("gq_moe_combine_backward", index, stream, lib().gq_moe_combine_backward, g.data_ptr(),
+          y.data_ptr(), _DTYPES[y.dtype], rows, H, pos.data_ptr(), weights.data_ptr(), T, k,
+          dy.data_ptr(), dweights.data_ptr())
     return dy, dweights
