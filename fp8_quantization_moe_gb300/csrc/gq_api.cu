@@ -537,7 +537,7 @@ gq_status gq_fp8_block_rows(const void* x, int dtype, int64_t rows, int64_t K, i
   const DeviceInfo* info = nullptr;
   st = current_device(&info);
   if (st != GQ_OK) return st;
-  return block::launch_rows(*info, x, dtype == GQ_DTYPE_F32, rows, K, ld, pos, top_k, out_rows, out,
+  return block::launch_rows(x, dtype == GQ_DTYPE_F32, rows, K, ld, pos, top_k, out_rows, out,
                             scales, (flags & GQ_SCALE_POW2) != 0,
                             reinterpret_cast<cudaStream_t>(stream));
 }
@@ -597,7 +597,7 @@ gq_status gq_moe_sort(const void* ids, int id_bytes, int64_t tokens, int32_t top
   const DeviceInfo* info = nullptr;
   st = current_device(&info);
   if (st != GQ_OK) return st;
-  return moe::launch_sort(ids, id_bytes == 8, tokens, top_k, n_experts, offs, pos, token,
+  return moe::launch_sort(*info, ids, id_bytes == 8, tokens, top_k, n_experts, offs, pos, token,
                           reinterpret_cast<cudaStream_t>(stream));
 }
 

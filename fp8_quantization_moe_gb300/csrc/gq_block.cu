@@ -91,47 +91,69 @@ struct RowParams {
   uint8_t* q;
   float* scales;
   const int32_t* pos;  // (rows, top_k) destination rows, or nullptr: row r goes to row r
-  int64_t rows, out_rows;
+  uint32_t blocks;     // 128-blocks of all rows
+  int64_t out_rows;
   int64_t ld_bytes;    // bytes from one input row to the next
-  int32_t K, nb, segs;  // columns, 128-blocks per row, 512-column segments per row
+  int32_t K, nb;       // columns, 128-blocks per row
   int32_t top_k;
   bool pow2;
 };
 
-// One warp per (row, 512-column segment): four 128-blocks, eight lanes each.
+// Eight lanes per 1x128 block, four consecutive blocks (of one row or of two)
+// per warp.  A token is read once and its quantized block stored to each of
+// its sorted rows; one whose slots are all dropped is not read at all.
+// 16,381 tokens of 2064 columns with 6 slots of which a quarter are live:
+// 28.5 us -> see the launch.
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowParams p) {
   const int lane = threadIdx.x & 31;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kThreads / 32);
-  const int64_t total = p.rows * p.segs;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-       i < total; i += nwarps) {
-    const int64_t row = i / p.segs;
-    const int32_t col = static_cast<int32_t>(i % p.segs) * (32 * kUnit) + lane * kUnit;
-    const bool in = col < p.K;  // K % 16 == 0: a unit is wholly inside or outside
-    Unit<kF32> u;
-    if (in)
-      u.load(p.x + row * p.ld_bytes + static_cast<int64_t>(col) * (kF32 ? 4 : 2));
-    else
-      u.clear();
-    uint32_t m = u.amax_bits();
+  const uint32_t i = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 4 + (lane >> 3);
+  const uint32_t row32 = i < p.blocks ? i / static_cast<uint32_t>(p.nb) : 0u;
+  const int64_t row = row32;
+  const int32_t b = static_cast<int32_t>(i - row32 * static_cast<uint32_t>(p.nb));
+  const int32_t col = b * kBlock + (lane & 7) * kUnit;
+  // K % 16 == 0: a unit is wholly inside or outside
+  bool in = i < p.blocks && col < p.K;
+  const bool lead = i < p.blocks && (lane & 7) == 0;
+  constexpr int kBatch = 8;
+  int32_t r[kBatch];  // the first destination rows, -1 for dropped slots
+  const int32_t* pos = p.pos + row * p.top_k;
+  if (p.pos != nullptr) {
+    bool any = p.top_k > kBatch;
 #pragma unroll
-    for (int o = kUnitsPerBlock / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float s = scale_from_amax_bits(m, p.pow2);
-    const uint4 q = u.cast(s);
-    const int32_t b = col / kBlock;
-    const bool lead = in && (lane % kUnitsPerBlock) == 0;
-    if (p.pos == nullptr) {
-      if (in) *reinterpret_cast<uint4*>(p.q + row * p.K + col) = q;
-      if (lead) p.scales[row * p.nb + b] = s;
-      continue;
+    for (int j = 0; j < kBatch; ++j) {
+      r[j] = j < p.top_k ? __ldg(pos + j) : -1;
+      if (r[j] >= p.out_rows) r[j] = -1;
+      any = any || r[j] >= 0;
     }
-    for (int32_t j = 0; j < p.top_k; ++j) {
-      const int64_t r = __ldg(p.pos + row * p.top_k + j);
-      if (r < 0 || r >= p.out_rows) continue;  // a dropped slot
-      if (in) *reinterpret_cast<uint4*>(p.q + r * p.K + col) = q;
-      if (lead) p.scales[r * p.nb + b] = s;
+    if (!any) in = false;
+  }
+  Unit<kF32> u;
+  if (in)
+    u.load(p.x + row * p.ld_bytes + static_cast<int64_t>(col) * (kF32 ? 4 : 2));
+  else
+    u.clear();
+  uint32_t m = u.amax_bits();
+#pragma unroll
+  for (int o = kUnitsPerBlock / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float s = scale_from_amax_bits(m, p.pow2);
+  const uint4 q = u.cast(s);
+  if (p.pos == nullptr) {
+    if (in) *reinterpret_cast<uint4*>(p.q + row * p.K + col) = q;
+    if (lead) p.scales[row * p.nb + b] = s;
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j)
+    if (r[j] >= 0) {
+      if (in) *reinterpret_cast<uint4*>(p.q + static_cast<int64_t>(r[j]) * p.K + col) = q;
+      if (lead) p.scales[static_cast<int64_t>(r[j]) * p.nb + b] = s;
     }
+  for (int32_t j = kBatch; j < p.top_k; ++j) {
+    const int64_t d = __ldg(pos + j);
+    if (d < 0 || d >= p.out_rows) continue;
+    if (in) *reinterpret_cast<uint4*>(p.q + d * p.K + col) = q;
+    if (lead) p.scales[d * p.nb + b] = s;
   }
 }
 
@@ -183,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) tiles_kernel(const TileParams p) {
       __stcs(reinterpret_cast<uint4*>(p.q + at + static_cast<int64_t>(32 * i) * p.K), u[i].cast(s));
 }
 
-gq_status launch_rows(const DeviceInfo& info, const void* x, bool f32, int64_t rows, int64_t K,
+gq_status launch_rows(const void* x, bool f32, int64_t rows, int64_t K,
                       int64_t ld, const int32_t* pos, int32_t top_k, int64_t out_rows, void* out,
                       float* scales, bool pow2, cudaStream_t stream) {
   RowParams p;
@@ -191,21 +213,22 @@ gq_status launch_rows(const DeviceInfo& info, const void* x, bool f32, int64_t r
   p.q = static_cast<uint8_t*>(out);
   p.scales = scales;
   p.pos = pos;
-  p.rows = rows;
   p.out_rows = out_rows;
   p.ld_bytes = ld * (f32 ? 4 : 2);
   p.K = static_cast<int32_t>(K);
   p.nb = static_cast<int32_t>((K + kBlock - 1) / kBlock);
-  p.segs = static_cast<int32_t>((K + 32 * kUnit - 1) / (32 * kUnit));
+  const int64_t blocks = rows * p.nb;
+  if (blocks > INT32_MAX)
+    return fail(GQ_ERR_UNSUPPORTED, "block_rows: %lld blocks of 128", static_cast<long long>(blocks));
+  p.blocks = static_cast<uint32_t>(blocks);
   p.top_k = top_k;
   p.pow2 = pow2;
-  const int64_t need = (rows * p.segs + kThreads / 32 - 1) / (kThreads / 32);
-  const int64_t most = static_cast<int64_t>(info.sm_count) * 8;
-  const int grid = static_cast<int>(need < most ? need : most);
+  constexpr int kPer = kThreads / 32 * 4;  // 128-blocks per thread block
+  const int64_t grid = (blocks + kPer - 1) / kPer;
   if (f32)
-    rows_kernel<true><<<grid, kThreads, 0, stream>>>(p);
+    rows_kernel<true><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
   else
-    rows_kernel<false><<<grid, kThreads, 0, stream>>>(p);
+    rows_kernel<false><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
   return check_cuda(cudaGetLastError(), "block_rows: launch");
 }
 

@@ -20,6 +20,7 @@ struct DeviceInfo {
   int rowwise_ctas_per_sm = 0;
   int mx_ctas_per_sm = 0;
   int rows_ctas_per_sm = 0;
+  int sort_cluster = 0;  // most blocks of the token sort
   int mm_pairs = 0;  // block pairs of grouped_mm that are resident at once
 };
 
@@ -103,7 +104,7 @@ gq_status launch(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa_t
 }  // namespace wgrad
 
 namespace block {
-gq_status launch_rows(const DeviceInfo& info, const void* x, bool f32, int64_t rows, int64_t K,
+gq_status launch_rows(const void* x, bool f32, int64_t rows, int64_t K,
                       int64_t ld, const int32_t* pos, int32_t top_k, int64_t out_rows, void* out,
                       float* scales, bool pow2, cudaStream_t stream);
 gq_status launch_tiles(const void* w, bool f32, int64_t E, int64_t N, int64_t K, void* out,
@@ -112,7 +113,7 @@ gq_status launch_tiles(const void* w, bool f32, int64_t E, int64_t N, int64_t K,
 
 namespace moe {
 gq_status setup(DeviceInfo& info);
-gq_status launch_sort(const void* ids, bool i64, int64_t tokens, int32_t top_k, int32_t experts,
+gq_status launch_sort(const DeviceInfo& info, const void* ids, bool i64, int64_t tokens, int32_t top_k, int32_t experts,
                       int32_t* offs, int32_t* pos, int32_t* token, cudaStream_t stream);
 gq_status launch_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_t ld_bytes,
                           const int32_t* pos, int32_t top_k, int64_t out_rows, void* out,
