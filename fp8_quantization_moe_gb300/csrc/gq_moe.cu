@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kSortWarpsMax * 32) sort_kernel(const SortPara
 // of a few threads.  (Whole rows per block, several chunks per thread, took
 // 116 us instead of 92 for the sum below: too few loads in flight.)
 constexpr int kThreads = 256;
-constexpr int kBatch = 8;  // slots whose loads are in flight together
+constexpr int kBatch = 8;  // slots whose loads are in flight together (4 where a token has no more)
 
 struct Spans {
   int32_t count, chunks, threads;  // spans per row, chunks of each, block size
@@ -258,10 +258,11 @@ struct DispatchParams {
 };
 
 // The sorted rows of a batch of a token's slots, -1 for the dropped ones.
+template <int kB>
 __device__ __forceinline__ void load_rows(const int32_t* pos, int32_t j0, int32_t top_k,
-                                          int64_t rows, int32_t (&r)[kBatch]) {
+                                          int64_t rows, int32_t (&r)[kB]) {
 #pragma unroll
-  for (int j = 0; j < kBatch; ++j) {
+  for (int j = 0; j < kB; ++j) {
     r[j] = j0 + j < top_k ? __ldg(pos + j0 + j) : -1;
     if (r[j] >= rows) r[j] = -1;
   }
@@ -339,7 +340,7 @@ struct CombineParams {
 
 // One block per token and span; the loads of kBatch slots are in flight
 // together, their sum runs in slot order.
-template <bool kF32>
+template <bool kF32, int kB>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p) {
   using C = Chunk<kF32>;
   const int64_t t = blockIdx.x;
@@ -348,19 +349,19 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p
   float acc[C::kN];
 #pragma unroll
   for (int i = 0; i < C::kN; ++i) acc[i] = 0.0f;
-  for (int32_t j0 = 0; j0 < p.top_k; j0 += kBatch) {
-    int32_t r[kBatch];
+  for (int32_t j0 = 0; j0 < p.top_k; j0 += kB) {
+    int32_t r[kB];
     load_rows(p.pos + t * p.top_k, j0, p.top_k, p.rows, r);
-    uint4 v[kBatch];
-    float w[kBatch];
+    uint4 v[kB];
+    float w[kB];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j)
+    for (int j = 0; j < kB; ++j)
       if (r[j] >= 0) {
         v[j] = __ldcs(p.y + static_cast<int64_t>(r[j]) * p.chunks + c);
         w[j] = p.weights != nullptr ? __ldg(p.weights + t * p.top_k + j0 + j) : 1.0f;
       }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j)
+    for (int j = 0; j < kB; ++j)
       if (r[j] >= 0) {
         float f[C::kN];
         C::unpack(v[j], f);
@@ -371,35 +372,35 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p
   p.out[t * p.chunks + c] = C::pack(acc);
 }
 
-// One block per token: a chunk of g is read once per kBatch slots, whose dot
+// One block per token: a chunk of g is read once per kB slots, whose dot
 // products are summed together: in a thread over its chunks, then over the
 // warp by halving (a lane keeps half of its values in each step, so eight
 // values take nine exchanges), then over the warps.
-template <bool kF32>
+template <bool kF32, int kB>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const CombineParams p) {
   using C = Chunk<kF32>;
-  __shared__ float part[kThreads / 32][kBatch];
+  __shared__ float part[kThreads / 32][kB];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int32_t j0 = 0; j0 < p.top_k; j0 += kBatch) {
-    int32_t r[kBatch];
+  for (int32_t j0 = 0; j0 < p.top_k; j0 += kB) {
+    int32_t r[kB];
     load_rows(p.pos + t * p.top_k, j0, p.top_k, p.rows, r);
-    float w[kBatch], dot[kBatch];
+    float w[kB], dot[kB];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
+    for (int j = 0; j < kB; ++j) {
       w[j] = r[j] >= 0 ? __ldg(p.weights + t * p.top_k + j0 + j) : 0.0f;
       dot[j] = 0.0f;
     }
     for (int32_t c = threadIdx.x; c < p.chunks; c += blockDim.x) {
       float g[C::kN];
-      uint4 v[kBatch];
+      uint4 v[kB];
       const uint4 gv = __ldg(p.g + t * p.chunks + c);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
+      for (int j = 0; j < kB; ++j)
         if (r[j] >= 0) v[j] = __ldcs(p.y + static_cast<int64_t>(r[j]) * p.chunks + c);
       C::unpack(gv, g);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
+      for (int j = 0; j < kB; ++j)
         if (r[j] >= 0) {
           float f[C::kN], d[C::kN];
           C::unpack(v[j], f);
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Combin
         }
     }
 #pragma unroll
-    for (int n = kBatch / 2, o = 16; n > 0; n >>= 1, o >>= 1) {
+    for (int n = kB / 2, o = 16; n > 0; n >>= 1, o >>= 1) {
       const bool up = (lane & o) != 0;
 #pragma unroll
       for (int i = 0; i < n; ++i) {
@@ -421,12 +422,12 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(const Combin
         dot[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
       }
     }
-    // lane l holds a partial sum of slot j0 + l / 4
-    dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 2);
-    dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 1);
-    if ((lane & 3) == 0) part[warp][lane >> 2] = dot[0];
+    // lane l holds a partial sum of slot j0 + l / (32 / kB)
+#pragma unroll
+    for (int o = 16 / kB; o > 0; o >>= 1) dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], o);
+    if (lane % (32 / kB) == 0) part[warp][lane / (32 / kB)] = dot[0];
     __syncthreads();
-    if (threadIdx.x < kBatch && j0 + static_cast<int32_t>(threadIdx.x) < p.top_k) {
+    if (threadIdx.x < kB && j0 + static_cast<int32_t>(threadIdx.x) < p.top_k) {
       float sum = 0.0f;
       for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) sum += part[i][threadIdx.x];
       p.dweights[t * p.top_k + j0 + threadIdx.x] = sum;
@@ -546,10 +547,10 @@ gq_status launch_combine(const void* y, bool f32, int64_t rows, int64_t H, const
   const Spans spans = spans_of(p.chunks);
   p.span = spans.chunks;
   const dim3 grid(static_cast<unsigned>(tokens), spans.count);
-  if (f32)
-    combine_kernel<true><<<grid, spans.threads, 0, stream>>>(p);
-  else
-    combine_kernel<false><<<grid, spans.threads, 0, stream>>>(p);
+  void (*kernel)(CombineParams) =
+      f32 ? (top_k <= 4 ? combine_kernel<true, 4> : combine_kernel<true, kBatch>)
+          : (top_k <= 4 ? combine_kernel<false, 4> : combine_kernel<false, kBatch>);
+  kernel<<<grid, spans.threads, 0, stream>>>(p);
   return check_cuda(cudaGetLastError(), "moe_combine: launch");
 }
 
@@ -568,10 +569,10 @@ gq_status launch_combine_backward(const void* g, const void* y, bool f32, int64_
   p.chunks = static_cast<int32_t>(H / (f32 ? 4 : 8));
   p.top_k = top_k;
   const int threads = p.chunks > 0 ? spans_of(p.chunks).threads : 32;
-  if (f32)
-    combine_backward_kernel<true><<<static_cast<unsigned>(tokens), threads, 0, stream>>>(p);
-  else
-    combine_backward_kernel<false><<<static_cast<unsigned>(tokens), threads, 0, stream>>>(p);
+  void (*kernel)(CombineParams) =
+      f32 ? (top_k <= 4 ? combine_backward_kernel<true, 4> : combine_backward_kernel<true, kBatch>)
+          : (top_k <= 4 ? combine_backward_kernel<false, 4> : combine_backward_kernel<false, kBatch>);
+  kernel<<<static_cast<unsigned>(tokens), threads, 0, stream>>>(p);
   return check_cuda(cudaGetLastError(), "moe_combine_backward: launch");
 }
 
