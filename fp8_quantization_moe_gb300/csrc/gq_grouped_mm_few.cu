@@ -3,17 +3,18 @@
 // a handful of rows, so HBM bounds it, 1 byte per weight.
 //
 // Here the weights are the MMA's M operand (128 output columns) and the rows
-// its N operand, 16 to 64 of them in steps of 16: an MMA costs as many cycles
-// as there are rows, and eight accumulators of 64 TMEM columns keep the
-// tensor cores, the epilogue and 128 KB of loads per SM in flight at once.
-// A lane of the epilogue owns an output column and needs every row's factor
-// 1/sa * 1/sb; with few rows those shared loads are cheap.
+// its N operand, up to 128 of them in steps of 16: an MMA costs as many cycles
+// as there are rows, and four accumulators keep the tensor cores, the epilogue
+// and 96 KB of weights per SM in flight at once.  A lane of the epilogue owns
+// an output column and needs every row's factor 1/sa * 1/sb; with few rows
+// those shared loads are cheap.
 //
 // One persistent block per SM; its warps:
-//   0-3   epilogue: TMEM lane quarter w (32 output columns);
-//   4     TMA loads (one lane);
-//   5     TMEM allocation and the MMAs (one lane);
-//   6     the factors, four 128-blocks at a time, into a ring.
+//   0-7   epilogue: TMEM lane quarter w % 4 (32 output columns), rows
+//         64 (w / 4) and on;
+//   8     TMA loads (one lane);
+//   9     TMEM allocation and the MMAs (one lane);
+//   10    the factors, four 128-blocks at a time, into a ring.
 // Every wait is bounded, as in the other kernels.
 #include <cuda_bf16.h>
 
@@ -25,17 +26,17 @@ namespace gmm {
 namespace {
 
 constexpr int kCols = 128;     // output columns of a tile (the MMA's M)
-constexpr int kTok = 64;       // rows of a tile, at most (the MMA's N)
-constexpr int kUnit = 16;
-constexpr int kStages = 8;
+constexpr int kTok = 128;      // rows of a tile, at most (the MMA's N)
+constexpr int kUnit = 16;      // rows of a tile come in units
+constexpr int kWarpTok = 64;   // rows of an epilogue warp, at most
 constexpr int kWBytes = kCols * kBlock;   // 16 KB
-constexpr int kABytes = kTok * kBlock;    // 8 KB
-constexpr int kStageBytes = kWBytes + kABytes;
-constexpr int kBufs = 512 / kTok;
-constexpr int kEpiWarps = 4;
-constexpr int kThreads = (kEpiWarps + 3) * 32;
 constexpr int kScaleKb = 4;    // 128-blocks per entry of the factor ring
 constexpr int kScaleRing = 4;
+constexpr int kStages = 6;
+constexpr int kStageBytes = kWBytes + kTok * kBlock;
+constexpr int kBufs = 512 / kTok;
+constexpr int kEpiWarps = 4 * (kTok / kWarpTok);
+constexpr int kThreads = (kEpiWarps + 3) * 32;
 
 struct Smem {
   uint8_t stage[kStages][kStageBytes];
@@ -64,13 +65,16 @@ struct Rings {
   bool hold = false;           // test hook: withhold the next release
 };
 
-// A tile with kU * 16 rows; false if a wait expired.
+// A tile of which this warp has kU * 16 rows from row j0 on (kU = 0: none, it
+// only keeps step); false if a wait expired.
 template <int kU>
 __device__ __forceinline__ bool tile_body(const Params& p, Smem& s, const Tile& t, Rings& x,
-                                          uint32_t tmem0, int q, int lane, uint64_t wait_ns) {
-  float acc[kU][kUnit];
+                                          uint32_t tmem0, int32_t j0, int q, int lane,
+                                          uint64_t wait_ns) {
+  constexpr int kN = kU > 0 ? kU : 1;
+  float acc[kN][kUnit];
 #pragma unroll
-  for (int a = 0; a < kU * kUnit; ++a) acc[a / kUnit][a % kUnit] = 0.0f;
+  for (int a = 0; a < kN * kUnit; ++a) acc[a / kUnit][a % kUnit] = 0.0f;
   const uint32_t done = smem_addr(s.done), fac_full = smem_addr(s.fac_full);
   const uint32_t factors = smem_addr(s.factor), acc_empty = smem_addr(s.acc_empty);
 #pragma unroll 1
@@ -79,50 +83,50 @@ __device__ __forceinline__ bool tile_body(const Params& p, Smem& s, const Tile& 
     if (e == 0 && !mbar_wait_warp(fac_full + x.r * 8, x.sc_use & 1, wait_ns, p.err)) return false;
     if (!mbar_wait_warp(done + x.st * 8, x.use & 1, wait_ns, p.err)) return false;
     tc_fence_after();
-    uint32_t h[kU][kUnit];
+    uint32_t h[kN][kUnit];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) tmem_ld_32x32b_x16(tmem0 + x.b * kTok + u * kUnit, h[u]);
-    uint4 f[kU][4];
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        f[u][v] = lds128_ordered(factors + ((x.r * kScaleKb + e) * kTok + u * kUnit + 4 * v) * 4);
+    for (int u = 0; u < kU; ++u) tmem_ld_32x32b_x16(tmem0 + x.b * kTok + j0 + u * kUnit, h[u]);
 #pragma unroll
     for (int u = 0; u < kU; ++u) tmem_ld_wait16(h[u]);
     tc_fence_before();
     __syncwarp();
-    const bool last = e == kScaleKb - 1 || kb == p.kbs - 1;
-    if (lane == 0) {
-      if (!x.hold) mbar_arrive_addr(acc_empty + x.b * 8);
-      if (last) mbar_arrive(&s.fac_empty[x.r]);
-    }
+    if (lane == 0 && !x.hold) mbar_arrive_addr(acc_empty + x.b * 8);
     x.hold = false;
+    const uint32_t fac = factors + ((x.r * kScaleKb + e) * kTok + j0) * 4;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      uint4 f[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) f[v] = lds128_ordered(fac + (u * kUnit + 4 * v) * 4);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float w[4] = {__uint_as_float(f[v].x), __uint_as_float(f[v].y),
+                            __uint_as_float(f[v].z), __uint_as_float(f[v].w)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[u][4 * v + j] = __fmaf_rn(__uint_as_float(h[u][4 * v + j]), w[j], acc[u][4 * v + j]);
+      }
+    }
     if (++x.b == kBufs) x.b = 0;
     if (++x.st == kStages) {
       x.st = 0;
       ++x.use;
     }
-    if (last && ++x.r == kScaleRing) {
-      x.r = 0;
-      ++x.sc_use;
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        acc[u][4 * v] = __fmaf_rn(__uint_as_float(h[u][4 * v]), __uint_as_float(f[u][v].x), acc[u][4 * v]);
-        acc[u][4 * v + 1] = __fmaf_rn(__uint_as_float(h[u][4 * v + 1]), __uint_as_float(f[u][v].y), acc[u][4 * v + 1]);
-        acc[u][4 * v + 2] = __fmaf_rn(__uint_as_float(h[u][4 * v + 2]), __uint_as_float(f[u][v].z), acc[u][4 * v + 2]);
-        acc[u][4 * v + 3] = __fmaf_rn(__uint_as_float(h[u][4 * v + 3]), __uint_as_float(f[u][v].w), acc[u][4 * v + 3]);
+    if (e == kScaleKb - 1 || kb == p.kbs - 1) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.fac_empty[x.r]);
+      if (++x.r == kScaleRing) {
+        x.r = 0;
+        ++x.sc_use;
       }
+    }
   }
   // Two rows at a time: neighbouring lanes swap one value each, so that even
   // lanes hold two columns of the first row and odd lanes of the second;
   // a store covers 64 bytes of both.
   const int32_t c = t.c0 + 32 * q + (lane & ~1);
   const int32_t odd = lane & 1;
-  uint16_t* dst = p.out + static_cast<int64_t>(t.m0 + odd) * p.outer + c;
+  uint16_t* dst = p.out + static_cast<int64_t>(t.m0 + j0 + odd) * p.outer + c;
 #pragma unroll
   for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -130,7 +134,7 @@ __device__ __forceinline__ bool tile_body(const Params& p, Smem& s, const Tile& 
       const float give = odd ? acc[u][j] : acc[u][j + 1];
       const float got = __shfl_xor_sync(0xffffffffu, give, 1);
       const uint32_t w = odd ? bf16x2_of(got, acc[u][j + 1]) : bf16x2_of(acc[u][j], got);
-      if (u * kUnit + j + odd < t.rows && c < p.outer)
+      if (j0 + u * kUnit + j + odd < t.rows && c < p.outer)
         *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(u * kUnit + j) * p.outer) = w;
     }
   return true;
@@ -320,17 +324,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // --------------------------------------------------------- epilogue --
-    const uint32_t tmem0 = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const int q = warp & 3;
+    const uint32_t tmem0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const int32_t j0 = (warp >> 2) * kWarpTok;
     Rings x;
     x.hold = p.skip_arrival && blockIdx.x == 0;
     bool ok = true;
     for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
       const Tile t = tile_of(p, s.tiles, i, kTok, kCols);
-      switch (units_of(t)) {
-        case 1: ok = tile_body<1>(p, s, t, x, tmem0, warp, lane, wait_ns); break;
-        case 2: ok = tile_body<2>(p, s, t, x, tmem0, warp, lane, wait_ns); break;
-        case 3: ok = tile_body<3>(p, s, t, x, tmem0, warp, lane, wait_ns); break;
-        default: ok = tile_body<4>(p, s, t, x, tmem0, warp, lane, wait_ns); break;
+      switch (min(units_of(t) - j0 / kUnit, kWarpTok / kUnit)) {
+        case 4: ok = tile_body<4>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 3: ok = tile_body<3>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 2: ok = tile_body<2>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 1: ok = tile_body<1>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        default: ok = tile_body<0>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
       }
     }
     tc_fence_before();
@@ -347,19 +354,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 gq_status setup_few(DeviceInfo& info) {
   (void)info;
-  const gq_status st = check_cuda(
-      cudaFuncSetAttribute(few_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kSmemBytes)),
-      "grouped_mm: shared memory size");
-  if (st != GQ_OK) return st;
-  return check_cuda(cudaFuncSetAttribute(few_kernel<true>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(kSmemBytes)),
-                    "grouped_mm: shared memory size");
+  for (const void* f : {reinterpret_cast<const void*>(few_kernel<false>),
+                        reinterpret_cast<const void*>(few_kernel<true>)}) {
+    const gq_status st = check_cuda(
+        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemBytes)),
+        "grouped_mm: shared memory size");
+    if (st != GQ_OK) return st;
+  }
+  return GQ_OK;
 }
 
-gq_status launch_few(const DeviceInfo& info, Params p, const void* qa, const void* qb, int32_t N,
-                     int32_t K, cudaStream_t stream) {
+gq_status launch_few(const DeviceInfo& info, Params p, const void* qa, const void* qb,
+                     int32_t N, int32_t K, cudaStream_t stream) {
   CUtensorMap amap, wmap;
   gq_status st = encode_tiled_2d(&amap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(qa),
                                  static_cast<uint64_t>(p.inner), static_cast<uint64_t>(p.M),
@@ -377,10 +384,8 @@ gq_status launch_few(const DeviceInfo& info, Params p, const void* qa, const voi
   if (most > INT32_MAX)
     return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: %lld tiles", static_cast<long long>(most));
   const unsigned grid = static_cast<unsigned>(most < info.sm_count ? most : info.sm_count);
-  if (p.transposed)
-    few_kernel<true><<<grid, kThreads, kSmemBytes, stream>>>(amap, wmap, p);
-  else
-    few_kernel<false><<<grid, kThreads, kSmemBytes, stream>>>(amap, wmap, p);
+  const auto kernel = p.transposed ? few_kernel<true> : few_kernel<false>;
+  kernel<<<grid, kThreads, kSmemBytes, stream>>>(amap, wmap, p);
   return check_cuda(cudaGetLastError(), "grouped_mm: launch");
 }
 

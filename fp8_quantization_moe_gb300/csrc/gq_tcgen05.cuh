@@ -1,12 +1,6 @@
-// gq_tcgen05.cuh -- inline-PTX wrappers of the tensor-core instructions in
-// block pairs (cta_group::2), of cluster addressing and barriers, and of the
-// register and shared-memory instructions around them.
-//
-// A pair is a cluster of two blocks.  TMEM is allocated and freed by one
-// warp of each of the two blocks together; one thread of the first block
-// issues the MMAs for both: each block's shared memory holds, at the same
-// offsets, its half of A (rows) and of B (rows), and each block's TMEM gets
-// its half of D's rows.
+// gq_tcgen05.cuh -- inline-PTX wrappers around the tensor-core instructions
+// (tcgen05, TMEM, their operands by TMA), of cluster addressing, and of
+// register and shared-memory instructions of the MoE-layer kernels.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -43,16 +37,7 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ void mbar_arrive_addr(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// Arrival on a barrier of any block of the cluster, ordering nothing but what
-// tcgen05 fences order: with cluster-scope release semantics it would wait
-// for every outstanding memory operation, 2000 cycles and more each.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
+// ------------------------------------------- barriers by shared address --
 // True in one lane of a converged warp.  The tensor-core and TMA instructions
 // take warp-uniform operands: under this predicate the compiler knows that a
 // single lane is active, under `lane == 0` it does not and issues each of
@@ -76,9 +61,6 @@ __device__ __forceinline__ bool mbar_test_addr(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// mbar_wait by a whole converged warp on a shared address; the result is the
-// same in every lane.  A suspended try_wait answers 75 cycles after the
-// arrival; polling took 180.
 __device__ __forceinline__ bool mbar_try_wait_addr(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -89,6 +71,21 @@ __device__ __forceinline__ bool mbar_try_wait_addr(uint32_t bar, uint32_t parity
       : "r"(bar), "r"(parity), "r"(kSuspendNs)
       : "memory");
   return ok != 0;
+}
+// mbar_wait by one lane, and by a whole converged warp with the same result in
+// every lane.  (A suspended try_wait answers 75 cycles after the arrival, a
+// loop of test_waits took 180.)
+__device__ __forceinline__ bool mbar_wait_addr(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                               unsigned* err) {
+  if (mbar_try_wait_addr(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait_addr(bar, parity)) {
+    if (global_timer_ns() - t0 > timeout_ns) {
+      atomicOr(err, kErrMbarTimeout);
+      return false;
+    }
+  }
+  return true;
 }
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
                                                unsigned* err) {
@@ -102,18 +99,12 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, ui
   }
   return true;
 }
+__device__ __forceinline__ void mbar_arrive_addr(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+}
 
 // ------------------------------------------------------------------- TMA --
-// Tiled loads into this block's shared memory whose bytes complete on a
-// barrier of either block of the pair (`bar`: a shared::cluster address).
-__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, int32_t x,
-                                                 int32_t y, uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
-      : "memory");
-}
+// Tiled 3-D load, as tma_load_2d.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y,
                                             int32_t z, uint64_t* bar, uint64_t policy) {
   asm volatile(
@@ -122,56 +113,14 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int32_t x,
-                                                 int32_t y, int32_t z, uint32_t bar,
-                                                 uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
-      : "memory");
-}
 
 // --------------------------------------------------------------- tcgen05 --
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                   smem_addr(dst)),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish_pair() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-               : "memory");
-}
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// The barrier at this offset in every block of `mask` gets one arrival once
-// all MMAs that this thread has issued so far are complete.
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_addr(bar)),
-      "h"(mask)
-      : "memory");
-}
-// D (TMEM) = A * B (+ D), e4m3 x e4m3 -> fp32, over the pair.
-template <bool kAccumulate>
-__device__ __forceinline__ void tc_mma_e4m3_pair(uint32_t d, uint64_t adesc, uint64_t bdesc,
-                                                 uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "n"(kAccumulate ? 1 : 0)
-      : "memory");
-}
-// The same for one block alone (cta_group::1).  A kernel uses one form only.
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                    smem_addr(dst)),
@@ -185,12 +134,15 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }
+// The barrier gets one arrival once every MMA this thread has issued is
+// complete.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_addr(bar))
       : "memory");
 }
+// D (TMEM) = A * B (+ D), e4m3 x e4m3 -> fp32.
 template <bool kAccumulate>
 __device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t adesc, uint64_t bdesc,
                                             uint32_t idesc) {
@@ -203,10 +155,10 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t adesc, uint64_t
 // Shared-memory matrix descriptor, 128-byte swizzle, atoms of 8 rows x 128
 // bytes one after the other: start address >> 4 (bits 0-13), stride between
 // atoms >> 4 (32-45), descriptor version 1 (46-47), swizzle mode 2 (61-63).
-// The leading offset (16-29, between atoms across the rows) is not used: an
-// operand is one atom wide.
-__device__ __forceinline__ uint64_t operand_desc_sw128(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (uint64_t(1024u >> 4) << 16) |
+// Leading offset >> 4 (16-29): for MN-major operands wider than 128 bytes the
+// distance from one 128-byte column of atoms to the next; else unused.
+__device__ __forceinline__ uint64_t operand_desc_sw128(uint32_t saddr, uint32_t leading = 1024u) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (uint64_t(leading >> 4) << 16) |
          (uint64_t(1024u >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 // 32 consecutive fp32 columns of this thread's TMEM lane.  (Measured per SM
@@ -267,6 +219,15 @@ __device__ __forceinline__ float rcp_approx(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+// (a0, a1) += (h0, h1) * f, each one IEEE fused multiply-add of fp32 values (h
+// as bits).
+__device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t h0, uint32_t h1, float f) {
+  asm("{\n\t.reg .b64 h, f, a;\n\t"
+      "mov.b64 h, {%2, %3};\n\tmov.b64 f, {%4, %4};\n\tmov.b64 a, {%0, %1};\n\t"
+      "fma.rn.f32x2 a, h, f, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "r"(h0), "r"(h1), "f"(f));
+}
 // Two fp32 values as bf16x2, the first in the lower half.
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   uint32_t d;
@@ -280,18 +241,6 @@ __device__ __forceinline__ float lds32_ordered(uint32_t addr) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
-}
-// 4-byte copy global -> shared.
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-// Four 8x8 b16 matrices stored transposed: lane l gives the address of row
-// l % 8 of matrix l / 8 (16 bytes); its register j holds, of matrix j, the
-// elements of stored rows 2 (l % 4) and + 1 at position l / 4.
-__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, const uint32_t (&r)[4]) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-               : "memory");
 }
 // 16-byte shared load ordered after the warp's preceding shared stores.
 __device__ __forceinline__ uint4 lds128_ordered(uint32_t addr) {
