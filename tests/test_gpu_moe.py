@@ -361,6 +361,10 @@ PRODUCTS = [
     (64, 2064, 4112, [10, 20, 40, 64]),
     (2600, 768, 640, [2600]),
     (260, 48, 2048, [130, 260]),
+    (520, 400, 528, [0, 3, 3, 303, 310, 311, 311, 312, 360, 400, 401, 402, 403, 404, 405, 520]),  # uneven
+    (1500, 528, 1296, [5, 10, 700, 700, 1500]),
+    (97, 1040, 656, [97]),
+    (96, 272, 144, [33, 96]),
 ]
 
 
@@ -368,6 +372,46 @@ PRODUCTS = [
 @pytest.mark.parametrize("transposed", [False, True])
 def test_grouped_mm(gq, M, N, K, offs, transposed):
     check_product(gq, M, N, K, offs, transposed)
+
+
+@pytest.mark.parametrize("rows", [20, 200])  # either kernel
+@pytest.mark.parametrize("transposed", [False, True])
+def test_grouped_mm_keeps_nan_in_its_group(gq, rows, transposed):
+    """NaN in one expert's weights, in one group's rows and behind the last
+    group reaches no other group's results (ragged N and K: tiles and
+    128-blocks reach past each expert's own)."""
+    N, K, E = 272, 400, 4
+    M = rows * E + 5
+    a, w = product_inputs(rows, M, N, K, E, transposed)
+    qa, sa = gq.block_rows(torch.from_numpy(a).to(DEV))
+    qb, sb = gq.block_tiles(torch.from_numpy(w).to(DEV))
+    o = torch.arange(rows, rows * E + 1, rows, dtype=torch.int32, device=DEV)
+    want = gq.grouped_mm(qa, sa, qb, sb, o, transpose_b=transposed)
+    qb.view(torch.uint8)[1] = 0x7F
+    sb[1] = float("nan")
+    qa.view(torch.uint8)[2 * rows:3 * rows] = 0xFF
+    sa[2 * rows:3 * rows] = float("nan")
+    qa.view(torch.uint8)[E * rows:] = 0x7F
+    sa[E * rows:] = float("nan")
+    got = gq.grouped_mm(qa, sa, qb, sb, o, transpose_b=transposed)
+    gq.check_device_error()
+    for g in range(E):
+        at = slice(g * rows, (g + 1) * rows)
+        if g in (1, 2):
+            assert got[at].isnan().all()
+        else:
+            assert torch.equal(got[at], want[at]), g
+
+
+def test_grouped_mm_is_deterministic(gq):
+    M, N, K, E = 3000, 1040, 1296, 7
+    a, w = product_inputs(9, M, N, K, E, False)
+    qa, sa = gq.block_rows(torch.from_numpy(a).to(DEV))
+    qb, sb = gq.block_tiles(torch.from_numpy(w).to(DEV))
+    o = torch.tensor([100, 100, 900, 1500, 1501, 2800, 3000], dtype=torch.int32, device=DEV)
+    first = gq.grouped_mm(qa, sa, qb, sb, o)
+    for _ in range(10):
+        assert torch.equal(gq.grouped_mm(qa, sa, qb, sb, o), first)
 
 
 @pytest.mark.parametrize("transposed", [False, True])
@@ -400,6 +444,54 @@ def test_grouped_mm_input_and_output_gradient_are_adjoint(gq):
     gq.check_device_error()
     assert fwd.float().abs().max() < 256 and bwd.float().abs().max() < 256  # integers below 2^8: exact in bf16
     assert (fwd.double() * G.double()).sum() == (bwd.double() * D.double()).sum()
+
+
+def test_past_2_31_elements(gq):
+    """Offsets past 31 bits: 65 x 8192 x 4096 weights (2.2e9), 300,000 rows of
+    8192 (2.5e9) into and out of expert order, checked on sampled rows."""
+    E, N, K = 65, 8192, 4096
+    w = torch.empty(E, N, K, dtype=torch.bfloat16, device=DEV).normal_()
+    qb, sb = gq.block_tiles(w)
+    for e in (0, E - 1):
+        blocks = w[e].float().view(N // 128, 128, K // 128, 128)
+        assert torch.equal(sb[e], 448.0 / blocks.abs().amax((1, 3)).clamp_min(1e-12)) or \
+            torch.allclose(sb[e], 448.0 / blocks.abs().amax((1, 3)), rtol=2 ** -22, atol=0)
+        err = (qb[e].float().view_as(blocks) / sb[e][:, None, :, None] - blocks).abs()
+        assert (err <= blocks.abs() * 2 ** -4 + 2.0 ** -10 / sb[e][:, None, :, None]).all()
+    del w
+    a = activations(3, 4, K, torch.bfloat16)
+    qa, sa = gq.block_rows(a)
+    offs = torch.zeros(E, dtype=torch.int32, device=DEV)
+    offs[E - 1] = 4
+    got = gq.grouped_mm(qa, sa, qb, sb, offs)
+    gq.check_device_error()
+    want, S, _ = product_plain(qa, sa, qb[E - 1:], sb[E - 1:], [4], False, 4, N)
+    assert (np.abs(f32(got) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -12 * S).all()
+    del qb
+
+    T, k, H = 150000, 2, 8192
+    ids = torch.from_numpy(rng(5).integers(0, 8, (T, k))).to(DEV)
+    order = gq.sort_tokens(ids, 8)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=DEV).normal_()
+    rows = gq.dispatch(x, order.pos)
+    q, s = gq.dispatch_block(x, order.pos)
+    plain_q, plain_s = gq.block_rows(x)
+    some = torch.from_numpy(rng(6).integers(0, T * k, 2000)).to(DEV)
+    some[:2] = torch.tensor([0, T * k - 1])
+    token = order.token[some].long()
+    assert torch.equal(rows[some], x[token])
+    assert torch.equal(q.view(torch.uint8)[some], plain_q.view(torch.uint8)[token])
+    assert torch.equal(s[some], plain_s[token])
+    w = torch.rand(T, k, device=DEV)
+    some = some // k
+    pos = order.pos[some].long()
+    out = gq.combine(rows, order.pos, w)[some].double()
+    want = (rows[pos].double() * w[some, :, None].double()).sum(1)
+    assert ((out - want).abs() <= 2 ** -7 * want.abs()).all()  # both rows are the token's own
+    dy, dw = gq.combine_backward(x, rows, order.pos, w)
+    assert torch.equal(dy[pos], (w[some, :, None] * x[some][:, None].float()).to(torch.bfloat16))
+    want = (x[some][:, None].double() * rows[pos].double()).sum(2)
+    assert ((dw[some] - want).abs() <= H * 2.0 ** -24 * want).all()  # sums of squares
 
 
 def test_other_stream_and_graph(gq):
