@@ -17,6 +17,16 @@
 // need every row's factor, and those loads alone -- shared memory returns 128
 // bytes a cycle -- would cost as much as the MMAs.
 //
+// What bounds it: shared memory, which takes 48 KB of operands per 128-block
+// and serves 48 KB to the MMAs, and the output's exchanges between lanes, at
+// 128 bytes a cycle: about 780 cycles against 512 of MMAs.  A turn measures
+// 850.  16,640 rows of 16 groups, K 4096 to N 8192: 460 us, 2.43 PFLOP/s;
+// transposed, 32,768 rows of 64 groups, N 2048 to K 4096: 265 us, 2.07 PFLOP/s
+// (in a long run the power limit lowers the clock: the first takes 500 us and
+// more).  Blocks in pairs that share the weights' loads (cta_group::2) relieve
+// shared memory, but release accumulators across blocks and pad the groups to
+// 256 rows: 505 and 316 us.
+//
 // One persistent block per SM; its warps:
 //   0-7   epilogue: lane quarter w % 4 (32 rows), column half w / 4;
 //   8     TMA loads (one lane);
@@ -45,6 +55,8 @@ constexpr int kBufs = 2;          // accumulators in TMEM
 constexpr uint32_t kTmemCols = kBufs * kCols;
 constexpr int kEpiWarps = 8;      // two per TMEM lane quarter
 constexpr int kThreads = (kEpiWarps + 4) * 32;
+constexpr int kEpiRegs = 232;     // registers per thread after the split:
+constexpr int kOtherRegs = 40;    // what the block was launched with, no more
 constexpr int kChunk = 32;        // columns per step of the epilogue
 constexpr int kChunks = kCols / 2 / kChunk;
 constexpr int kScaleKb = 4;       // 128-blocks per entry of the factor ring
@@ -53,8 +65,9 @@ static_assert(kTmemCols == 512 && kChunks == 4, "two accumulators fill the TMEM"
 
 struct Smem {
   uint8_t stage[kStages][kStageBytes];  // 1024-byte aligned (swizzle atoms)
-  alignas(16) uint8_t rows[kEpiWarps][32 * kChunk * 2];
   float factor[kScaleRing][kScaleKb][2][kRows];  // of the tile's two column halves
+  int4 tile[kScaleRing];         // the entry's tile: first row, rows, first column
+  uint32_t cols[kStages];        // output columns of the stage's tile
   TileTable tiles;
   uint64_t full[kStages];         // the stage's loads
   uint64_t done[kStages];         // its MMAs are complete: the stage is free, the accumulator full
@@ -75,11 +88,22 @@ __device__ __forceinline__ int32_t boxes_of(const Tile& t) {
 // acc += h * f, h the bits of fp32 values, two at a time.  A packed multiply-
 // add occupies the FMA pipe for as long as two scalar ones (measured 2 cycles)
 // but issues once: with scalar ones the warp that issues the MMAs waits for
-// its turn (500 us instead of 488 for the case below).
+// its turn (500 us instead of 488 for 16,640 rows).
 __device__ __forceinline__ void scale_add(float (&acc)[kChunk], const uint32_t (&h)[kChunk],
                                           float f) {
 #pragma unroll
   for (int e = 0; e < kChunk; e += 2) fma2(acc[e], acc[e + 1], h[e], h[e + 1], f);
+}
+
+// Exchanges b of a lane without bit kD with a of its partner with that bit.
+template <int kD>
+__device__ __forceinline__ void swap_with(uint32_t& a, uint32_t& b, int lane) {
+  const bool up = (lane & kD) != 0;
+  const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, kD);
+  if (up)
+    a = got;
+  else
+    b = got;
 }
 
 template <bool kT>
@@ -124,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int32_t tiles = s.tiles.first[p.E] * p.tiles_c;  // below 2^31: the host checks
 
   if (warp >= kEpiWarps) {
-    setmaxnreg_dec<40>();
+    setmaxnreg_dec<kOtherRegs>();
     if (warp == kEpiWarps) {
       // ---------------------------------------------------------- loads --
       const uint64_t pol = policy_evict_normal();
@@ -132,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t st = 0, use = 0;  // stage, its use
       bool ok = true;
       for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-        const Tile t = tile_of(p, s.tiles, i, kRows, kCols);
+        const Tile t = tile_of(p, s.tiles, i, kRows, kCols, lane);
         const int32_t boxes = boxes_of(t);
         const uint32_t bytes = 2 * kWHalf + static_cast<uint32_t>(boxes) * (kBoxRows * kBlock);
         for (int32_t k = 0; k < p.inner; k += kBlock) {
@@ -141,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             uint8_t* base = s.stage[st];
             uint64_t* bar = &s.full[st];
+            s.cols[st] = min(kCols, p.outer - t.c0);
             mbar_arrive_expect_tx(bar, bytes);
             for (int h = 0; h < 2; ++h) {
               const int32_t c = t.c0 + h * kCols / 2;
@@ -175,11 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t st = 0, st_use = 0, b = 0, use = 0;  // stage and accumulator, their uses
         bool ok = true, issued = false;
         for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-          const Tile t = tile_of(p, s.tiles, i, kRows, kCols);
-          // the tile's columns: a multiple of 16, as the MMA's N has to be
-          const uint32_t n = min(kCols, p.outer - t.c0);
-          // D fp32, e4m3 x e4m3, B MN-major if transposed, N = n, M = 128
-          const uint32_t idesc = (1u << 4) | (kT ? 1u << 16 : 0u) | ((n >> 3) << 17) | (8u << 24);
+          uint32_t idesc = 0;
           for (int32_t left = p.inner; left > 0; left -= kBlock) {
             // rows: K-major; weights: K-major rows of 128 bytes, or MN-major
             // (32 contraction rows = 4 KB, the column halves kWHalf apart)
@@ -189,6 +210,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_addr(full + st * 8, st_use & 1, wait_ns, p.err) &&
                  mbar_wait_addr(acc_empty + b * 8, (use & 1) ^ 1u, wait_ns, p.err);
             if (!ok) break;
+            if (left == p.inner) {
+              // the tile's columns: a multiple of 16, as the MMA's N has to be
+              const uint32_t n = s.cols[st];
+              // D fp32, e4m3 x e4m3, B MN-major if transposed, N = n, M = 128
+              idesc = (1u << 4) | (kT ? 1u << 16 : 0u) | ((n >> 3) << 17) | (8u << 24);
+            }
             tc_fence_after();
             tc_mma_e4m3<false>(d, ad, wd, idesc);
 #pragma unroll
@@ -222,11 +249,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows that exist are read (clamped to one row, the loads of all blocks
       // would queue up at a single L2 line).
       const int32_t first = (warp - kEpiWarps - 2) * 64 + lane;
-      float v[2][kScaleKb], w[2][kScaleKb];
+      float v[2][kScaleKb] = {}, w[2][kScaleKb];
       int32_t i = blockIdx.x, kb = 0;
       Tile t = {};
       auto load = [&]() {  // the entry (tile i, 128-blocks kb ..)
-        if (kb == 0) t = tile_of(p, s.tiles, i, kRows, kCols);
+        if (kb == 0) t = tile_of(p, s.tiles, i, kRows, kCols, lane);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float* sb = p.sb + t.g * p.sb_expert +
@@ -268,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s.factor[r][u][1][first + 32 * j] = __fmul_rn(ra, w1);
           }
         }
+        if (threadIdx.x == (kEpiWarps + 2) * 32) s.tile[r] = make_int4(t.m0, t.rows, t.c0, 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.fac_full[r]);
         if (++r == kScaleRing) {
@@ -287,17 +315,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Lane l of warp (q, hc) owns row 32 q + l of the tile and its columns
     // [128 hc, 128 hc + 128), one scale block of the weights.  A turn (one
     // 128-block) has to be short against the MMAs, and shared memory, which
-    // carries their operands, answers slowly: a turn's factor is read, and its
-    // MMAs' completion probed, during the turn before.
-    setmaxnreg_inc<232>();
+    // carries their operands, answers slowly: a turn's factor is read, its
+    // MMAs' completion probed and its first 32 columns loaded during the turn
+    // before, and every load of TMEM runs under the multiply-adds of the
+    // columns before it.  (All of a turn's loads at its start, to release the
+    // accumulator sooner: 474 us instead of 463.)  The tile comes with its
+    // factors: looking it up here took 1100 cycles, in which nothing moved.
+    setmaxnreg_inc<kEpiRegs>();
     const int q = warp & 3, hc = warp >> 2;
-    const uint32_t stage_rows = smem_addr(s.rows[warp]);
-    const uint32_t my_row = stage_rows + static_cast<uint32_t>(lane * kChunk * 2);
-    const uint32_t my_swz = static_cast<uint32_t>((lane >> 1) & 3);
     const uint32_t done = smem_addr(s.done), fac_full = smem_addr(s.fac_full);
     const uint32_t acc_empty = smem_addr(s.acc_empty);
     const uint32_t tmem0 = tmem + (static_cast<uint32_t>(32 * q) << 16) + hc * (kCols / 2);
     const uint32_t fac = smem_addr(&s.factor[0][0][hc][32 * q + lane]);
+    const uint32_t tile = smem_addr(s.tile);
     constexpr uint32_t kFacKb = 2 * kRows * 4, kFacEntry = kScaleKb * kFacKb;
     uint32_t b = 0;               // accumulator
     uint32_t st = 0, use = 0;     // the stage whose MMAs filled it, its use
@@ -306,36 +336,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool hold = p.skip_arrival && blockIdx.x == 0;  // withhold the next release
     bool ok = true;
     for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-      const Tile t = tile_of(p, s.tiles, i, kRows, kCols);
-      const int32_t rows = t.rows - 32 * q;  // of this warp, if positive
-      const int32_t c = t.c0 + hc * (kCols / 2);
+      ok = mbar_wait_warp(fac_full + r * 8, fac_use & 1, wait_ns, p.err);
+      if (!ok) break;
+      const uint4 ti = lds128_ordered(tile + r * 16);
+      float f = lds32_ordered(fac + r * kFacEntry);
+      const int32_t row0 = static_cast<int32_t>(ti.x) + 32 * q;
+      const int32_t rows = static_cast<int32_t>(ti.y) - 32 * q;  // of this warp, if positive
+      const int32_t c = static_cast<int32_t>(ti.z) + hc * (kCols / 2);
       const bool mine = rows > 0 && c < p.outer;
       float acc[kChunks][kChunk];
 #pragma unroll
       for (int a = 0; a < kChunks * kChunk; ++a) acc[a / kChunk][a % kChunk] = 0.0f;
-      ok = mbar_wait_warp(fac_full + r * 8, fac_use & 1, wait_ns, p.err);
-      if (!ok) break;
-      float f = lds32_ordered(fac + r * kFacEntry);
       uint32_t e = 0;  // the 128-block's place in its entry
+      uint32_t h0[kChunk], h1[kChunk];
+      if (!__all_sync(0xffffffffu, ready)) {
+        ok = mbar_wait_warp(done + st * 8, use & 1, wait_ns, p.err);
+        if (!ok) break;
+      }
+      tc_fence_after();
+      if (mine) {
+        tmem_ld_32x32b_x32(tmem0 + b * kCols, h0);
+        tmem_ld_wait32(h0);
+      }
 #pragma unroll 1
       for (int32_t left = p.kbs; left > 0; --left) {
-        if (!__all_sync(0xffffffffu, ready)) {
-          ok = mbar_wait_warp(done + st * 8, use & 1, wait_ns, p.err);
-          if (!ok) break;
-        }
-        tc_fence_after();
         const uint32_t tacc = tmem0 + b * kCols;
-        uint32_t h0[kChunk], h1[kChunk];
         if (mine) {
-          tmem_ld_32x32b_x32(tacc, h0);
           tmem_ld_32x32b_x32(tacc + kChunk, h1);
-          tmem_ld_wait32(h0);
-          tmem_ld_wait32(h1);
           scale_add(acc[0], h0, f);
+          tmem_ld_wait32(h1);
           tmem_ld_32x32b_x32(tacc + 2 * kChunk, h0);
           scale_add(acc[1], h1, f);
-          tmem_ld_32x32b_x32(tacc + 3 * kChunk, h1);
           tmem_ld_wait32(h0);
+          tmem_ld_32x32b_x32(tacc + 3 * kChunk, h1);
+          scale_add(acc[2], h0, f);
           tmem_ld_wait32(h1);
         }
         tc_fence_before();
@@ -363,40 +397,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float next = lds32_ordered(fac + r * kFacEntry + e * kFacKb);
-        if (mine) {
-          scale_add(acc[2], h0, f);
+        if (left > 1) {
+          if (!__all_sync(0xffffffffu, ready)) {
+            ok = mbar_wait_warp(done + st * 8, use & 1, wait_ns, p.err);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          if (mine) {
+            tmem_ld_32x32b_x32(tmem0 + b * kCols, h0);
+            scale_add(acc[3], h1, f);
+            tmem_ld_wait32(h0);
+          }
+        } else if (mine) {
           scale_add(acc[3], h1, f);
         }
         f = next;
       }
       if (!ok) break;
       if (!mine) continue;
-      // 32 columns at a time: each lane writes its row's 64-byte run into the
-      // warp's staging rows (16-byte parts XOR-swizzled by (row / 2) % 4: no
-      // bank conflicts on either side), then eight rows per store
+      // 32 columns at a time: four lanes exchange their rows' 16-byte parts by
+      // shuffles, so that a store covers 64-byte runs of eight rows.  (Staged in
+      // shared memory: 456 us instead of 452; sent from there by TMA, with a
+      // stage less for the operands, 480; without an exchange 495; exchanged by
+      // pairs of lanes 472, by eight lanes 465 against 465 here.)
       const int part = lane & 3;
-      uint16_t* orow = p.out + static_cast<int64_t>(t.m0 + 32 * q) * p.outer + c + part * 8;
+      uint16_t* orow = p.out + static_cast<int64_t>(row0 + (lane & ~3)) * p.outer + c + part * 8;
 #pragma unroll
       for (int ch = 0; ch < kChunks; ++ch) {
-        if (c + ch * kChunk >= p.outer) break;
+        uint32_t x[4][4];  // [part][word] of this lane's row
 #pragma unroll
         for (int w = 0; w < 4; ++w)
-          sts128(my_row + ((static_cast<uint32_t>(w) ^ my_swz) << 4),
-                 make_uint4(bf16x2_of(acc[ch][8 * w], acc[ch][8 * w + 1]),
-                            bf16x2_of(acc[ch][8 * w + 2], acc[ch][8 * w + 3]),
-                            bf16x2_of(acc[ch][8 * w + 4], acc[ch][8 * w + 5]),
-                            bf16x2_of(acc[ch][8 * w + 6], acc[ch][8 * w + 7])));
-        __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            x[w][j] = bf16x2_of(acc[ch][8 * w + 2 * j], acc[ch][8 * w + 2 * j + 1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          swap_with<1>(x[0][j], x[1][j], lane);
+          swap_with<1>(x[2][j], x[3][j], lane);
+          swap_with<2>(x[0][j], x[2][j], lane);
+          swap_with<2>(x[1][j], x[3][j], lane);
+        }
+        // x[k] is part lane & 3 of row (lane & ~3) + k
         const bool c_ok = c + ch * kChunk + part * 8 < p.outer;  // outer % 16 == 0
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int m = 8 * k + (lane >> 2);
-          const uint4 v =
-              lds128_ordered(stage_rows + m * (kChunk * 2) + ((part ^ ((m >> 1) & 3)) << 4));
-          if (m < rows && c_ok)
-            *reinterpret_cast<uint4*>(orow + static_cast<int64_t>(m) * p.outer + ch * kChunk) = v;
-        }
-        __syncwarp();
+        for (int k = 0; k < 4; ++k)
+          if ((lane & ~3) + k < rows && c_ok)
+            *reinterpret_cast<uint4*>(orow + static_cast<int64_t>(k) * p.outer + ch * kChunk) =
+                make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
       }
     }
     tc_fence_before();
@@ -420,11 +467,17 @@ constexpr int kFewRows = 48;
 gq_status setup(DeviceInfo& info) {
   for (const void* f : {reinterpret_cast<const void*>(product_kernel<false>),
                         reinterpret_cast<const void*>(product_kernel<true>)}) {
-    const gq_status st = check_cuda(
+    gq_status st = check_cuda(
         cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes)),
         "grouped_mm: shared memory size");
     if (st != GQ_OK) return st;
+    // a split above the launch's registers would wait for ever
+    cudaFuncAttributes a;
+    st = check_cuda(cudaFuncGetAttributes(&a, f), "grouped_mm: registers");
+    if (st != GQ_OK) return st;
+    if (a.numRegs * kThreads < 32 * (kEpiWarps * kEpiRegs + (kThreads / 32 - kEpiWarps) * kOtherRegs))
+      return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: built with %d registers per thread", a.numRegs);
   }
   return setup_few(info);
 }

@@ -62,22 +62,22 @@ struct Tile {
   int32_t g, c0, m0, rows;  // group, first column, first row, rows of the group from there
 };
 
+// Tile i, found by a whole warp: the last group whose first tile is at or
+// before i, in one vote over blocks of 32 groups and one within a block.
 __device__ __forceinline__ Tile tile_of(const Params& p, const TileTable& s, int32_t i,
-                                        int32_t rows, int32_t cols) {
-  // the last group whose first tile is at or before i
-  int32_t lo = 0, hi = p.E;
-  while (hi - lo > 1) {
-    const int32_t mid = (lo + hi) >> 1;
-    if (s.first[mid] * p.tiles_c <= i) lo = mid; else hi = mid;
-  }
+                                        int32_t rows, int32_t cols, int lane) {
+  int32_t g = 0;
+  if (p.E > 32)
+    g = 32 * __popc(__ballot_sync(0xffffffffu, s.first[min(32 * lane + 32, p.E)] * p.tiles_c <= i));
+  g += __popc(__ballot_sync(0xffffffffu, s.first[min(g + lane + 1, p.E)] * p.tiles_c <= i));
+  const int32_t first = s.first[g];
+  const uint32_t row_tiles = s.first[g + 1] - first, r = i - first * p.tiles_c;
+  const uint32_t c = r / row_tiles;
   Tile t;
-  t.g = lo;
-  const int32_t tt = s.first[lo + 1] - s.first[lo];
-  const int32_t r = i - s.first[lo] * p.tiles_c;
-  const int32_t start = lo > 0 ? s.ends[lo - 1] : 0;
-  t.c0 = (r / tt) * cols;
-  t.m0 = start + (r % tt) * rows;
-  t.rows = s.ends[lo] - t.m0;
+  t.g = g;
+  t.c0 = c * cols;
+  t.m0 = (g > 0 ? s.ends[g - 1] : 0) + (r - c * row_tiles) * rows;
+  t.rows = s.ends[g] - t.m0;
   return t;
 }
 
