@@ -9,7 +9,12 @@
 //                  their two passes, one HBM read; a unit far longer than
 //                  the ring is cut into parts that several blocks take;
 //   gq_mxfp8.cu    a plain coalesced stream;
-//   gq_wgrad.cu    a tcgen05 grouped GEMM.
+//   gq_wgrad.cu    a tcgen05 grouped GEMM;
+//   gq_block.cu    plain streams with the block held in registers;
+//   gq_moe.cu      one cluster for the sort, a block per token and span of its
+//                  row for the rest;
+//   gq_grouped_mm.cu, gq_grouped_mm_few.cu   tcgen05 grouped products, one
+//                  persistent block per SM.
 //
 // Every wait on another warp or block is bounded by %globaltimer: on expiry
 // the waiter records a bit in the per-device error word and returns false,

@@ -21,7 +21,6 @@ struct DeviceInfo {
   int mx_ctas_per_sm = 0;
   int rows_ctas_per_sm = 0;
   int sort_cluster = 0;  // most blocks of the token sort
-  int mm_pairs = 0;  // block pairs of grouped_mm that are resident at once
 };
 
 // Launch-time knobs (test hooks).

@@ -34,7 +34,8 @@ namespace moe {
 //
 // Bound by latency (65,536 slots are half a megabyte): a warp keeps up to
 // kSortHold ids per lane in registers, all loaded at once, for both passes;
-// longer segments are read twice, in batches of that size.  A segment of 256
+// longer segments are read twice, in batches of that size.  65,536 slots of
+// 64 experts in 16 blocks: 7.9 us, 8 slots 3.1 us.  A segment of 256
 // slots read 32 at a time in both passes took 12.6 us for 65,536 slots in
 // 8 blocks.
 constexpr int kSortHold = 8;

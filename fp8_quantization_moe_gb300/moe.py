@@ -88,10 +88,13 @@ _FLOAT = (torch.bfloat16, torch.float32)
 
 def _pitch(x: torch.Tensor, what: str) -> int:
     """Elements from one row of x to the next; the rows themselves are dense."""
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    rows, cols = x.shape
+    pitch, step = x.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{what} must have dense rows")
-    pitch = x.stride(0) if x.shape[0] > 1 else x.shape[1]
-    if pitch < x.shape[1]:
+    if rows <= 1:
+        return cols
+    if pitch < cols:
         raise ValueError(f"{what} must have rows that do not overlap")
     return pitch
 
@@ -149,24 +152,29 @@ def _block_rows(name, x, pos, out, scales, pow2_scales, stream):
     _need(x, name + ": x", 2, _FLOAT, contiguous=False)
     T, K = x.shape
     dev = x.device
+    index = dev.index
     pitch = _pitch(x, name + ": x")
-    k, rows = 1, T
+    k, rows, to = 1, T, None
     if pos is not None:
-        _need(pos, name + ": pos", 2, _I32, dev.index)
-        if pos.shape[0] != T:
+        _need(pos, name + ": pos", 2, _I32, index)
+        tokens, k = pos.shape
+        if tokens != T:
             raise ValueError(f"{name}: pos must have a row for each row of x")
-        k = pos.shape[1]
-        rows = T * k if out is None else len(out)
+        rows = T * k
+        to = pos.data_ptr()
+        if out is not None:
+            _need(out, name + ": out", 2, _FP8, index)
+            rows = out.shape[0]
     if out is None:
         out = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=dev)
     else:
-        _need(out, name + ": out", 2, _FP8, dev.index, (rows, K))
+        _need(out, name + ": out", 2, _FP8, index, (rows, K))
     if scales is None:
         scales = torch.empty((rows, _blocks(K)), dtype=torch.float32, device=dev)
     else:
-        _need(scales, name + ": scales", 2, _F32, dev.index, (rows, _blocks(K)))
-    _call("gq_fp8_block_rows", dev.index, stream, lib().gq_fp8_block_rows, x.data_ptr(),
-          _DTYPES[x.dtype], T, K, pitch, None if pos is None else pos.data_ptr(), k, rows,
+        _need(scales, name + ": scales", 2, _F32, index, (rows, _blocks(K)))
+    _call("gq_fp8_block_rows", index, stream, lib().gq_fp8_block_rows, x.data_ptr(),
+          _DTYPES[x.dtype], T, K, pitch, to, k, rows,
           out.data_ptr(), scales.data_ptr(), GQ_SCALE_POW2 if pow2_scales else 0)
     return out, scales
 

@@ -420,7 +420,8 @@ gq_status gq_fp8_block_tiles(const void* w, int dtype, int64_t E, int64_t N, int
  * for every row m of group g: the layer's forward product and, with the same
  * stored weights, its grad_input.  The e4m3 products of one 128-block of the
  * contraction are summed in fp32 on the tensor cores (order unspecified),
- * that sum is multiplied by fp32(fp32(1/sa) * fp32(1/sb)) and added in fp32.
+ * that sum is multiplied by the factor 1/sa * 1/sb, an fp32 product of two
+ * reciprocals that are within one unit in the last place, and added in fp32.
  *
  *   qa       e4m3 [M, K] (transpose_b: [M, N]), 16-byte aligned.  (input)
  *   sa       fp32 [M, ceil(columns of qa / 128)].                 (input)
@@ -496,8 +497,9 @@ int gq_version(void);
  *          amax-complete signal of the (first row band, first group) unit
  *          (waiters: the warps that would cast it), or, in a call that
  *          splits units, the count of the first split unit's first part
- *          (waiters: the other parts); grouped_wgrad: the release of thread
- *          block 0's first TMEM accumulator (waiter: the block's MMA warp);
+ *          (waiters: the other parts); grouped_wgrad and grouped_mm: the
+ *          release of thread block 0's first TMEM accumulator (waiter: the
+ *          block's MMA warp);
  *   bit 1  rowwise_t never splits units across blocks (results are the
  *          same; the path a call takes when it does not find all of its
  *          blocks resident).
