@@ -17,15 +17,17 @@
 // need every row's factor, and those loads alone -- shared memory returns 128
 // bytes a cycle -- would cost as much as the MMAs.
 //
-// What bounds it: shared memory, which takes 48 KB of operands per 128-block
-// and serves 48 KB to the MMAs, and the output's exchanges between lanes, at
-// 128 bytes a cycle: about 780 cycles against 512 of MMAs.  A turn measures
-// 850.  16,640 rows of 16 groups, K 4096 to N 8192: 460 us, 2.43 PFLOP/s;
-// transposed, 32,768 rows of 64 groups, N 2048 to K 4096: 265 us, 2.07 PFLOP/s
-// (in a long run the power limit lowers the clock: the first takes 500 us and
-// more).  Blocks in pairs that share the weights' loads (cta_group::2) relieve
-// shared memory, but release accumulators across blocks and pad the groups to
-// 256 rows: 505 and 316 us.
+// What bounds it: with two accumulators, all of TMEM, the MMAs wait for the
+// epilogue.  A 128-block takes 860 cycles, 512 of them MMAs; without the
+// epilogue's multiply-adds (half of the FMA pipe's time at the tensor cores'
+// full rate) it would take 720, without the stores 780: a tile's 64 KB leave
+// the SM at 32 bytes a cycle, and for those 2000 cycles the MMAs run ahead by
+// two 128-blocks at most.  16,640 rows of 16 groups, K 4096 to N 8192: 460 us,
+// 2.43 PFLOP/s; transposed, 32,768 rows of 64 groups, N 2048 to K 4096: 265 us,
+// 2.07 PFLOP/s (in a long run the power limit lowers the clock: the first takes
+// 515 to 540 us).  Blocks in pairs that share the weights' loads
+// (cta_group::2) release accumulators across blocks and pad the groups to 256
+// rows: 505 and 316 us.
 //
 // One persistent block per SM; its warps:
 //   0-7   epilogue: lane quarter w % 4 (32 rows), column half w / 4;
@@ -458,8 +460,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Up to this many rows per group on average the kernel for few rows is ahead,
 // whose narrower tiles spread the weights more evenly: in us, few / this,
-// 64 experts of 2048 x 2048: 44 / 50 at 32 rows each, 51 / 53 at 64, 107 / 72
-// at 160; 16 of 4096 x 4096: 47 / 48, 52 / 50, 93 / 71.
+// 64 experts of 2048 x 2048: 43 / 50 at 32 rows each, 45 / 51 at 48, 54 / 54 at
+// 96; 16 of 4096 x 4096: 45 / 47 at 16, 50 / 49 at 48, 54 / 51 at 96; 8 of
+// 8192 x 2048: 25 / 27 at 32, 28 / 28 at 48, 32 / 29 at 96.
 constexpr int kFewRows = 48;
 
 }  // namespace
