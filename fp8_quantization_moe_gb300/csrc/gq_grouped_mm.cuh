@@ -38,24 +38,52 @@ struct TileTable {
   int32_t first[kMaxGroups + 1];  // row tiles before each group
 };
 
-// Fills the table (one warp).
+// Fills the table (one warp, four groups per lane at a time): ends are the
+// running maximum of the offsets, clamped to the rows, as in the other calls.
+// No load of a block can start before it, so its length counts: with 32 groups
+// at a time, 64 experts cost 0.7 us more.
 __device__ __forceinline__ void build_tiles(const Params& p, int32_t rows, TileTable& s, int lane) {
-  build_ends(p.offs, 0, p.E, p.M, s.ends, lane);
-  __syncwarp();
-  int32_t carry = 0;
-  for (int base = 0; base < p.E; base += 32) {
-    const int g = base + lane;
-    int32_t v = 0;
-    if (g < p.E) v = (s.ends[g] - (g > 0 ? s.ends[g - 1] : 0) + rows - 1) / rows;
+  constexpr int kPer = 4;
+  int32_t high = 0, tiles = 0;  // the last end so far, unclamped, and the tiles before it
+  if (lane == 0) s.first[0] = 0;
+  for (int base = 0; base < p.E; base += 32 * kPer) {
+    const int g = base + lane * kPer;
+    int32_t v[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v[j] = g + j < p.E ? __ldg(p.offs + g + j) : 0;
+#pragma unroll
+    for (int j = 1; j < kPer; ++j) v[j] = max(v[j], v[j - 1]);
+    int32_t m = v[kPer - 1];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
-      if (lane >= d) v += o;
+      const int32_t o = __shfl_up_sync(0xffffffffu, m, d);
+      if (lane >= d) m = max(m, o);
     }
-    if (g < p.E) s.first[g + 1] = carry + v;
-    carry += __shfl_sync(0xffffffffu, v, 31);
+    int32_t prev = __shfl_up_sync(0xffffffffu, m, 1);
+    prev = lane > 0 ? max(prev, high) : high;
+    high = max(high, __shfl_sync(0xffffffffu, m, 31));
+    int32_t n[kPer], start = min(prev, p.M);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      v[j] = min(max(v[j], prev), p.M);
+      n[j] = (v[j] - start + rows - 1) / rows + (j > 0 ? n[j - 1] : 0);
+      start = v[j];
+    }
+    int32_t sum = n[kPer - 1];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    const int32_t first = tiles + sum - n[kPer - 1];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (g + j < p.E) {
+        s.ends[g + j] = v[j];
+        s.first[g + j + 1] = first + n[j];
+      }
+    tiles += __shfl_sync(0xffffffffu, sum, 31);
   }
-  if (lane == 0) s.first[0] = 0;
 }
 
 struct Tile {

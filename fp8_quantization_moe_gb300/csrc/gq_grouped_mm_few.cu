@@ -1,8 +1,8 @@
 // gq_grouped_mm_few.cu -- the grouped block-scaled product where the groups
 // have few rows (decoding): every touched expert's weights are read once for
 // a handful of rows, so HBM bounds it, 1 byte per weight.  512 rows of 64
-// experts, K 2064 to N 2832: 60 us, 6.3 TB/s; eight rows of eight experts, K
-// 2048 to N 4096: 15.7 us, of which 9.9 us are the weights and most of the
+// experts, K 2064 to N 2832: 59 us, 6.4 TB/s; eight rows of eight experts, K
+// 2048 to N 4096: 14.9 us, of which 9.9 us are the weights and most of the
 // rest the launch, the first loads and the last tile.
 //
 // Here the weights are the MMA's M operand (128 output columns) and the rows

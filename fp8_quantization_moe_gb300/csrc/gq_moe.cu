@@ -35,9 +35,9 @@ namespace moe {
 // Bound by latency (65,536 slots are half a megabyte): a warp keeps up to
 // kSortHold ids per lane in registers, all loaded at once, for both passes;
 // longer segments are read twice, in batches of that size.  65,536 slots of
-// 64 experts in 16 blocks: 7.9 us, 8 slots 3.1 us.  A segment of 256
-// slots read 32 at a time in both passes took 12.6 us for 65,536 slots in
-// 8 blocks.
+// 64 experts in 16 blocks: 7.9 us, 8 slots 3.1 us (3.8 launched as a cluster
+// of one block).  A segment of 256 slots read 32 at a time in both passes took
+// 12.6 us for 65,536 slots in 8 blocks.
 constexpr int kSortHold = 8;
 // The rows' tokens are written in the order of the rows, through shared
 // memory, where a block has no more than kSortStage slots: each store written
@@ -508,7 +508,7 @@ gq_status launch_sort(const DeviceInfo& info, const void* ids, bool i64, int64_t
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = blocks > 1 ? 1 : 0;
   return check_cuda(i64 ? cudaLaunchKernelEx(&cfg, sort_kernel<true>, p)
                         : cudaLaunchKernelEx(&cfg, sort_kernel<false>, p),
                     "moe_sort: launch");
