@@ -91,10 +91,12 @@ struct RowParams {
   uint8_t* q;
   float* scales;
   const int32_t* pos;  // (rows, top_k) destination rows, or nullptr: row r goes to row r
-  uint32_t blocks;     // 128-blocks of all rows
-  int64_t out_rows;
+  uint32_t blocks;     // 128-blocks of all rows, below 2^31
+  uint32_t out_rows;   // of pos
   int64_t ld_bytes;    // bytes from one input row to the next
   int32_t K, nb;       // columns, 128-blocks per row
+  uint32_t magic;      // block / nb = block * magic >> shift
+  int32_t shift;
   int32_t top_k;
   bool pow2;
 };
@@ -102,17 +104,19 @@ struct RowParams {
 // Eight lanes per 1x128 block, four consecutive blocks (of one row or of
 // several) per warp; a block's values and its token's positions are loaded at
 // the same time.  A token is read once and its quantized block stored to each
-// of its sorted rows.  65,536 x 4096 bf16: 126 us, 6.4 TB/s; to one sorted row
-// each 147 us, to six 322 us, 6.7 TB/s.  (Two blocks per lane group measured
-// 124 us plain but 156 us sorted; positions before values, to skip tokens
-// without a live slot, 171 us.)
+// of its sorted rows.  65,536 x 4096 bf16: 115 us, 7.1 TB/s; to one sorted row
+// each 120 us; 32,768 x 4096 to six rows each 164 us, 6.7 TB/s.  Issue slots
+// are the next limit: with a division for the row and 64-bit positions 126, 146
+// and 163 us.  (Two blocks per lane group and positions before values, to skip
+// tokens without a live slot, were slower.)
 constexpr int kPosBatch = 8;  // positions held in registers
 
-template <bool kF32>
+template <bool kF32, bool kStream>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowParams p) {
   const int lane = threadIdx.x & 31;
   const uint32_t i = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 4 + (lane >> 3);
-  const uint32_t row = i < p.blocks ? i / static_cast<uint32_t>(p.nb) : 0u;
+  const uint32_t row =
+      i < p.blocks ? static_cast<uint32_t>(static_cast<uint64_t>(i) * p.magic >> p.shift) : 0u;
   const int32_t b = static_cast<int32_t>(i - row * static_cast<uint32_t>(p.nb));
   const int32_t col = b * kBlock + (lane & 7) * kUnit;
   // K % 16 == 0: a unit is wholly inside or outside
@@ -134,22 +138,32 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const RowParams p) {
   for (int o = kUnitsPerBlock / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float s = scale_from_amax_bits(m, p.pow2);
   const uint4 q = u.cast(s);
-  auto store = [&](int64_t r) {
-    if (in) *reinterpret_cast<uint4*>(p.q + r * p.K + col) = q;
-    if (lead) p.scales[r * p.nb + b] = s;
+  uint8_t* const q0 = p.q + col;
+  float* const s0 = p.scales + b;
+  auto store = [&](int32_t r) {
+    uint4* const to_q = reinterpret_cast<uint4*>(q0 + static_cast<int64_t>(r) * p.K);
+    if (in && kStream) __stcs(to_q, q);
+    if (in && !kStream) *to_q = q;
+    if (lead) s0[static_cast<int64_t>(r) * p.nb] = s;
   };
   if (p.pos == nullptr) {
-    store(row);
+    store(static_cast<int32_t>(row));
     return;
   }
+  // a negative position is past every row as an unsigned number
 #pragma unroll
   for (int j = 0; j < kPosBatch; ++j)
-    if (to[j] >= 0 && to[j] < p.out_rows) store(to[j]);
+    if (static_cast<uint32_t>(to[j]) < p.out_rows) store(to[j]);
   for (int32_t j = kPosBatch; j < p.top_k; ++j) {
-    const int64_t r = __ldg(pos + j);
-    if (r >= 0 && r < p.out_rows) store(r);
+    const int32_t r = __ldg(pos + j);
+    if (static_cast<uint32_t>(r) < p.out_rows) store(r);
   }
 }
+
+// An output of this size or more leaves L2 anyway before it is read: stored
+// past it (8192 tokens of 4096 columns to eight rows: 52.3 us instead of 53.9;
+// 16,384 rows of 2048 columns, which stay in L2: 7.2 us instead of 6.5).
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
 
 struct TileParams {
   const uint8_t* w;
@@ -208,7 +222,8 @@ gq_status launch_rows(const void* x, bool f32, int64_t rows, int64_t K,
   p.q = static_cast<uint8_t*>(out);
   p.scales = scales;
   p.pos = pos;
-  p.out_rows = out_rows;
+  constexpr int64_t kMaxRows = int64_t(1) << 31;  // positions are int32
+  p.out_rows = static_cast<uint32_t>(out_rows < kMaxRows ? out_rows : kMaxRows);
   p.ld_bytes = ld * (f32 ? 4 : 2);
   p.K = static_cast<int32_t>(K);
   p.nb = static_cast<int32_t>((K + kBlock - 1) / kBlock);
@@ -216,14 +231,20 @@ gq_status launch_rows(const void* x, bool f32, int64_t rows, int64_t K,
   if (blocks > INT32_MAX)
     return fail(GQ_ERR_UNSUPPORTED, "block_rows: %lld blocks of 128", static_cast<long long>(blocks));
   p.blocks = static_cast<uint32_t>(blocks);
+  // exact for blocks below 2^31, as in moe_sort
+  int l = 0;
+  while ((1 << l) < p.nb) ++l;
+  p.shift = 31 + l;
+  p.magic = static_cast<uint32_t>(((uint64_t(1) << p.shift) + p.nb - 1) / p.nb);
   p.top_k = top_k;
   p.pow2 = pow2;
   constexpr int kPer = kThreads / 32 * 4;  // 128-blocks per thread block
   const int64_t grid = (blocks + kPer - 1) / kPer;
-  if (f32)
-    rows_kernel<true><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
-  else
-    rows_kernel<false><<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
+  const bool past_l2 = (pos != nullptr ? static_cast<int64_t>(p.out_rows) : rows) * K >= kStreamBytes;
+  void (*kernel)(RowParams) =
+      f32 ? (past_l2 ? rows_kernel<true, true> : rows_kernel<true, false>)
+          : (past_l2 ? rows_kernel<false, true> : rows_kernel<false, false>);
+  kernel<<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
   return check_cuda(cudaGetLastError(), "block_rows: launch");
 }
 
