@@ -422,6 +422,18 @@ def test_grouped_mm_many_groups(gq, transposed):
     check_product(gq, int(offs[-1]), 144, 160, offs.tolist(), transposed)
 
 
+@pytest.mark.parametrize("M", [3000, 20000])  # either kernel
+def test_grouped_mm_unordered_ends_of_many_groups(gq, M):
+    """Ends that fall back (also below zero) leave empty groups, ends past M
+    stop there; more groups than the tile table takes at a time."""
+    r = rng(13)
+    ends = np.sort(r.integers(0, M, 300))
+    back = r.choice(290, 60, replace=False)
+    ends[back] = r.integers(-M, np.maximum(ends[back], 1))
+    ends[297:] = M + 7, 5, M + 1
+    check_product(gq, M, 144, 160, ends.tolist(), False)
+
+
 def test_grouped_mm_input_and_output_gradient_are_adjoint(gq):
     """The product is linear in A: along any direction D the difference of
     sum(G * out) is sum(G * product(D)), which grad_input has to give as
