@@ -29,8 +29,9 @@ namespace moe {
 // become each warp's first row of each expert (prefix over the block's
 // warps, over the cluster's blocks through distributed shared memory, over
 // the experts), and a second pass numbers the slots.  Within 32 slots the
-// lanes of one expert find each other by a ballot on every bit of its
-// number and rank themselves, so the sort is stable and its result unique.
+// lanes of one expert find each other, by a match or by a ballot on every bit
+// of its number, and rank themselves, so the sort is stable and its result
+// unique.
 //
 // Bound by latency (65,536 slots are half a megabyte): a warp keeps up to
 // kSortHold ids per lane in registers, all loaded at once, for both passes;
@@ -44,6 +45,11 @@ constexpr int kSortHold = 8;
 // where its slot is found touches 32 sectors, and a block's stores alone would
 // take a cycle each.
 constexpr int kSortStage = 8192;
+// A match takes a step per distinct value, a ballot per bit of the expert's
+// number a fixed time: matches up to this many live lanes of a warp.  98,286
+// slots with three of four dropped: 8.0 us with matches, 9.3 with ballots;
+// 65,536 live slots of 64 experts 9.1 and 7.9.
+constexpr int kSortMatch = 16;
 constexpr int kSortWarpsMax = 32;
 constexpr int kSortClusterMax = 16;  // 8 where a device has no room for 16
 
@@ -189,12 +195,16 @@ __global__ void __launch_bounds__(kSortWarpsMax * 32) sort_kernel(const SortPara
       if (s0 + 32 * i >= hi) break;  // the whole warp
       const int32_t slot = s0 + 32 * i + lane;
       const int32_t e = ids[i];
-      // the lanes with the same expert, from a ballot on every bit of it
+      // the lanes with the same expert
       uint32_t peers = __ballot_sync(0xffffffffu, e >= 0);
-      for (int k = 0; k < p.bits; ++k) {
-        const bool set = (e >> k) & 1;
-        const uint32_t with = __ballot_sync(0xffffffffu, set);
-        peers &= set ? with : ~with;
+      if (__popc(peers) <= kSortMatch) {
+        peers = __match_any_sync(0xffffffffu, e);
+      } else {
+        for (int k = 0; k < p.bits; ++k) {
+          const bool set = (e >> k) & 1;
+          const uint32_t with = __ballot_sync(0xffffffffu, set);
+          peers &= set ? with : ~with;
+        }
       }
       uint32_t place = 0;
       if (e >= 0) place = mine[e] + __popc(peers & ((1u << lane) - 1u));
