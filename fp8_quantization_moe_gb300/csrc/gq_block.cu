@@ -113,6 +113,7 @@ constexpr int kPosBatch = 8;  // positions held in registers
 
 template <bool kF32, bool kStream>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const RowParams p) {
+  grid_wait();
   const int lane = threadIdx.x & 31;
   const uint32_t i = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 4 + (lane >> 3);
   const uint32_t row =
@@ -182,6 +183,7 @@ constexpr int kTileUnits = kBlock * kUnitsPerBlock / kThreads;  // 4 units per t
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads) tiles_kernel(const TileParams p) {
   __shared__ uint32_t red[kThreads / 32];
+  grid_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t per = static_cast<int64_t>(p.nn) * p.nk;
   const int64_t e = blockIdx.x / per;
@@ -244,8 +246,8 @@ gq_status launch_rows(const void* x, bool f32, int64_t rows, int64_t K,
   void (*kernel)(RowParams) =
       f32 ? (past_l2 ? rows_kernel<true, true> : rows_kernel<true, false>)
           : (past_l2 ? rows_kernel<false, true> : rows_kernel<false, false>);
-  kernel<<<static_cast<unsigned>(grid), kThreads, 0, stream>>>(p);
-  return check_cuda(cudaGetLastError(), "block_rows: launch");
+  return launch_chained("block_rows: launch", kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0,
+                        stream, 1, p);
 }
 
 gq_status launch_tiles(const void* w, bool f32, int64_t E, int64_t N, int64_t K, void* out,
@@ -260,11 +262,8 @@ gq_status launch_tiles(const void* w, bool f32, int64_t E, int64_t N, int64_t K,
   p.nk = static_cast<int32_t>((K + kBlock - 1) / kBlock);
   p.pow2 = pow2;
   p.tiles = E * p.nn * p.nk;  // the caller keeps it below 2^31
-  if (f32)
-    tiles_kernel<true><<<static_cast<unsigned>(p.tiles), kThreads, 0, stream>>>(p);
-  else
-    tiles_kernel<false><<<static_cast<unsigned>(p.tiles), kThreads, 0, stream>>>(p);
-  return check_cuda(cudaGetLastError(), "block_tiles: launch");
+  return launch_chained("block_tiles: launch", f32 ? tiles_kernel<true> : tiles_kernel<false>,
+                        dim3(static_cast<unsigned>(p.tiles)), kThreads, 0, stream, 1, p);
 }
 
 }  // namespace block

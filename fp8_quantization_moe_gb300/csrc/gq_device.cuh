@@ -219,6 +219,14 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// First thing in a kernel launched with launch_chained: waits for the kernels
+// before it in the stream and their writes (every thread: a kernel must not
+// end, nor write, before they do), and lets the next one be brought up, which
+// waits in the same way.
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Returns v unchanged, but the compiler must assume it changed here: the
 // addresses of the pure shared loads below are derived from a value pinned
 // after the stage's full barrier, so those loads cannot be issued before the

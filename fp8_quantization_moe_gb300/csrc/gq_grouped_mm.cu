@@ -120,16 +120,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   const uint64_t wait_ns = 4 * p.timeout_ns;
 
-  if (warp == kEpiWarps) {
-    build_tiles(p, kRows, s.tiles, lane);
-    if (lane == 0) {
-      prefetch_tensormap(&amap);
-      prefetch_tensormap(&amap32);
-      prefetch_tensormap(&wmap);
-    }
-  } else if (warp == kEpiWarps + 1) {
-    tmem_alloc(&s.tmem_base, kTmemCols);
-    tmem_relinquish();
+  if (warp == kEpiWarps && lane == 0) {
+    prefetch_tensormap(&amap);
+    prefetch_tensormap(&amap32);
+    prefetch_tensormap(&wmap);
   } else if (warp == kEpiWarps + 2 && lane == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], 1);
@@ -142,6 +136,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&s.drain, 1);
     fence_mbar_init();
+  }
+  grid_wait();
+  if (warp == kEpiWarps) {
+    build_tiles(p, kRows, s.tiles, lane);
+  } else if (warp == kEpiWarps + 1) {
+    tmem_alloc(&s.tmem_base, kTmemCols);
+    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
@@ -532,8 +533,8 @@ gq_status launch(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa, 
   if (st != GQ_OK) return st;
   const unsigned grid = static_cast<unsigned>(most < info.sm_count ? most : info.sm_count);
   const auto kernel = transposed ? product_kernel<true> : product_kernel<false>;
-  kernel<<<grid, kThreads, kSmemBytes, stream>>>(amap, amap32, wmap, p);
-  return check_cuda(cudaGetLastError(), "grouped_mm: launch");
+  return launch_chained("grouped_mm: launch", kernel, dim3(grid), kThreads, kSmemBytes, stream, 1,
+                        amap, amap32, wmap, p);
 }
 
 }  // namespace gmm

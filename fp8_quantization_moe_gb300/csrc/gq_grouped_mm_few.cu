@@ -2,7 +2,7 @@
 // have few rows (decoding): every touched expert's weights are read once for
 // a handful of rows, so HBM bounds it, 1 byte per weight.  512 rows of 64
 // experts, K 2064 to N 2832: 59 us, 6.4 TB/s; eight rows of eight experts, K
-// 2048 to N 4096: 14.9 us, of which 9.9 us are the weights and most of the
+// 2048 to N 4096: 14.3 us, of which 9.9 us are the weights and most of the
 // rest the launch, the first loads and the last tile.
 //
 // Here the weights are the MMA's M operand (128 output columns) and the rows
@@ -153,15 +153,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int lane = threadIdx.x & 31;
   const uint64_t wait_ns = 4 * p.timeout_ns;
 
-  if (warp == kEpiWarps) {
-    build_tiles(p, kTok, s.tiles, lane);
-    if (lane == 0) {
-      prefetch_tensormap(&amap);
-      prefetch_tensormap(&wmap);
-    }
-  } else if (warp == kEpiWarps + 1) {
-    tmem_alloc(&s.tmem_base, 512);
-    tmem_relinquish();
+  if (warp == kEpiWarps && lane == 0) {
+    prefetch_tensormap(&amap);
+    prefetch_tensormap(&wmap);
   } else if (warp == kEpiWarps + 2 && lane == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&s.full[i], 1);
@@ -174,6 +168,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&s.drain, 1);
     fence_mbar_init();
+  }
+  grid_wait();
+  if (warp == kEpiWarps) {
+    build_tiles(p, kTok, s.tiles, lane);
+  } else if (warp == kEpiWarps + 1) {
+    tmem_alloc(&s.tmem_base, 512);
+    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
@@ -388,8 +389,8 @@ gq_status launch_few(const DeviceInfo& info, Params p, const void* qa, const voi
     return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: %lld tiles", static_cast<long long>(most));
   const unsigned grid = static_cast<unsigned>(most < info.sm_count ? most : info.sm_count);
   const auto kernel = p.transposed ? few_kernel<true> : few_kernel<false>;
-  kernel<<<grid, kThreads, kSmemBytes, stream>>>(amap, wmap, p);
-  return check_cuda(cudaGetLastError(), "grouped_mm: launch");
+  return launch_chained("grouped_mm: launch", kernel, dim3(grid), kThreads, kSmemBytes, stream, 1,
+                        amap, wmap, p);
 }
 
 }  // namespace gmm

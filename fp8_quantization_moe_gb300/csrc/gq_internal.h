@@ -49,6 +49,32 @@ gq_status fail(gq_status st, const char* fmt, ...);
 // Returns GQ_ERR_CUDA with the runtime's message if `e` is an error.
 gq_status check_cuda(cudaError_t e, const char* what);
 
+// Launches a kernel that begins with grid_wait: it may be brought up while the
+// kernel before it in the stream still runs, which hides the launch (a sort
+// and the dispatch after it: 33.6 -> 30.5 us in a stream).  `cluster` blocks
+// form a cluster.
+template <typename... P, typename... A>
+gq_status launch_chained(const char* what, void (*kernel)(P...), dim3 grid, unsigned threads,
+                         size_t smem, cudaStream_t stream, unsigned cluster, A... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) (void)cudaGetLastError();  // reported here, once
+  return check_cuda(e, what);
+}
+
 // Colwise workspace layout: a 256-byte header (work counters), one counter
 // per (group, 128-column slab) strip, then the (G, K) amax words.  Offsets
 // in bytes; every region starts on a 256-byte boundary.  Every launch

@@ -82,6 +82,7 @@ __device__ __forceinline__ int32_t expert_of(const SortParams& p, int32_t slot, 
 template <bool kI64>
 __global__ void __launch_bounds__(kSortWarpsMax * 32) sort_kernel(const SortParams p) {
   extern __shared__ uint32_t smem[];
+  grid_wait();
   const int E = p.experts;
   const int warps = blockDim.x >> 5;
   uint32_t* total = smem;          // [E] this block's count of each expert
@@ -282,6 +283,7 @@ __device__ __forceinline__ void load_rows(const int32_t* pos, int32_t j0, int32_
 // One block per token and span: a chunk is read once and stored to each of
 // the token's rows.  8192 tokens of 8 KB to 8 rows each: 92 us, 6.6 TB/s.
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const DispatchParams p) {
+  grid_wait();
   const int64_t t = blockIdx.x;
   const int32_t c = blockIdx.y * p.span + threadIdx.x;
   if (static_cast<int32_t>(threadIdx.x) >= p.span || c >= p.chunks) return;
@@ -353,6 +355,7 @@ struct CombineParams {
 // together, their sum runs in slot order.
 template <bool kF32, int kB>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p) {
+  grid_wait();
   using C = Chunk<kF32>;
   const int64_t t = blockIdx.x;
   const int32_t c = blockIdx.y * p.span + threadIdx.x;
@@ -393,6 +396,7 @@ template <bool kF32, int kB>
 __global__ void __launch_bounds__(kThreads, kB == kBatch ? 3 : 0) combine_backward_kernel(const CombineParams p) {
   using C = Chunk<kF32>;
   __shared__ float part[kThreads / 32][kB];
+  grid_wait();
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int32_t j0 = 0; j0 < p.top_k; j0 += kB) {
@@ -507,23 +511,11 @@ gq_status launch_sort(const DeviceInfo& info, const void* ids, bool i64, int64_t
   while (blocks < info.sort_cluster && static_cast<int64_t>(blocks) * warps * 2 <= groups32) blocks *= 2;
   const int64_t nwarps = static_cast<int64_t>(blocks) * warps;
   p.per_warp = static_cast<int32_t>((groups32 + nwarps - 1) / nwarps * 32);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(warps * 32);
   p.stage = p.per_warp * warps <= kSortStage;
-  cfg.dynamicSmemBytes = static_cast<size_t>(3 + warps) * experts * 4 +
-                         (p.stage ? static_cast<size_t>(p.per_warp) * warps * 8 + 8 : 0);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = blocks;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = blocks > 1 ? 1 : 0;
-  return check_cuda(i64 ? cudaLaunchKernelEx(&cfg, sort_kernel<true>, p)
-                        : cudaLaunchKernelEx(&cfg, sort_kernel<false>, p),
-                    "moe_sort: launch");
+  const size_t smem = static_cast<size_t>(3 + warps) * experts * 4 +
+                      (p.stage ? static_cast<size_t>(p.per_warp) * warps * 8 + 8 : 0);
+  return launch_chained("moe_sort: launch", i64 ? sort_kernel<true> : sort_kernel<false>, dim3(blocks),
+                        warps * 32, smem, stream, blocks, p);
 }
 
 gq_status launch_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int64_t ld_bytes,
@@ -541,8 +533,7 @@ gq_status launch_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int6
   const Spans spans = spans_of(p.chunks);
   p.span = spans.chunks;
   const dim3 grid(static_cast<unsigned>(tokens), spans.count);
-  dispatch_kernel<<<grid, spans.threads, 0, stream>>>(p);
-  return check_cuda(cudaGetLastError(), "moe_dispatch: launch");
+  return launch_chained("moe_dispatch: launch", dispatch_kernel, grid, spans.threads, 0, stream, 1, p);
 }
 
 gq_status launch_combine(const void* y, bool f32, int64_t rows, int64_t H, const int32_t* pos,
@@ -563,8 +554,7 @@ gq_status launch_combine(const void* y, bool f32, int64_t rows, int64_t H, const
   void (*kernel)(CombineParams) =
       f32 ? (top_k <= 4 ? combine_kernel<true, 4> : combine_kernel<true, kBatch>)
           : (top_k <= 4 ? combine_kernel<false, 4> : combine_kernel<false, kBatch>);
-  kernel<<<grid, spans.threads, 0, stream>>>(p);
-  return check_cuda(cudaGetLastError(), "moe_combine: launch");
+  return launch_chained("moe_combine: launch", kernel, grid, spans.threads, 0, stream, 1, p);
 }
 
 gq_status launch_combine_backward(const void* g, const void* y, bool f32, int64_t rows, int64_t H,
@@ -585,8 +575,8 @@ gq_status launch_combine_backward(const void* g, const void* y, bool f32, int64_
   void (*kernel)(CombineParams) =
       f32 ? (top_k <= 4 ? combine_backward_kernel<true, 4> : combine_backward_kernel<true, kBatch>)
           : (top_k <= 4 ? combine_backward_kernel<false, 4> : combine_backward_kernel<false, kBatch>);
-  kernel<<<static_cast<unsigned>(tokens), threads, 0, stream>>>(p);
-  return check_cuda(cudaGetLastError(), "moe_combine_backward: launch");
+  return launch_chained("moe_combine_backward: launch", kernel, dim3(static_cast<unsigned>(tokens)),
+                        threads, 0, stream, 1, p);
 }
 
 }  // namespace moe

@@ -539,6 +539,43 @@ def test_other_stream_and_graph(gq):
     gq.check_device_error()
 
 
+def test_kernels_wait_for_what_the_stream_waits_for(gq):
+    """A kernel may be brought up while the one before it runs; between two of
+    them, a wait for another stream's event, a copy from the host and a plain
+    kernel still come first, and a late reader sees complete results."""
+    T, k, E, H = 512, 4, 8, 1024
+    r = rng(41)
+    ids = torch.from_numpy(r.integers(0, E, (T, k))).to(DEV)
+    host = [torch.from_numpy(r.standard_normal((T, H)).astype(np.float32)).to(torch.bfloat16).pin_memory()
+            for _ in range(3)]
+    busy = torch.randn(4096, 4096, device=DEV)
+    x = torch.zeros(3, T, H, dtype=torch.bfloat16, device=DEV)
+    late = host[0].to(DEV)
+    torch.cuda.synchronize()
+    other, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    event = torch.cuda.Event()
+    with torch.cuda.stream(other):
+        for _ in range(20):
+            busy = busy @ busy * 1e-3
+        x[0].copy_(late)
+        event.record()
+    with torch.cuda.stream(mine):
+        order = gq.sort_tokens(ids, E)
+        mine.wait_event(event)
+        first = gq.dispatch(x[0], order.pos)
+        x[1].copy_(host[1], non_blocking=True)
+        second, _ = gq.dispatch_block(x[1], order.pos)
+        x[2].copy_(host[2].to(DEV, non_blocking=True))
+        third = gq.combine(gq.dispatch(x[2], order.pos), order.pos)
+        x.zero_()
+    torch.cuda.synchronize()
+    pos = order.pos.long()
+    assert torch.equal(first[pos], late[:, None].expand(T, k, H))
+    q, _ = gq.block_rows(host[1].to(DEV))
+    assert torch.equal(second.view(torch.uint8)[pos], q.view(torch.uint8)[:, None].expand(T, k, H))
+    assert torch.equal(third, host[2].to(DEV) * k)  # k copies of a row: exact
+
+
 def test_binding_refuses_bad_arguments(gq):
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
     pos = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
