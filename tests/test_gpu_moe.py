@@ -576,6 +576,69 @@ def test_kernels_wait_for_what_the_stream_waits_for(gq):
     assert torch.equal(third, host[2].to(DEV) * k)  # k copies of a row: exact
 
 
+@pytest.mark.parametrize("T,k,E,H,N", [(1, 8, 16, 512, 256), (96, 4, 8, 1040, 528), (1500, 2, 4, 256, 640)])
+def test_steps_that_share_buffers(gq, T, k, E, H, N):
+    """Steps on other inputs run one after the other through the same buffers
+    and without a stop give what they give alone: no kernel reads or writes a
+    buffer that one before it still uses."""
+    r = rng(42)
+    steps = 40
+    x = torch.from_numpy(r.standard_normal((steps, T, H)).astype(np.float32)).to(DEV).to(torch.bfloat16)
+    ids = torch.from_numpy(r.integers(0, E, (steps, T, k))).to(DEV)
+    wt = torch.from_numpy(r.random((steps, T, k)).astype(np.float32)).to(DEV)
+    qw, sw = gq.block_tiles(torch.from_numpy(r.standard_normal((E, N, H)).astype(np.float32)).to(DEV))
+    q = torch.empty(T * k, H, dtype=torch.float8_e4m3fn, device=DEV)
+    s = torch.empty(T * k, -(-H // 128), device=DEV)
+    y, dy = (torch.empty(T * k, N, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    dx_rows = torch.empty(T * k, H, dtype=torch.bfloat16, device=DEV)
+
+    def step(i, out, dw, dx, stop):
+        order = gq.sort_tokens(ids[i], E)
+        stop()
+        gq.dispatch_block(x[i], order.pos, out=q, scales=s)
+        stop()
+        gq.grouped_mm(q, s, qw, sw, order.offs, out=y)
+        stop()
+        gq.combine(y, order.pos, wt[i], out=out)
+        stop()
+        gq.combine_backward(out, y, order.pos, wt[i], dy=dy, dweights=dw)
+        stop()
+        qd, sd = gq.block_rows(dy)
+        stop()
+        gq.grouped_mm(qd, sd, qw, sw, order.offs, transpose_b=True, out=dx_rows)
+        stop()
+        gq.combine(dx_rows, order.pos, out=dx)
+        stop()
+
+    def run(stop):
+        out = torch.empty(steps, T, N, dtype=torch.bfloat16, device=DEV)
+        dw = torch.empty(steps, T, k, device=DEV)
+        dx = torch.empty(steps, T, H, dtype=torch.bfloat16, device=DEV)
+        for i in range(steps):
+            step(i, out[i], dw[i], dx[i], stop)
+        gq.check_device_error()
+        return out, dw, dx
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(5):
+        for g, w in zip(run(lambda: None), want):
+            assert torch.equal(g, w)
+    # and the same from one CUDA graph, where nothing but the GPU sets the pace
+    out, dw, dx = (torch.zeros_like(w) for w in want)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            for i in range(steps):
+                step(i, out[i], dw[i], dx[i], lambda: None)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    for g, w in zip((out, dw, dx), want):
+        assert torch.equal(g, w)
+
+
 def test_binding_refuses_bad_arguments(gq):
     x = torch.zeros(4, 64, dtype=torch.bfloat16, device=DEV)
     pos = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
