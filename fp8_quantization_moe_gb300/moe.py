@@ -160,6 +160,8 @@ def _block_rows(name, x, pos, out, scales, pow2_scales, stream):
         tokens, k = pos.shape
         if tokens != T:
             raise ValueError(f"{name}: pos must have a row for each row of x")
+        if T > 0 and k == 0:  # an empty tensor's address is NULL: no positions, a row per token
+            raise ValueError(f"{name}: pos must have at least one column")
         rows = T * k
         to = pos.data_ptr()
         if out is not None:
