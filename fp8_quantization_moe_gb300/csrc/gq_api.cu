@@ -660,7 +660,8 @@ gq_status gq_moe_combine_backward(const void* g, const void* y, int dtype, int64
     return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
   if (!aligned(pos, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
     return fail(GQ_ERR_INVALID_ARG, "%s: pos, weights and dweights must be 4-byte aligned", name);
-  if (rows > 0 && H > 0 && (g == nullptr || y == nullptr || dy == nullptr))
+  // g is read for every token, whether or not a slot is live
+  if (H > 0 && (g == nullptr || (rows > 0 && (y == nullptr || dy == nullptr))))
     return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
   if (!aligned(g, 16) || !aligned(y, 16) || !aligned(dy, 16))
     return fail(GQ_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", name);
