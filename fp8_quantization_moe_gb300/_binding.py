@@ -154,6 +154,20 @@ def _stream_handle(stream, device):
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """Memory for an output of a call on ``stream`` (None: the current
+    stream), from that stream's pool: the allocator hands out what was freed
+    on a stream in that stream's order only, so the current stream may still
+    be at work on what its own pool gives, and a temporary that is dropped
+    after the call has to wait for ``stream``."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _ws_ptr(buf):
     if buf is None:
         return None, 0

@@ -12,8 +12,8 @@
 Argument marshalling over include/gq_fp8.h, as in the rest of the binding:
 torch supplies device memory and streams, every call is asynchronous on
 ``stream`` (default: the current stream), and can be captured into a CUDA
-graph.  Outputs that are not passed in are allocated uninitialised; rows that
-a call does not write keep what they held.
+graph.  Outputs that are not passed in are allocated uninitialised, on
+``stream``; rows that a call does not write keep what they held.
 """
 from __future__ import annotations
 
@@ -21,7 +21,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._binding import GQ_DTYPE_BF16, GQ_DTYPE_F32, GQ_SCALE_POW2, _check, lib
+from ._binding import GQ_DTYPE_BF16, GQ_DTYPE_F32, GQ_SCALE_POW2, _check, _empty, lib
 
 BLOCK = 128
 _DTYPES = {torch.bfloat16: GQ_DTYPE_BF16, torch.float32: GQ_DTYPE_F32}
@@ -109,9 +109,9 @@ def sort_tokens(ids: torch.Tensor, n_experts: int, *, stream=None) -> TokenOrder
     _need(ids, "sort_tokens: ids", 2, _INT)
     T, k = ids.shape
     dev = ids.device
-    offs = torch.empty(n_experts if n_experts > 0 else 0, dtype=torch.int32, device=dev)
-    pos = torch.empty((T, k), dtype=torch.int32, device=dev)
-    token = torch.empty(T * k, dtype=torch.int32, device=dev)
+    offs = _empty(n_experts if n_experts > 0 else 0, torch.int32, dev, stream)
+    pos = _empty((T, k), torch.int32, dev, stream)
+    token = _empty(T * k, torch.int32, dev, stream)
     _call("gq_moe_sort", dev.index, stream, lib().gq_moe_sort, ids.data_ptr(), ids.element_size(),
           T, k, n_experts, offs.data_ptr(), pos.data_ptr(), token.data_ptr())
     return TokenOrder(offs, pos, token)
@@ -137,7 +137,7 @@ def dispatch(x: torch.Tensor, pos: torch.Tensor, *, out=None, stream=None) -> to
         raise ValueError("dispatch: pos must have a row for each row of x")
     k = pos.shape[1]
     if out is None:
-        out = torch.empty((T * k, H), dtype=x.dtype, device=dev)
+        out = _empty((T * k, H), x.dtype, dev, stream)
     else:
         _need(out, "dispatch: out", 2, (x.dtype,), dev.index)
         if out.shape[1] != H:
@@ -168,11 +168,11 @@ def _block_rows(name, x, pos, out, scales, pow2_scales, stream):
             _need(out, name + ": out", 2, _FP8, index)
             rows = out.shape[0]
     if out is None:
-        out = torch.empty((rows, K), dtype=torch.float8_e4m3fn, device=dev)
+        out = _empty((rows, K), torch.float8_e4m3fn, dev, stream)
     else:
         _need(out, name + ": out", 2, _FP8, index, (rows, K))
     if scales is None:
-        scales = torch.empty((rows, _blocks(K)), dtype=torch.float32, device=dev)
+        scales = _empty((rows, _blocks(K)), torch.float32, dev, stream)
     else:
         _need(scales, name + ": scales", 2, _F32, index, (rows, _blocks(K)))
     _call("gq_fp8_block_rows", index, stream, lib().gq_fp8_block_rows, x.data_ptr(),
@@ -208,11 +208,11 @@ def block_tiles(w: torch.Tensor, *, out=None, scales=None, pow2_scales: bool = F
     E, N, K = w.shape
     dev = w.device
     if out is None:
-        out = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=dev)
+        out = _empty((E, N, K), torch.float8_e4m3fn, dev, stream)
     else:
         _need(out, "block_tiles: out", 3, _FP8, dev.index, (E, N, K))
     if scales is None:
-        scales = torch.empty((E, _blocks(N), _blocks(K)), dtype=torch.float32, device=dev)
+        scales = _empty((E, _blocks(N), _blocks(K)), torch.float32, dev, stream)
     else:
         _need(scales, "block_tiles: scales", 3, _F32, dev.index, (E, _blocks(N), _blocks(K)))
     _call("gq_fp8_block_tiles", dev.index, stream, lib().gq_fp8_block_tiles, w.data_ptr(),
@@ -247,7 +247,7 @@ def grouped_mm(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.T
     _need(sb, "grouped_mm: sb", 3, _F32, index, (E, _blocks(N), _blocks(K)))
     _need(offs, "grouped_mm: offs", 1, _I32, index, (E,))
     if out is None:
-        out = torch.empty((M, outer), dtype=torch.bfloat16, device=dev)
+        out = _empty((M, outer), torch.bfloat16, dev, stream)
     else:
         _need(out, "grouped_mm: out", 2, (torch.bfloat16,), index, (M, outer))
     _call("gq_grouped_mm", index, stream, lib().gq_grouped_mm, qa.data_ptr(), sa.data_ptr(), M,
@@ -276,7 +276,7 @@ def combine(y: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] 
     if weights is not None:
         _need(weights, "combine: weights", 2, _F32, index, (T, k))
     if out is None:
-        out = torch.empty((T, H), dtype=y.dtype, device=dev)
+        out = _empty((T, H), y.dtype, dev, stream)
     else:
         _need(out, "combine: out", 2, (y.dtype,), index, (T, H))
     _call("gq_moe_combine", index, stream, lib().gq_moe_combine, y.data_ptr(), _DTYPES[y.dtype],
@@ -301,11 +301,11 @@ def combine_backward(g: torch.Tensor, y: torch.Tensor, pos: torch.Tensor, weight
     _need(g, "combine_backward: g", 2, (y.dtype,), index, (T, H))
     _need(weights, "combine_backward: weights", 2, _F32, index, (T, k))
     if dy is None:
-        dy = torch.empty((rows, H), dtype=y.dtype, device=dev)
+        dy = _empty((rows, H), y.dtype, dev, stream)
     else:
         _need(dy, "combine_backward: dy", 2, (y.dtype,), index, (rows, H))
     if dweights is None:
-        dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        dweights = _empty((T, k), torch.float32, dev, stream)
     else:
         _need(dweights, "combine_backward: dweights", 2, _F32, index, (T, k))
     _call("gq_moe_combine_backward", index, stream, lib().gq_moe_combine_backward, g.data_ptr(),

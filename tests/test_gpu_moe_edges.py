@@ -23,6 +23,11 @@ def randn(seed, *shape, dtype=torch.bfloat16):
     return torch.from_numpy(r.standard_normal(shape).astype(np.float32)).to(DEV).to(dtype)
 
 
+def draw_ids(seed, T, k, E, local):
+    ids = torch.from_numpy(np.random.default_rng(seed).integers(0, E, (T, k))).to(DEV)
+    return torch.where(ids < local, ids, -1)
+
+
 # ------------------------------------------------------------------ slots --
 
 def test_dispatch_block_refuses_tokens_without_slots(gq):
@@ -39,3 +44,72 @@ def test_dispatch_block_refuses_tokens_without_slots(gq):
         gq.dispatch_block(x, pos)
     q, s = gq.dispatch_block(x[:0], pos[:0])  # no tokens either: nothing to do
     assert q.shape == (0, 64) and s.shape == (0, 1)
+
+
+# ---------------------------------------------------------------- streams --
+
+def stream_of(t):
+    """The stream whose pool the allocator took t's memory from."""
+    p = t.data_ptr()
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= p < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's memory")
+
+
+def test_outputs_belong_to_the_stream_of_the_call(gq):
+    """A call on another stream takes its outputs from that stream's memory:
+    what the current stream has freed may still be in use there."""
+    T, k, E, H, N = 64, 4, 8, 256, 128
+    x, w, g, ids = randn(13, T, H), randn(14, E, N, H), randn(15, T, N), draw_ids(16, T, k, E, E)
+    wt = torch.rand(T, k, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, torch.cuda.ExternalStream(side.cuda_stream)):
+        order = gq.sort_tokens(ids, E, stream=stream)
+        rows = gq.dispatch(x, order.pos, stream=stream)
+        q, s = gq.dispatch_block(x, order.pos, stream=stream)
+        q2, s2 = gq.block_rows(x, stream=stream)
+        qw, sw = gq.block_tiles(w, stream=stream)
+        y = gq.grouped_mm(q, s, qw, sw, order.offs, stream=stream)
+        out = gq.combine(y, order.pos, wt, stream=stream)
+        dy, dw = gq.combine_backward(g, y, order.pos, wt, stream=stream)
+        for t in (*order, rows, q, s, q2, s2, qw, sw, y, out, dy, dw):
+            assert stream_of(t) == side.cuda_stream
+        torch.cuda.synchronize()
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    assert stream_of(gq.block_rows(x)[0]) == torch.cuda.default_stream().cuda_stream
+    assert stream_of(gq.block_rows(x, stream=torch.cuda.default_stream())[0]) == torch.cuda.default_stream().cuda_stream
+
+
+def test_chain_on_a_passed_stream_beside_the_current_one(gq):
+    """The chain with stream=, while the current stream frees and allocates
+    buffers of the same sizes, gives what it gives alone."""
+    T, k, E, H, N = 256, 4, 8, 512, 384
+    x, w, wt = randn(17, T, H), randn(18, E, N, H), torch.rand(T, k, device=DEV)
+    ids = draw_ids(19, T, k, E, 6)
+    qw, sw = gq.block_tiles(w)
+
+    def chain(stream=None):
+        order = gq.sort_tokens(ids, E, stream=stream)
+        q, s = gq.dispatch_block(x, order.pos, stream=stream)
+        y = gq.grouped_mm(q, s, qw, sw, order.offs, stream=stream)
+        return gq.combine(y, order.pos, wt, stream=stream)
+
+    want = chain()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    sums, kept = [], torch.ones(T * k, N, dtype=torch.bfloat16, device=DEV)
+    for _ in range(30):
+        # twins of the chain's buffers, read on the current stream after they were freed
+        for shape, dtype in (((T * k, H), torch.uint8), ((T * k, N), torch.bfloat16), ((T, N), torch.bfloat16)):
+            b = torch.ones(shape, dtype=dtype, device=DEV)
+            sums.append((b.double().sum(), b.numel()))
+            del b
+        kept = kept @ torch.eye(N, dtype=torch.bfloat16, device=DEV)
+        got.append(chain(side))
+    torch.cuda.synchronize()
+    gq.check_device_error()
+    assert all(torch.equal(g, want) for g in got)
+    assert all(float(s) == n for s, n in sums) and (kept == 1).all()
