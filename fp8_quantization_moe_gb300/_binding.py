@@ -210,9 +210,9 @@ def colwise(x: torch.Tensor, offs: torch.Tensor, *, out=None, scales=None,
     G = offs.numel()
     dev = x.device
     if out is None:
-        out = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        out = _empty((M, K), torch.float8_e4m3fn, dev, stream)
     if scales is None:
-        scales = torch.empty((G, K), dtype=torch.float32, device=dev)
+        scales = _empty((G, K), torch.float32, dev, stream)
     if out.shape != (M, K) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("colwise: out must be a contiguous 1-byte (M, K) tensor")
     if scales.shape != (G, K) or scales.dtype != torch.float32 or not scales.is_contiguous():
@@ -247,9 +247,9 @@ def rowwise_t(a: torch.Tensor, offs: torch.Tensor, *, out=None, scales=None,
     G = offs.numel()
     dev = a.device
     if out is None:
-        out = torch.empty((Mg, N), dtype=torch.float8_e4m3fn, device=dev)
+        out = _empty((Mg, N), torch.float8_e4m3fn, dev, stream)
     if scales is None:
-        scales = torch.empty((N, G), dtype=torch.float32, device=dev)
+        scales = _empty((N, G), torch.float32, dev, stream)
     if out.shape != (Mg, N) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("rowwise_t: out must be a contiguous 1-byte (Mg, N) tensor")
     if scales.shape != (N, G) or scales.dtype != torch.float32 or not scales.is_contiguous():
@@ -281,9 +281,9 @@ def expert_dim1(w: torch.Tensor, *, out=None, scales=None, stream=None, workspac
     E, K, N = w.shape
     dev = w.device
     if out is None:
-        out = torch.empty((E, K, N), dtype=torch.float8_e4m3fn, device=dev)
+        out = _empty((E, K, N), torch.float8_e4m3fn, dev, stream)
     if scales is None:
-        scales = torch.empty((E, N), dtype=torch.float32, device=dev)
+        scales = _empty((E, N), torch.float32, dev, stream)
     if out.shape != (E, K, N) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("expert_dim1: out must be a contiguous 1-byte (E, K, N) tensor")
     if scales.shape != (E, N) or scales.dtype != torch.float32 or not scales.is_contiguous():
@@ -315,9 +315,9 @@ def expert_rowwise(w: torch.Tensor, *, out=None, scales=None, stream=None,
     E, N, K = w.shape
     dev = w.device
     if out is None:
-        out = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=dev)
+        out = _empty((E, N, K), torch.float8_e4m3fn, dev, stream)
     if scales is None:
-        scales = torch.empty((E, N), dtype=torch.float32, device=dev)
+        scales = _empty((E, N), torch.float32, dev, stream)
     if out.shape != (E, N, K) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("expert_rowwise: out must be a contiguous 1-byte (E, N, K) tensor")
     if scales.shape != (E, N) or scales.dtype != torch.float32 or not scales.is_contiguous():
@@ -344,9 +344,9 @@ def mxfp8_dim0(x: torch.Tensor, mode: str = "floor", *, out=None, scales=None, s
     M, K = x.shape
     dev = x.device
     if out is None:
-        out = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        out = _empty((M, K), torch.float8_e4m3fn, dev, stream)
     if scales is None:
-        scales = torch.empty((M, K // 32), dtype=torch.uint8, device=dev)
+        scales = _empty((M, K // 32), torch.uint8, dev, stream)
     if out.shape != (M, K) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("mxfp8_dim0: out must be a contiguous 1-byte (M, K) tensor")
     if scales.shape != (M, K // 32) or scales.element_size() != 1 or not scales.is_contiguous():
@@ -382,7 +382,7 @@ def grouped_wgrad(qa_t: torch.Tensor, sa: torch.Tensor, qx: torch.Tensor, sx: to
             raise ValueError(f"grouped_wgrad: {name} must be a contiguous float32 {shape} CUDA tensor")
     dev = qa_t.device
     if out is None:
-        out = torch.empty((G, N, K), dtype=torch.bfloat16, device=dev)
+        out = _empty((G, N, K), torch.bfloat16, dev, stream)
     if out.shape != (G, N, K) or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("grouped_wgrad: out must be a contiguous bf16 (G, N, K) tensor")
     sh = _stream_handle(stream, dev)
@@ -406,9 +406,9 @@ def colwise_noalloc(x: torch.Tensor, offs: torch.Tensor, *, out=None,
     G = offs.numel()
     dev = x.device
     if out is None:
-        out = torch.empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
+        out = _empty((M, K), torch.float8_e4m3fn, dev, stream)
     if scales is None:
-        scales = torch.empty((G, K), dtype=torch.float32, device=dev)
+        scales = _empty((G, K), torch.float32, dev, stream)
     if out.shape != (M, K) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("colwise_noalloc: out must be a contiguous 1-byte (M, K) tensor")
     if scales.shape != (G, K) or scales.dtype != torch.float32 or not scales.is_contiguous():

@@ -82,6 +82,27 @@ def test_outputs_belong_to_the_stream_of_the_call(gq):
     assert stream_of(gq.block_rows(x, stream=torch.cuda.default_stream())[0]) == torch.cuda.default_stream().cuda_stream
 
 
+def test_outputs_of_the_per_group_calls_belong_to_the_stream_of_the_call(gq):
+    """The same of the calls that scale per token group."""
+    M, K, G = 256, 128, 4
+    x, w = randn(22, M, K), randn(23, G, K, K)
+    xt = x.t().contiguous()
+    offs = torch.arange(M // G, M + 1, M // G, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    q, s = gq.colwise(x, offs, stream=side)
+    qt, st = gq.rowwise_t(xt, offs, stream=side)
+    outs = [q, s, qt, st, gq.grouped_wgrad(qt, st, q, s, offs, stream=side)]
+    for call in (gq.expert_dim1, gq.expert_rowwise):
+        outs += call(w, stream=side)
+    outs += gq.mxfp8_dim0(x, stream=side)
+    outs += gq.colwise_noalloc(x, offs, stream=side)
+    torch.cuda.synchronize()
+    gq.check_device_error()
+    assert len(outs) == 13
+    assert all(stream_of(t) == side.cuda_stream for t in outs)
+
+
 def test_chain_on_a_passed_stream_beside_the_current_one(gq):
     """The chain with stream=, while the current stream frees and allocates
     buffers of the same sizes, gives what it gives alone."""
