@@ -54,7 +54,9 @@ struct Unit<false> {
   __device__ __forceinline__ uint32_t amax_bits() const {
     const uint32_t a = absmax_bf16x2(absmax_bf16x2(v[0].x, v[0].y), absmax_bf16x2(v[0].z, v[0].w));
     const uint32_t b = absmax_bf16x2(absmax_bf16x2(v[1].x, v[1].y), absmax_bf16x2(v[1].z, v[1].w));
-    return amax_bits_of(absmax_bf16x2(a, b));
+    // the last maximum, with zero, drops a NaN that all values of a half share;
+    // its bits would win every comparison that follows
+    return amax_bits_of(absmax_bf16x2(absmax_bf16x2(a, b), 0u));
   }
   __device__ __forceinline__ uint4 cast(float s) const {
     return make_uint4(quant4(v[0].x, v[0].y, s, s, s, s), quant4(v[0].z, v[0].w, s, s, s, s),

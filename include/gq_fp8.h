@@ -379,6 +379,9 @@ gq_status gq_moe_combine_backward(const void* g, const void* y, int dtype, int64
  * quantized row t and its scales go to the sorted rows pos[t][j] (the
  * quantized form of gq_moe_dispatch; untouched and dropped rows as there),
  * without it (NULL) to row t.
+ * A NaN becomes e4m3's NaN and does not count in its block's amax; an
+ * infinity becomes e4m3's NaN and its block's scale 0, the block's other
+ * values zeros.
  *
  *   x        bf16 or fp32 (dtype) [rows, K], rows ld elements apart, 16-byte
  *            aligned, a row pitch multiple of 16 bytes.           (input)

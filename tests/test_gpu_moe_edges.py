@@ -6,6 +6,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
+NAN, INF = float("nan"), float("inf")
 
 
 @pytest.fixture(scope="module")
@@ -44,6 +45,47 @@ def test_dispatch_block_refuses_tokens_without_slots(gq):
         gq.dispatch_block(x, pos)
     q, s = gq.dispatch_block(x[:0], pos[:0])  # no tokens either: nothing to do
     assert q.shape == (0, 64) and s.shape == (0, 1)
+
+
+# ----------------------------------------------------- non-finite values --
+
+def holes(seed, R, K):
+    """A mask of single elements, whole and half 16-column units, and whole
+    128-blocks."""
+    r = np.random.default_rng(seed)
+    m = r.random((R, K)) < 0.01
+    for _ in range(R // 2):
+        row, unit = r.integers(R), 16 * r.integers(K // 16)
+        m[row, unit + r.integers(2):unit + 16:r.integers(1, 3)] = True
+        m[r.integers(R), unit:unit + 16] = True
+    m[R // 3, :128] = True
+    return torch.from_numpy(m).to(DEV)
+
+
+@pytest.mark.parametrize("form", ["rows", "dispatch", "tiles"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_block_scales_do_not_count_nan(gq, form, dtype):
+    """A NaN becomes e4m3's NaN and counts for nothing in its block's scale,
+    wherever it stands and in either type: the block's other values are
+    quantized as if it were zero."""
+    R, K = 130, 400
+    x, nan = randn(5, R, K, dtype=dtype), holes(6, R, K)
+
+    def quantized(v):
+        if form == "rows":
+            return gq.block_rows(v)
+        if form == "tiles":
+            return gq.block_tiles(v.view(2, R // 2, K))
+        return gq.dispatch_block(v, torch.arange(R, dtype=torch.int32, device=DEV).flip(0)[:, None])
+
+    want_q, want_s = quantized(x.masked_fill(nan, 0.0))
+    for sign in (1.0, -1.0):
+        q, s = quantized(x.masked_fill(nan, 0.0) + torch.where(nan, sign * NAN, 0.0).to(dtype))
+        at = nan.flip(0) if form == "dispatch" else nan
+        assert torch.equal(s, want_s)
+        q, wq = q.view(torch.uint8).reshape(R, K), want_q.view(torch.uint8).reshape(R, K)
+        assert ((q[at] & 0x7F) == 0x7F).all()
+        assert torch.equal(q[~at], wq[~at])
 
 
 # ---------------------------------------------------------------- streams --
