@@ -41,6 +41,12 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
+def _count(n: int) -> int:
+    """n as a 32-bit argument of the library.  What does not fit is passed as
+    the largest, which it refuses, and not cut to its lower half."""
+    return n if n < 1 << 31 else (1 << 31) - 1
+
+
 # A call on small sizes is as long as its host side: the current stream and
 # device are asked for directly (0.1 us each; torch.cuda.current_stream takes
 # 2 us), and an argument's checks are one expression.
@@ -113,7 +119,7 @@ def sort_tokens(ids: torch.Tensor, n_experts: int, *, stream=None) -> TokenOrder
     pos = _empty((T, k), torch.int32, dev, stream)
     token = _empty(T * k, torch.int32, dev, stream)
     _call("gq_moe_sort", dev.index, stream, lib().gq_moe_sort, ids.data_ptr(), ids.element_size(),
-          T, k, n_experts, offs.data_ptr(), pos.data_ptr(), token.data_ptr())
+          T, _count(k), _count(n_experts), offs.data_ptr(), pos.data_ptr(), token.data_ptr())
     return TokenOrder(offs, pos, token)
 
 
@@ -144,7 +150,7 @@ def dispatch(x: torch.Tensor, pos: torch.Tensor, *, out=None, stream=None) -> to
             raise ValueError(f"dispatch: out must have rows of {H} columns")
     size = x.element_size()
     _call("gq_moe_dispatch", dev.index, stream, lib().gq_moe_dispatch, x.data_ptr(), T, H * size,
-          pitch * size, pos.data_ptr(), k, out.shape[0], out.data_ptr())
+          pitch * size, pos.data_ptr(), _count(k), out.shape[0], out.data_ptr())
     return out
 
 
@@ -176,7 +182,7 @@ def _block_rows(name, x, pos, out, scales, pow2_scales, stream):
     else:
         _need(scales, name + ": scales", 2, _F32, index, (rows, _blocks(K)))
     _call("gq_fp8_block_rows", index, stream, lib().gq_fp8_block_rows, x.data_ptr(),
-          _DTYPES[x.dtype], T, K, pitch, to, k, rows,
+          _DTYPES[x.dtype], T, K, pitch, to, _count(k), rows,
           out.data_ptr(), scales.data_ptr(), GQ_SCALE_POW2 if pow2_scales else 0)
     return out, scales
 
@@ -280,7 +286,7 @@ def combine(y: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] 
     else:
         _need(out, "combine: out", 2, (y.dtype,), index, (T, H))
     _call("gq_moe_combine", index, stream, lib().gq_moe_combine, y.data_ptr(), _DTYPES[y.dtype],
-          rows, H, pos.data_ptr(), None if weights is None else weights.data_ptr(), T, k,
+          rows, H, pos.data_ptr(), None if weights is None else weights.data_ptr(), T, _count(k),
           out.data_ptr())
     return out
 
@@ -309,6 +315,6 @@ def combine_backward(g: torch.Tensor, y: torch.Tensor, pos: torch.Tensor, weight
     else:
         _need(dweights, "combine_backward: dweights", 2, _F32, index, (T, k))
     _call("gq_moe_combine_backward", index, stream, lib().gq_moe_combine_backward, g.data_ptr(),
-          y.data_ptr(), _DTYPES[y.dtype], rows, H, pos.data_ptr(), weights.data_ptr(), T, k,
+          y.data_ptr(), _DTYPES[y.dtype], rows, H, pos.data_ptr(), weights.data_ptr(), T, _count(k),
           dy.data_ptr(), dweights.data_ptr())
     return dy, dweights

@@ -47,6 +47,26 @@ def test_dispatch_block_refuses_tokens_without_slots(gq):
     assert q.shape == (0, 64) and s.shape == (0, 1)
 
 
+def test_counts_past_32_bits_are_refused(gq):
+    """The library takes slots per token and experts as 32-bit numbers; larger
+    ones are not cut to their lower half."""
+    many = torch.empty(1, 2 ** 32 + 2, dtype=torch.int32, device=DEV)
+    many[:, :2] = 0
+    x = randn(2, 1, 64)
+    out, scales = torch.zeros(1, 64, dtype=torch.float8_e4m3fn, device=DEV), torch.zeros(1, 1, device=DEV)
+    for call in (
+        lambda: gq.sort_tokens(many, 4),
+        lambda: gq.dispatch(x, many, out=x.clone()),
+        lambda: gq.dispatch_block(x, many, out=out, scales=scales),
+        lambda: gq.combine(x, many),
+        lambda: gq.sort_tokens(torch.zeros(1, 1, dtype=torch.int32, device=DEV), 2 ** 32 + 4),
+    ):
+        with pytest.raises(gq.GQError) as e:
+            call()
+        assert e.value.status == 2
+        torch.cuda.empty_cache()
+
+
 # ----------------------------------------------------- non-finite values --
 
 def holes(seed, R, K):
