@@ -187,10 +187,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // every load has landed and been read before the block may exit
-      for (uint32_t u = 0; ok && u < kStages; ++u) {
+      // the block must not exit while a load is still writing its memory, also
+      // after a wait that ran out; the MMAs that read it are waited for below
+      for (uint32_t u = 0; u < kStages; ++u) {
         const uint32_t uses = use + (u < st ? 1 : 0);
-        if (uses > 0) ok = mbar_wait_warp(done + u * 8, (uses - 1) & 1, wait_ns, p.err);
+        if (uses > 0) mbar_wait_warp(smem_addr(&s.full[u]), (uses - 1) & 1, wait_ns, p.err);
       }
     } else if (warp == kEpiWarps + 1) {
       // ----------------------------------------------------------- MMAs --

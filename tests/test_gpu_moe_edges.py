@@ -196,3 +196,30 @@ def test_chain_on_a_passed_stream_beside_the_current_one(gq):
     gq.check_device_error()
     assert all(torch.equal(g, want) for g in got)
     assert all(float(s) == n for s, n in sums) and (kept == 1).all()
+
+
+# ------------------------------------------------------------------ waits --
+
+@pytest.mark.parametrize("M", [40, 64])  # either kernel
+@pytest.mark.parametrize("transposed", [False, True])
+def test_grouped_mm_waits_run_out(gq, M, transposed):
+    """A withheld accumulator release makes the first block's MMAs wait in vain
+    (eight 128-blocks, more than either kernel has accumulators): every role
+    leaves its loop after the shortened limit, the status is GQ_ERR_TIMEOUT,
+    and the next call is right."""
+    N, K = (1024, 256) if transposed else (256, 1024)
+    qa, sa = gq.block_rows(randn(20, M, 1024))
+    qb, sb = gq.block_tiles(randn(21, 1, N, K))
+    o = torch.tensor([M], dtype=torch.int32, device=DEV)
+    want = gq.grouped_mm(qa, sa, qb, sb, o, transpose_b=transposed)
+    gq.check_device_error()
+    try:
+        gq.debug_set(skip_arrival=True, wait_timeout_ns=5_000_000)
+        gq.grouped_mm(qa, sa, qb, sb, o, transpose_b=transposed)
+        with pytest.raises(gq.GQError) as e:
+            gq.check_device_error()
+        assert e.value.status == 4
+    finally:
+        gq.debug_set(False, 0)
+    assert torch.equal(gq.grouped_mm(qa, sa, qb, sb, o, transpose_b=transposed), want)
+    gq.check_device_error()
