@@ -67,6 +67,46 @@ def test_counts_past_32_bits_are_refused(gq):
         torch.cuda.empty_cache()
 
 
+def outside(rows, T, k, seed):
+    """Positions of which about half lie outside a buffer of `rows` rows."""
+    r = np.random.default_rng(seed)
+    pos = np.full(T * k, -1, np.int64)
+    inside = r.permutation(T * k)[:rows]
+    pos[inside] = r.permutation(rows)[:inside.size]
+    bad = pos < 0
+    pos[bad] = r.choice([-1, -5, -2 ** 31, rows, rows + 1, rows + 1000, 2 ** 31 - 1], bad.sum())
+    return torch.from_numpy(pos.reshape(T, k).astype(np.int32)).to(DEV)
+
+
+@pytest.mark.parametrize("T,k,rows,H,dtype", [
+    (60, 4, 100, 264, torch.bfloat16), (33, 3, 40, 136, torch.float32), (20, 12, 130, 2064, torch.bfloat16),
+    (5, 2, 0, 64, torch.bfloat16),  # an empty row buffer: every position is outside
+])
+def test_positions_outside_the_rows_are_dropped_slots(gq, T, k, rows, H, dtype):
+    pos = outside(rows, T, k, T)
+    live = (pos >= 0) & (pos < rows)
+    plain = torch.where(live, pos, -1)
+    y, g, w = randn(3, rows, H, dtype=dtype), randn(4, T, H, dtype=dtype), torch.rand(T, k, device=DEV)
+    out = gq.combine(y, pos, w)
+    assert torch.equal(out, gq.combine(y, plain, w))
+    assert (out[~live.any(1)] == 0).all()
+    dy, dw = gq.combine_backward(g, y, pos, w, dy=torch.full_like(y, 7.0))
+    dy2, dw2 = gq.combine_backward(g, y, plain, w, dy=torch.full_like(y, 7.0))
+    assert torch.equal(dy, dy2) and torch.equal(dw, dw2)
+    assert (dw[~live] == 0).all()
+    t, j = live.nonzero(as_tuple=True)
+    if H % 16 == 0:
+        q = torch.full((rows, H), 0x5A, dtype=torch.uint8, device=DEV)
+        s = torch.full((rows, -(-H // 128)), -3.0, device=DEV)
+        gq.dispatch_block(g, pos, out=q, scales=s)
+        want_q, want_s = gq.block_rows(g)
+        at = pos[t, j].long()
+        assert torch.equal(q[at], want_q.view(torch.uint8)[t]) and torch.equal(s[at], want_s[t])
+        named = torch.zeros(rows, dtype=torch.bool, device=DEV)
+        named[at] = True
+        assert (q[~named] == 0x5A).all() and (s[~named] == -3.0).all()
+
+
 # ----------------------------------------------------- non-finite values --
 
 def holes(seed, R, K):
@@ -106,6 +146,109 @@ def test_block_scales_do_not_count_nan(gq, form, dtype):
         q, wq = q.view(torch.uint8).reshape(R, K), want_q.view(torch.uint8).reshape(R, K)
         assert ((q[at] & 0x7F) == 0x7F).all()
         assert torch.equal(q[~at], wq[~at])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_infinities_stay_in_their_block(gq, dtype):
+    """An infinite row leaves the other rows of a 1x128 quantization as they
+    are, an infinite element the other tiles of a matrix."""
+    R, K = 200, 400
+    x = randn(7, R, K, dtype=dtype)
+    want_q, want_s = gq.block_rows(x)
+    bad = x.clone()
+    bad[3], bad[150, 200] = INF, -INF
+    q, s = gq.block_rows(bad)
+    keep = torch.ones(R, 4, dtype=torch.bool, device=DEV)
+    keep[3], keep[150, 1] = False, False
+    assert torch.equal(s[keep], want_s[keep])
+    cols = keep.repeat_interleave(128, 1)[:, :K]
+    assert torch.equal(q.view(torch.uint8)[cols], want_q.view(torch.uint8)[cols])
+    tq, ts = gq.block_tiles(x[None])
+    bq, bs = gq.block_tiles(torch.where(torch.arange(R * K, device=DEV).view(R, K) == 150 * K + 200, INF, x)[None].to(dtype))
+    tile = torch.zeros(2, 4, dtype=torch.bool, device=DEV)
+    tile[1, 1] = True
+    assert torch.equal(bs[0][~tile], ts[0][~tile])
+    cols = tile.repeat_interleave(128, 0)[:R].repeat_interleave(128, 1)[:, :K]
+    assert torch.equal(bq[0].view(torch.uint8)[~cols], tq[0].view(torch.uint8)[~cols])
+
+
+@pytest.mark.parametrize("value", [INF, -INF, NAN])
+def test_combine_keeps_non_finite_values_in_their_token(gq, value):
+    """Behind the last group, in the weight of a dropped slot and in another
+    token's rows they count for nothing."""
+    T, k, H = 70, 4, 264
+    order = gq.sort_tokens(draw_ids(8, T, k, 8, 5), 5)
+    y, g, w = randn(9, T * k, H), randn(10, T, H), torch.rand(T, k, device=DEV)
+    dead = order.pos < 0
+    want = gq.combine(y, order.pos, w)
+    want_dy, want_dw = gq.combine_backward(g, y, order.pos, w, dy=torch.zeros_like(y))
+    t = int((~dead).sum(1).argmax())
+    r = order.pos[t][~dead[t]][0].long()
+    y[int(order.offs[-1]):] = value
+    y[r] = value
+    w = torch.where(dead, value, w)
+    out = gq.combine(y, order.pos, w)
+    dy, dw = gq.combine_backward(g, y, order.pos, w, dy=torch.zeros_like(y))
+    others = torch.arange(T, device=DEV) != t
+    assert torch.equal(out[others], want[others]) and torch.equal(dw[others], want_dw[others])
+    assert not out[t].isfinite().any()
+    assert torch.equal(dy, want_dy)  # dy does not read y
+
+
+@pytest.mark.parametrize("rows", [20, 200])  # either kernel
+@pytest.mark.parametrize("transposed", [False, True])
+def test_grouped_mm_keeps_infinities_in_their_group(gq, rows, transposed):
+    """Infinities in one expert's weights, in one group's rows and behind the
+    last group, quantized as they come, reach no other group's results."""
+    N, K, E = 272, 400, 4
+    M = rows * E + 5
+    inner = N if transposed else K
+    x, w = randn(11, M, inner), randn(12, E, N, K)
+    o = torch.arange(rows, rows * E + 1, rows, dtype=torch.int32, device=DEV)
+    want = gq.grouped_mm(*gq.block_rows(x), *gq.block_tiles(w), o, transpose_b=transposed)
+    w[1, ::7] = INF
+    x[2 * rows:3 * rows, 5] = -INF
+    x[E * rows:] = INF
+    got = gq.grouped_mm(*gq.block_rows(x), *gq.block_tiles(w), o, transpose_b=transposed)
+    gq.check_device_error()
+    for g in range(E):
+        at = slice(g * rows, (g + 1) * rows)
+        if g in (1, 2):
+            assert not got[at].isfinite().any()
+        else:
+            assert torch.equal(got[at], want[at]), g
+
+
+# ------------------------------------------------------------ large sizes --
+
+@pytest.mark.parametrize("M,E,outer,inner", [(530_000, 3, 4096, 128), (40_000, 1024, 65_536, 16)])  # either kernel
+@pytest.mark.parametrize("transposed", [False, True])
+def test_grouped_mm_outputs_past_2_31_elements(gq, M, E, outer, inner, transposed):
+    """Entries -2 .. 2 of which one in five is not zero, with unit scales: the
+    results are integers below 256, which bf16 holds, and the test is exact."""
+    gen = torch.Generator(device=DEV).manual_seed(M)
+
+    def fp8(*shape):
+        v = torch.randint(-2, 3, shape, device=DEV, generator=gen, dtype=torch.int8)
+        keep = torch.randint(0, 4, shape, device=DEV, generator=gen, dtype=torch.int8) == 0
+        return (v * keep).to(torch.float8_e4m3fn)
+
+    qa, w = fp8(M, inner), fp8(E, *((inner, outer) if transposed else (outer, inner)))
+    sb = torch.ones(E, -(-w.shape[1] // 128), -(-w.shape[2] // 128), device=DEV)
+    offs = torch.randint(0, M + 1, (E,), device=DEV, generator=gen).sort().values.to(torch.int32)
+    offs[-1] = M
+    out = gq.grouped_mm(qa, torch.ones(M, 1, device=DEV), w, sb, offs, transpose_b=transposed)
+    gq.check_device_error()
+    assert out.numel() > 2 ** 31
+    start = 0
+    for e, end in enumerate(offs.tolist()):
+        for at in range(start, end, 50_000):
+            rows = slice(at, min(end, at + 50_000))
+            m = w[e].float()
+            want = qa[rows].float() @ (m if transposed else m.t())
+            assert want.abs().max() < 256
+            assert torch.equal(out[rows].float(), want), e
+        start = end
 
 
 # ---------------------------------------------------------------- streams --
