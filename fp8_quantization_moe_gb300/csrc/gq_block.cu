@@ -172,7 +172,6 @@ struct TileParams {
   const uint8_t* w;
   uint8_t* q;
   float* scales;
-  int64_t tiles;
   int32_t N, K, nn, nk;  // sizes of one matrix, tiles along each
   bool pow2;
 };
@@ -263,9 +262,9 @@ gq_status launch_tiles(const void* w, bool f32, int64_t E, int64_t N, int64_t K,
   p.nn = static_cast<int32_t>((N + kBlock - 1) / kBlock);
   p.nk = static_cast<int32_t>((K + kBlock - 1) / kBlock);
   p.pow2 = pow2;
-  p.tiles = E * p.nn * p.nk;  // the caller keeps it below 2^31
+  const int64_t tiles = E * p.nn * p.nk;  // the caller keeps it below 2^31
   return launch_chained("block_tiles: launch", f32 ? tiles_kernel<true> : tiles_kernel<false>,
-                        dim3(static_cast<unsigned>(p.tiles)), kThreads, 0, stream, 1, p);
+                        dim3(static_cast<unsigned>(tiles)), kThreads, 0, stream, 1, p);
 }
 
 }  // namespace block

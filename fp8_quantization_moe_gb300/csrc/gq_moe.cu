@@ -263,7 +263,7 @@ struct DispatchParams {
   const uint8_t* x;
   uint8_t* out;
   const int32_t* pos;
-  int64_t tokens, out_rows, ld_bytes;
+  int64_t out_rows, ld_bytes;
   int32_t chunks;  // 16-byte chunks per row
   int32_t span;    // chunks of a block
   int32_t top_k;
@@ -347,7 +347,7 @@ struct CombineParams {
   const float* weights;  // or nullptr: ones (forward)
   uint4* out;            // forward: (tokens, H); backward: dy (rows, H)
   float* dweights;       // backward
-  int64_t tokens, rows;
+  int64_t rows;
   int32_t chunks, span, top_k;
 };
 
@@ -525,7 +525,6 @@ gq_status launch_dispatch(const void* x, int64_t tokens, int64_t row_bytes, int6
   p.x = static_cast<const uint8_t*>(x);
   p.out = static_cast<uint8_t*>(out);
   p.pos = pos;
-  p.tokens = tokens;
   p.out_rows = out_rows;
   p.ld_bytes = ld_bytes;
   p.chunks = static_cast<int32_t>(row_bytes / 16);
@@ -544,7 +543,6 @@ gq_status launch_combine(const void* y, bool f32, int64_t rows, int64_t H, const
   p.pos = pos;
   p.weights = weights;
   p.out = static_cast<uint4*>(out);
-  p.tokens = tokens;
   p.rows = rows;
   p.chunks = static_cast<int32_t>(H / (f32 ? 4 : 8));
   p.top_k = top_k;
@@ -567,7 +565,6 @@ gq_status launch_combine_backward(const void* g, const void* y, bool f32, int64_
   p.weights = weights;
   p.out = static_cast<uint4*>(dy);
   p.dweights = dweights;
-  p.tokens = tokens;
   p.rows = rows;
   p.chunks = static_cast<int32_t>(H / (f32 ? 4 : 8));
   p.top_k = top_k;
