@@ -107,7 +107,8 @@ struct RowParams {
 // several) per warp; a block's values and its token's positions are loaded at
 // the same time.  A token is read once and its quantized block stored to each
 // of its sorted rows.  65,536 x 4096 bf16: 115 us, 7.1 TB/s; to one sorted row
-// each 120 us; 32,768 x 4096 to six rows each 164 us, 6.7 TB/s.  Issue slots
+// each 120 us; 32,768 x 4096 to six rows each 164 us, 6.7 TB/s; 32,768 x 4096 fp32
+// 95 us, 7.1 TB/s.  Issue slots
 // are the next limit: with a division for the row and 64-bit positions 126, 146
 // and 163 us.  (Two blocks per lane group and positions before values, to skip
 // tokens without a live slot, were slower.)

@@ -17,17 +17,20 @@
 // need every row's factor, and those loads alone -- shared memory returns 128
 // bytes a cycle -- would cost as much as the MMAs.
 //
-// What bounds it: with two accumulators, all of TMEM, the MMAs wait for the
-// epilogue.  A 128-block takes 860 cycles, 512 of them MMAs; without the
-// epilogue's multiply-adds (half of the FMA pipe's time at the tensor cores'
-// full rate) it would take 720, without the stores 780: a tile's 64 KB leave
-// the SM at 32 bytes a cycle, and for those 2000 cycles the MMAs run ahead by
-// two 128-blocks at most.  16,640 rows of 16 groups, K 4096 to N 8192: 460 us,
-// 2.43 PFLOP/s; transposed, 32,768 rows of 64 groups, N 2048 to K 4096: 265 us,
-// 2.07 PFLOP/s (in a long run the power limit lowers the clock: the first takes
-// 515 to 540 us).  Blocks in pairs that share the weights' loads
-// (cta_group::2) release accumulators across blocks and pad the groups to 256
-// rows: 505 and 316 us.
+// What bounds it: the tensor cores work for 512 of a 128-block's 860 cycles.
+// With two accumulators, all of TMEM, the MMAs wait for the epilogue: without
+// its multiply-adds (half of the FMA pipe's time at the tensor cores' full
+// rate) a 128-block would take 720 cycles, without the stores 780: a tile's 64
+// KB leave the SM at 32 bytes a cycle, and for those 2000 cycles the MMAs run
+// ahead by two 128-blocks at most.  Without multiply-adds and TMEM loads 700 are
+// left, 188 above the MMAs; what of that the stores do not explain is not known.
+// 16,640 rows of 16 groups, K 4096 to N 8192: 460 us, 2.43 PFLOP/s; transposed,
+// 32,768 rows of 64 groups, N 2048 to K 4096: 265 us, 2.07 PFLOP/s; in a long
+// run, at the power limit's clock, 515 to 540 and 295 to 311 us.  Blocks in pairs
+// that share the weights' loads (cta_group::2) release accumulators across
+// blocks and pad the groups to 256 rows: 505 and 316 us when this kernel took
+// 485 and 284 (long runs 536 and 330 against 528 and 304); they were not
+// measured with what has made it faster since.
 //
 // One persistent block per SM; its warps:
 //   0-7   epilogue: lane quarter w % 4 (32 rows), column half w / 4;
@@ -460,11 +463,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Up to this many rows per group on average the kernel for few rows is ahead,
-// whose narrower tiles spread the weights more evenly: in us, few / this,
-// 64 experts of 2048 x 2048: 43 / 50 at 32 rows each, 45 / 51 at 48, 54 / 54 at
-// 96; 16 of 4096 x 4096: 45 / 47 at 16, 50 / 49 at 48, 54 / 51 at 96; 8 of
-// 8192 x 2048: 25 / 27 at 32, 28 / 28 at 48, 32 / 29 at 96.
+// Up to this many rows per group on average the kernel for few rows is ahead
+// or close, whose narrower tiles spread the weights more evenly: in us, few /
+// this, forward and transposed, at 16, 32, 48 and 96 rows each
+//   64 experts of 2048 x 2048   43/49 44/50 47/51 54/54   43/47 44/48 46/49 54/52
+//   16 of 4096 x 4096           48/49 50/50 52/50 56/52   46/44 47/45 49/46 54/47
+//   8 of 8192 x 2048            25/27 26/27 28/28 33/29   22/31 23/32 25/32 28/33
+//   8 of 2048 x 8192            22/32 23/33 25/34 28/34   25/26 26/26 28/27 33/28
+// The rows are those of the buffer, also behind the last group's end.
 constexpr int kFewRows = 48;
 
 }  // namespace

@@ -390,8 +390,9 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const CombineParams p
 // products are summed together: in a thread over its chunks, then over the
 // warp by halving (a lane keeps half of its values in each step, so eight
 // values take nine exchanges), then over the warps.  8192 tokens of 8 KB, 8
-// rows each: 174 us, 6.6 TB/s, with three thread blocks per SM; 183 with the
-// two that its registers would allow, 189 with four, which spill.
+// rows each: 174 us, 6.6 TB/s, with three thread blocks per SM, for which a
+// thread spills 28 bytes; 183 with the two that its registers would allow, 189
+// with four (128 bytes).
 template <bool kF32, int kB>
 __global__ void __launch_bounds__(kThreads, kB == kBatch ? 3 : 0) combine_backward_kernel(const CombineParams p) {
   using C = Chunk<kF32>;
@@ -497,7 +498,9 @@ gq_status launch_sort(const DeviceInfo& info, const void* ids, bool i64, int64_t
   p.bits = 0;
   while ((1 << p.bits) < experts) ++p.bits;
   // exact for slots below 2^31: with 2^l the power of two at or above top_k,
-  // magic = ceil(2^(31 + l) / top_k) <= 2^32 - 1 errs by less than 2^-31 / slot
+  // magic = ceil(2^(31 + l) / top_k) <= 2^32 - 1 exceeds the quotient by less
+  // than 1, so slot * magic / 2^(31 + l) exceeds slot / top_k by less than
+  // 2^-l <= 1 / top_k: the whole part is the same
   int l = 0;
   while ((int64_t(1) << l) < top_k) ++l;
   p.shift = 31 + l;

@@ -385,7 +385,7 @@ gq_status gq_moe_combine_backward(const void* g, const void* y, int dtype, int64
  *
  *   x        bf16 or fp32 (dtype) [rows, K], rows ld elements apart, 16-byte
  *            aligned, a row pitch multiple of 16 bytes.           (input)
- *   K        K % 16 == 0, K <= 2^22.
+ *   rows, K  K % 16 == 0, K <= 2^22; rows * ceil(K / 128) < 2^31.
  *   pos, top_k, out_rows   int32 [rows, top_k] or NULL (top_k and out_rows
  *            are then ignored).                                   (input)
  *   out      e4m3 bytes [out_rows or rows, K], 16-byte aligned.   (output)
