@@ -154,18 +154,23 @@ def _stream_handle(stream, device):
     return s.cuda_stream
 
 
-def _empty(shape, dtype, device, stream):
-    """Memory for an output of a call on ``stream`` (None: the current
-    stream), from that stream's pool: the allocator hands out what was freed
-    on a stream in that stream's order only, so the current stream may still
-    be at work on what its own pool gives, and a temporary that is dropped
-    after the call has to wait for ``stream``."""
-    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _empty_on(stream, index: int):
+    """torch.empty for the outputs of a call on ``stream``, with memory from
+    that stream's pool: the allocator hands out what was freed on a stream in
+    that stream's order only, so the current stream may still be at work on
+    what its own pool gives, and a temporary that is dropped after the call
+    has to wait for ``stream``.  (Without a stream the calls use torch.empty
+    itself: a function in between costs them some tenths of a microsecond.)"""
+    if stream.cuda_stream == torch._C._cuda_getCurrentRawStream(index):
+        return torch.empty
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream.cuda_stream, device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, torch.device("cuda", index))
+
+    def empty(*args, **kwargs):
+        with torch.cuda.stream(stream):
+            return torch.empty(*args, **kwargs)
+
+    return empty
 
 
 def _ws_ptr(buf):
@@ -209,10 +214,11 @@ def colwise(x: torch.Tensor, offs: torch.Tensor, *, out=None, scales=None,
     M, K = x.shape
     G = offs.numel()
     dev = x.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     if out is None:
-        out = _empty((M, K), torch.float8_e4m3fn, dev, stream)
+        out = empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
     if scales is None:
-        scales = _empty((G, K), torch.float32, dev, stream)
+        scales = empty((G, K), dtype=torch.float32, device=dev)
     if out.shape != (M, K) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("colwise: out must be a contiguous 1-byte (M, K) tensor")
     if scales.shape != (G, K) or scales.dtype != torch.float32 or not scales.is_contiguous():
@@ -246,10 +252,11 @@ def rowwise_t(a: torch.Tensor, offs: torch.Tensor, *, out=None, scales=None,
     N, Mg = a.shape
     G = offs.numel()
     dev = a.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     if out is None:
-        out = _empty((Mg, N), torch.float8_e4m3fn, dev, stream)
+        out = empty((Mg, N), dtype=torch.float8_e4m3fn, device=dev)
     if scales is None:
-        scales = _empty((N, G), torch.float32, dev, stream)
+        scales = empty((N, G), dtype=torch.float32, device=dev)
     if out.shape != (Mg, N) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("rowwise_t: out must be a contiguous 1-byte (Mg, N) tensor")
     if scales.shape != (N, G) or scales.dtype != torch.float32 or not scales.is_contiguous():
@@ -280,10 +287,11 @@ def expert_dim1(w: torch.Tensor, *, out=None, scales=None, stream=None, workspac
         raise ValueError("expert_dim1: w must be a contiguous 3-D bf16 CUDA tensor")
     E, K, N = w.shape
     dev = w.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     if out is None:
-        out = _empty((E, K, N), torch.float8_e4m3fn, dev, stream)
+        out = empty((E, K, N), dtype=torch.float8_e4m3fn, device=dev)
     if scales is None:
-        scales = _empty((E, N), torch.float32, dev, stream)
+        scales = empty((E, N), dtype=torch.float32, device=dev)
     if out.shape != (E, K, N) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("expert_dim1: out must be a contiguous 1-byte (E, K, N) tensor")
     if scales.shape != (E, N) or scales.dtype != torch.float32 or not scales.is_contiguous():
@@ -314,10 +322,11 @@ def expert_rowwise(w: torch.Tensor, *, out=None, scales=None, stream=None,
         raise ValueError("expert_rowwise: w must be a contiguous 3-D bf16 CUDA tensor")
     E, N, K = w.shape
     dev = w.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     if out is None:
-        out = _empty((E, N, K), torch.float8_e4m3fn, dev, stream)
+        out = empty((E, N, K), dtype=torch.float8_e4m3fn, device=dev)
     if scales is None:
-        scales = _empty((E, N), torch.float32, dev, stream)
+        scales = empty((E, N), dtype=torch.float32, device=dev)
     if out.shape != (E, N, K) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("expert_rowwise: out must be a contiguous 1-byte (E, N, K) tensor")
     if scales.shape != (E, N) or scales.dtype != torch.float32 or not scales.is_contiguous():
@@ -343,10 +352,11 @@ def mxfp8_dim0(x: torch.Tensor, mode: str = "floor", *, out=None, scales=None, s
         raise ValueError("mxfp8_dim0: mode must be 'floor' or 'rceil'")
     M, K = x.shape
     dev = x.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     if out is None:
-        out = _empty((M, K), torch.float8_e4m3fn, dev, stream)
+        out = empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
     if scales is None:
-        scales = _empty((M, K // 32), torch.uint8, dev, stream)
+        scales = empty((M, K // 32), dtype=torch.uint8, device=dev)
     if out.shape != (M, K) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("mxfp8_dim0: out must be a contiguous 1-byte (M, K) tensor")
     if scales.shape != (M, K // 32) or scales.element_size() != 1 or not scales.is_contiguous():
@@ -381,8 +391,9 @@ def grouped_wgrad(qa_t: torch.Tensor, sa: torch.Tensor, qx: torch.Tensor, sx: to
                 and t.is_contiguous()):
             raise ValueError(f"grouped_wgrad: {name} must be a contiguous float32 {shape} CUDA tensor")
     dev = qa_t.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     if out is None:
-        out = _empty((G, N, K), torch.bfloat16, dev, stream)
+        out = empty((G, N, K), dtype=torch.bfloat16, device=dev)
     if out.shape != (G, N, K) or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("grouped_wgrad: out must be a contiguous bf16 (G, N, K) tensor")
     sh = _stream_handle(stream, dev)
@@ -405,10 +416,11 @@ def colwise_noalloc(x: torch.Tensor, offs: torch.Tensor, *, out=None,
     M, K = x.shape
     G = offs.numel()
     dev = x.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     if out is None:
-        out = _empty((M, K), torch.float8_e4m3fn, dev, stream)
+        out = empty((M, K), dtype=torch.float8_e4m3fn, device=dev)
     if scales is None:
-        scales = _empty((G, K), torch.float32, dev, stream)
+        scales = empty((G, K), dtype=torch.float32, device=dev)
     if out.shape != (M, K) or out.element_size() != 1 or not out.is_contiguous():
         raise ValueError("colwise_noalloc: out must be a contiguous 1-byte (M, K) tensor")
     if scales.shape != (G, K) or scales.dtype != torch.float32 or not scales.is_contiguous():

@@ -21,7 +21,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._binding import GQ_DTYPE_BF16, GQ_DTYPE_F32, GQ_SCALE_POW2, _check, _empty, lib
+from ._binding import GQ_DTYPE_BF16, GQ_DTYPE_F32, GQ_SCALE_POW2, _check, _empty_on, lib
 
 BLOCK = 128
 _DTYPES = {torch.bfloat16: GQ_DTYPE_BF16, torch.float32: GQ_DTYPE_F32}
@@ -41,11 +41,9 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
-def _count(n: int) -> int:
-    """n as a 32-bit argument of the library.  What does not fit is passed as
-    the largest, which it refuses, and not cut to its lower half."""
-    return n if n < 1 << 31 else (1 << 31) - 1
-
+# The largest count of the library's 32-bit arguments, which it refuses: passed
+# for every larger one, which ctypes would cut to its lower half.
+_MOST = (1 << 31) - 1
 
 # A call on small sizes is as long as its host side: the current stream and
 # device are asked for directly (0.1 us each; torch.cuda.current_stream takes
@@ -115,11 +113,13 @@ def sort_tokens(ids: torch.Tensor, n_experts: int, *, stream=None) -> TokenOrder
     _need(ids, "sort_tokens: ids", 2, _INT)
     T, k = ids.shape
     dev = ids.device
-    offs = _empty(n_experts if n_experts > 0 else 0, torch.int32, dev, stream)
-    pos = _empty((T, k), torch.int32, dev, stream)
-    token = _empty(T * k, torch.int32, dev, stream)
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
+    offs = empty(n_experts if n_experts > 0 else 0, dtype=torch.int32, device=dev)
+    pos = empty((T, k), dtype=torch.int32, device=dev)
+    token = empty(T * k, dtype=torch.int32, device=dev)
     _call("gq_moe_sort", dev.index, stream, lib().gq_moe_sort, ids.data_ptr(), ids.element_size(),
-          T, _count(k), _count(n_experts), offs.data_ptr(), pos.data_ptr(), token.data_ptr())
+          T, k if k < _MOST else _MOST, n_experts if n_experts < _MOST else _MOST,
+          offs.data_ptr(), pos.data_ptr(), token.data_ptr())
     return TokenOrder(offs, pos, token)
 
 
@@ -137,20 +137,21 @@ def dispatch(x: torch.Tensor, pos: torch.Tensor, *, out=None, stream=None) -> to
         raise ValueError("dispatch: x must be a 2-D CUDA tensor")
     T, H = x.shape
     dev = x.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     pitch = _pitch(x, "dispatch: x")
     _need(pos, "dispatch: pos", 2, _I32, dev.index)
     if pos.shape[0] != T:
         raise ValueError("dispatch: pos must have a row for each row of x")
     k = pos.shape[1]
     if out is None:
-        out = _empty((T * k, H), x.dtype, dev, stream)
+        out = empty((T * k, H), dtype=x.dtype, device=dev)
     else:
         _need(out, "dispatch: out", 2, (x.dtype,), dev.index)
         if out.shape[1] != H:
             raise ValueError(f"dispatch: out must have rows of {H} columns")
     size = x.element_size()
     _call("gq_moe_dispatch", dev.index, stream, lib().gq_moe_dispatch, x.data_ptr(), T, H * size,
-          pitch * size, pos.data_ptr(), _count(k), out.shape[0], out.data_ptr())
+          pitch * size, pos.data_ptr(), k if k < _MOST else _MOST, out.shape[0], out.data_ptr())
     return out
 
 
@@ -158,6 +159,7 @@ def _block_rows(name, x, pos, out, scales, pow2_scales, stream):
     _need(x, name + ": x", 2, _FLOAT, contiguous=False)
     T, K = x.shape
     dev = x.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     index = dev.index
     pitch = _pitch(x, name + ": x")
     k, rows, to = 1, T, None
@@ -174,15 +176,15 @@ def _block_rows(name, x, pos, out, scales, pow2_scales, stream):
             _need(out, name + ": out", 2, _FP8, index)
             rows = out.shape[0]
     if out is None:
-        out = _empty((rows, K), torch.float8_e4m3fn, dev, stream)
+        out = empty((rows, K), dtype=torch.float8_e4m3fn, device=dev)
     else:
         _need(out, name + ": out", 2, _FP8, index, (rows, K))
     if scales is None:
-        scales = _empty((rows, _blocks(K)), torch.float32, dev, stream)
+        scales = empty((rows, _blocks(K)), dtype=torch.float32, device=dev)
     else:
         _need(scales, name + ": scales", 2, _F32, index, (rows, _blocks(K)))
     _call("gq_fp8_block_rows", index, stream, lib().gq_fp8_block_rows, x.data_ptr(),
-          _DTYPES[x.dtype], T, K, pitch, to, _count(k), rows,
+          _DTYPES[x.dtype], T, K, pitch, to, k if k < _MOST else _MOST, rows,
           out.data_ptr(), scales.data_ptr(), GQ_SCALE_POW2 if pow2_scales else 0)
     return out, scales
 
@@ -213,12 +215,13 @@ def block_tiles(w: torch.Tensor, *, out=None, scales=None, pow2_scales: bool = F
     _need(w, "block_tiles: w", 3, _FLOAT)
     E, N, K = w.shape
     dev = w.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     if out is None:
-        out = _empty((E, N, K), torch.float8_e4m3fn, dev, stream)
+        out = empty((E, N, K), dtype=torch.float8_e4m3fn, device=dev)
     else:
         _need(out, "block_tiles: out", 3, _FP8, dev.index, (E, N, K))
     if scales is None:
-        scales = _empty((E, _blocks(N), _blocks(K)), torch.float32, dev, stream)
+        scales = empty((E, _blocks(N), _blocks(K)), dtype=torch.float32, device=dev)
     else:
         _need(scales, "block_tiles: scales", 3, _F32, dev.index, (E, _blocks(N), _blocks(K)))
     _call("gq_fp8_block_tiles", dev.index, stream, lib().gq_fp8_block_tiles, w.data_ptr(),
@@ -243,6 +246,7 @@ def grouped_mm(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.T
     _need(qb, "grouped_mm: qb", 3, _FP8)
     E, N, K = qb.shape
     dev = qb.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     index = dev.index
     inner, outer = (N, K) if transpose_b else (K, N)
     _need(qa, "grouped_mm: qa", 2, _FP8, index)
@@ -253,7 +257,7 @@ def grouped_mm(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.T
     _need(sb, "grouped_mm: sb", 3, _F32, index, (E, _blocks(N), _blocks(K)))
     _need(offs, "grouped_mm: offs", 1, _I32, index, (E,))
     if out is None:
-        out = _empty((M, outer), torch.bfloat16, dev, stream)
+        out = empty((M, outer), dtype=torch.bfloat16, device=dev)
     else:
         _need(out, "grouped_mm: out", 2, (torch.bfloat16,), index, (M, outer))
     _call("gq_grouped_mm", index, stream, lib().gq_grouped_mm, qa.data_ptr(), sa.data_ptr(), M,
@@ -276,18 +280,19 @@ def combine(y: torch.Tensor, pos: torch.Tensor, weights: Optional[torch.Tensor] 
     _need(y, "combine: y", 2, _FLOAT)
     rows, H = y.shape
     dev = y.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     index = dev.index
     _need(pos, "combine: pos", 2, _I32, index)
     T, k = pos.shape
     if weights is not None:
         _need(weights, "combine: weights", 2, _F32, index, (T, k))
     if out is None:
-        out = _empty((T, H), y.dtype, dev, stream)
+        out = empty((T, H), dtype=y.dtype, device=dev)
     else:
         _need(out, "combine: out", 2, (y.dtype,), index, (T, H))
     _call("gq_moe_combine", index, stream, lib().gq_moe_combine, y.data_ptr(), _DTYPES[y.dtype],
-          rows, H, pos.data_ptr(), None if weights is None else weights.data_ptr(), T, _count(k),
-          out.data_ptr())
+          rows, H, pos.data_ptr(), None if weights is None else weights.data_ptr(), T,
+          k if k < _MOST else _MOST, out.data_ptr())
     return out
 
 
@@ -301,20 +306,21 @@ def combine_backward(g: torch.Tensor, y: torch.Tensor, pos: torch.Tensor, weight
     _need(y, "combine_backward: y", 2, _FLOAT)
     rows, H = y.shape
     dev = y.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
     index = dev.index
     _need(pos, "combine_backward: pos", 2, _I32, index)
     T, k = pos.shape
     _need(g, "combine_backward: g", 2, (y.dtype,), index, (T, H))
     _need(weights, "combine_backward: weights", 2, _F32, index, (T, k))
     if dy is None:
-        dy = _empty((rows, H), y.dtype, dev, stream)
+        dy = empty((rows, H), dtype=y.dtype, device=dev)
     else:
         _need(dy, "combine_backward: dy", 2, (y.dtype,), index, (rows, H))
     if dweights is None:
-        dweights = _empty((T, k), torch.float32, dev, stream)
+        dweights = empty((T, k), dtype=torch.float32, device=dev)
     else:
         _need(dweights, "combine_backward: dweights", 2, _F32, index, (T, k))
     _call("gq_moe_combine_backward", index, stream, lib().gq_moe_combine_backward, g.data_ptr(),
-          y.data_ptr(), _DTYPES[y.dtype], rows, H, pos.data_ptr(), weights.data_ptr(), T, _count(k),
-          dy.data_ptr(), dweights.data_ptr())
+          y.data_ptr(), _DTYPES[y.dtype], rows, H, pos.data_ptr(), weights.data_ptr(), T,
+          k if k < _MOST else _MOST, dy.data_ptr(), dweights.data_ptr())
     return dy, dweights
