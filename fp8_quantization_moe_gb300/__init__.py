@@ -17,7 +17,11 @@ Two paths, both in hand-written sm_103a CUDA kernels behind the C ABI of
 * ``sort_tokens``, ``dispatch``, ``dispatch_block``, ``combine``,
   ``combine_backward`` -- tokens into expert order and back, with gradients;
 * ``block_rows``, ``block_tiles``, ``grouped_mm`` -- one scale per block of
-  128, and the grouped product (forward and grad_input) of such operands.
+  128, and the grouped product (forward and grad_input) of such operands;
+* ``grouped_gated_mm``, ``gated_backward``, ``grouped_gated_grad`` -- the gated
+  feed-forward block of the experts and its backward pass;
+* ``grad_norm``, ``clip_grads`` -- the norm of a list of gradients, and the
+  gradients scaled to a largest norm.
 
 scale = 448 / max(amax, 1e-12) in IEEE fp32; q = saturating round-to-nearest-
 even e4m3 cast of fp32(x * scale); ``pow2_scales=True`` rounds every scale
@@ -32,13 +36,16 @@ from ._binding import (GQ_KIND_COLWISE, GQ_KIND_ROWWISE_T, GQ_MAX_GROUPS,
                        rowwise_t_host, set_lag, status_string, version,
                        workspace_bytes)
 from ._build import build
-from .moe import (TokenOrder, block_rows, block_tiles, combine, combine_backward, dispatch,
-                  dispatch_block, grouped_mm, sort_tokens)
+from .clip import clip_grads, grad_norm
+from .moe import (GatedRows, TokenOrder, block_rows, block_tiles, combine, combine_backward,
+                  dispatch, dispatch_block, gated_backward, grouped_gated_grad, grouped_gated_mm,
+                  grouped_mm, sort_tokens)
 
 __all__ = [
     "GQ_KIND_COLWISE", "GQ_KIND_ROWWISE_T", "GQ_MAX_GROUPS", "GQ_SCALE_POW2", "GQ_TWO_PHASE",
-    "GQ_WORKSPACE_ZEROED", "GQError", "TokenOrder",
-    "block_rows", "block_tiles", "combine", "combine_backward", "dispatch", "dispatch_block",
+    "GQ_WORKSPACE_ZEROED", "GQError", "GatedRows", "TokenOrder",
+    "block_rows", "block_tiles", "clip_grads", "combine", "combine_backward", "dispatch",
+    "dispatch_block", "gated_backward", "grad_norm", "grouped_gated_grad", "grouped_gated_mm",
     "grouped_mm", "sort_tokens",
     "build", "check_device_error", "colwise", "colwise_host",
     "colwise_noalloc", "debug_set", "expert_dim1", "expert_rowwise", "grouped_wgrad",

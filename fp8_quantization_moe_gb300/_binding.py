@@ -30,6 +30,8 @@ GQ_MX_FLOOR = 0
 GQ_MX_RCEIL = 1
 GQ_DTYPE_BF16 = 0
 GQ_DTYPE_F32 = 1
+GQ_ACT_SILU = 0
+GQ_ACT_GELU = 1
 
 # Every symbol the header declares, with its ctypes signature.
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
@@ -51,6 +53,12 @@ SIGNATURES = {
     "gq_fp8_block_rows": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _I32, _I64, _P, _P, ctypes.c_uint32, _P]),
     "gq_fp8_block_tiles": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, ctypes.c_uint32, _P]),
     "gq_grouped_mm": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, ctypes.c_int, _P, _I32, _P, _P]),
+    "gq_grouped_gated_mm": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, ctypes.c_int, _P, _I32, _P, _P, _P, _P, ctypes.c_uint32, _P]),
+    "gq_grouped_gated_grad": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _I32, _P, _P]),
+    "gq_gated_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_int, _P, _P, _P, ctypes.c_uint32, _P]),
+    "gq_grad_norm_workspace_bytes": (_SZ, [_I32]),
+    "gq_grad_norm": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _SZ, _P]),
+    "gq_clip_grads": (ctypes.c_int, [_P, _P, _P, _P, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "gq_check_device_error": (ctypes.c_int, [_P]),
     "gq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "gq_last_error": (ctypes.c_char_p, []),

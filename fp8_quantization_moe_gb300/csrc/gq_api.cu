@@ -275,6 +275,61 @@ gq_status validate_rows(int64_t rows, int64_t width, int bytes, const char* name
   return GQ_OK;
 }
 
+// Sizes of the gated block's products: both matrices of an expert are (N, K).
+gq_status validate_gated(int64_t M, int64_t N, int64_t K, int activation, int32_t n_groups,
+                         const char* name) {
+  if (M < 0 || N < 0 || K < 0)
+    return fail(GQ_ERR_INVALID_ARG, "%s: negative size (%lld, %lld, %lld)", name,
+                static_cast<long long>(M), static_cast<long long>(N), static_cast<long long>(K));
+  if (activation != GQ_ACT_SILU && activation != GQ_ACT_GELU)
+    return fail(GQ_ERR_INVALID_ARG, "%s: unknown activation %d", name, activation);
+  if (n_groups < 1)
+    return fail(GQ_ERR_INVALID_ARG, "%s: n_groups must be >= 1 (got %d)", name, n_groups);
+  if (n_groups > GQ_MAX_GROUPS)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: n_groups %d > %d", name, n_groups, GQ_MAX_GROUPS);
+  if (M > kMaxExtent || N > kMaxWidth || K > kMaxWidth || 2 * n_groups * N > kMaxExtent)
+    return fail(GQ_ERR_UNSUPPORTED,
+                "%s: 2^31 rows or more, or N or K above 2^22, or 2 * n_groups * N >= 2^31", name);
+  if (N % 16 != 0 || K % 16 != 0)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: N = %lld and K = %lld must be multiples of 16", name,
+                static_cast<long long>(N), static_cast<long long>(K));
+  return GQ_OK;
+}
+
+gq_status validate_operands(const void* qa, const float* sa, const void* qb, const float* sb,
+                            const char* name) {
+  if (qa == nullptr || sa == nullptr || qb == nullptr || sb == nullptr)
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL operand", name);
+  if (!aligned(qa, 16) || !aligned(qb, 16) || !aligned(sa, 4) || !aligned(sb, 4))
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: operands must be 16-byte aligned, scales 4-byte aligned", name);
+  return GQ_OK;
+}
+
+constexpr int32_t kMaxTensors = 1 << 20;
+constexpr int64_t kMaxElements = int64_t(1) << 42;  // of all tensors
+
+// A list of tensors, given by arrays on the host.
+gq_status validate_tensors(const void* const* tensors, const int64_t* sizes, const int32_t* dtypes,
+                           int32_t count, const char* name) {
+  if (count < 0) return fail(GQ_ERR_INVALID_ARG, "%s: %d tensors", name, count);
+  if (count > kMaxTensors)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: more than 2^20 tensors (%d)", name, count);
+  if (count > 0 && (tensors == nullptr || sizes == nullptr || dtypes == nullptr))
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL list", name);
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const int size = dtype_bytes(dtypes[i]);
+    if (size == 0 || sizes[i] < 0)
+      return fail(GQ_ERR_INVALID_ARG, "%s: tensor %d: unknown data type or negative size", name, i);
+    if (sizes[i] > kMaxElements || (total += sizes[i]) > kMaxElements)
+      return fail(GQ_ERR_UNSUPPORTED, "%s: more than 2^42 elements", name);
+    if (sizes[i] > 0 && (tensors[i] == nullptr || !aligned(tensors[i], size)))
+      return fail(GQ_ERR_INVALID_ARG, "%s: tensor %d: NULL or misaligned", name, i);
+  }
+  return GQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -712,6 +767,144 @@ gq_status gq_grouped_mm(const void* qa, const float* sa, int64_t M, const void* 
                      reinterpret_cast<cudaStream_t>(stream));
 }
 
+gq_status gq_grouped_gated_mm(const void* qa, const float* sa, int64_t M, const void* qb,
+                              const float* sb, int64_t N, int64_t K, int activation,
+                              const int32_t* offs, int32_t n_groups, void* out, void* q,
+                              float* scales, void* pre, uint32_t flags, gq_stream_t stream) {
+  const char* name = "gq_grouped_gated_mm";
+  if (flags & ~static_cast<uint32_t>(GQ_SCALE_POW2))
+    return fail(GQ_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name,
+                flags & ~static_cast<uint32_t>(GQ_SCALE_POW2));
+  gq_status st = validate_gated(M, N, K, activation, n_groups, name);
+  if (st != GQ_OK) return st;
+  if (M == 0 || N == 0) return GQ_OK;
+  if (offs == nullptr || (out == nullptr && q == nullptr) || (q != nullptr && scales == nullptr))
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(offs, 4) || !aligned(out, 16) || !aligned(q, 16) || !aligned(scales, 4) ||
+      !aligned(pre, 16))
+    return fail(GQ_ERR_INVALID_ARG, "%s: misaligned offsets or output", name);
+  if (K == 0) return fail(GQ_ERR_UNSUPPORTED, "%s: the contraction has no columns", name);
+  st = validate_operands(qa, sa, qb, sb, name);
+  if (st != GQ_OK) return st;
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return gated::launch_forward(*info, g_dbg, qa, sa, M, qb, sb, static_cast<int32_t>(N),
+                               static_cast<int32_t>(K), activation, offs, n_groups, out, q, scales,
+                               pre, (flags & GQ_SCALE_POW2) != 0,
+                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_grouped_gated_grad(const void* qd, const float* sd, int64_t M, const void* qb,
+                                const float* sb, int64_t N, int64_t K, const int32_t* offs,
+                                int32_t n_groups, void* out, gq_stream_t stream) {
+  const char* name = "gq_grouped_gated_grad";
+  gq_status st = validate_gated(M, N, K, GQ_ACT_SILU, n_groups, name);
+  if (st != GQ_OK) return st;
+  if (M == 0 || K == 0) return GQ_OK;
+  if (offs == nullptr || out == nullptr)
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(offs, 4) || !aligned(out, 16))
+    return fail(GQ_ERR_INVALID_ARG, "%s: misaligned offsets or output", name);
+  if (N == 0) return fail(GQ_ERR_UNSUPPORTED, "%s: the contraction has no columns", name);
+  st = validate_operands(qd, sd, qb, sb, name);
+  if (st != GQ_OK) return st;
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return gated::launch_grad(*info, g_dbg, qd, sd, M, qb, sb, static_cast<int32_t>(N),
+                            static_cast<int32_t>(K), offs, n_groups, out,
+                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_gated_backward(const void* g, const void* pre, int dtype, int64_t rows, int64_t N,
+                            int64_t ld, int activation, void* out, void* q, float* scales,
+                            uint32_t flags, gq_stream_t stream) {
+  const char* name = "gq_gated_backward";
+  if (flags & ~static_cast<uint32_t>(GQ_SCALE_POW2))
+    return fail(GQ_ERR_INVALID_ARG, "%s: unknown flags 0x%x", name,
+                flags & ~static_cast<uint32_t>(GQ_SCALE_POW2));
+  const int size = dtype_bytes(dtype);
+  gq_status st = validate_rows(rows, N, size, name);
+  if (st != GQ_OK) return st;
+  if (activation != GQ_ACT_SILU && activation != GQ_ACT_GELU)
+    return fail(GQ_ERR_INVALID_ARG, "%s: unknown activation %d", name, activation);
+  if (N % 16 != 0)
+    return fail(GQ_ERR_UNSUPPORTED, "%s: N = %lld is not a multiple of 16", name,
+                static_cast<long long>(N));
+  if (ld < N || ld > kMaxExtent || ld * size % 16 != 0)
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: row pitch %lld below N = %lld or not a multiple of 16 bytes", name,
+                static_cast<long long>(ld), static_cast<long long>(N));
+  if (rows == 0 || N == 0) return GQ_OK;
+  if (g == nullptr || pre == nullptr || (out == nullptr && q == nullptr) ||
+      (q != nullptr && scales == nullptr))
+    return fail(GQ_ERR_INVALID_ARG, "%s: NULL pointer", name);
+  if (!aligned(g, 16) || !aligned(pre, 16) || !aligned(out, 16) || !aligned(q, 16) ||
+      !aligned(scales, 4))
+    return fail(GQ_ERR_INVALID_ARG,
+                "%s: inputs and outputs must be 16-byte aligned, scales 4-byte aligned", name);
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return gated::launch_backward(g, pre, dtype == GQ_DTYPE_F32, rows, N, ld, activation, out, q,
+                                scales, (flags & GQ_SCALE_POW2) != 0,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t gq_grad_norm_workspace_bytes(int32_t count) {
+  return count < 1 || count > kMaxTensors ? 0 : clip::workspace_bytes(count);
+}
+
+gq_status gq_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes,
+                       int32_t count, float* norm, void* workspace, size_t workspace_bytes,
+                       gq_stream_t stream) {
+  const char* name = "gq_grad_norm";
+  gq_status st = validate_tensors(grads, sizes, dtypes, count, name);
+  if (st != GQ_OK) return st;
+  if (norm == nullptr || !aligned(norm, 4))
+    return fail(GQ_ERR_INVALID_ARG, "%s: norm NULL or misaligned", name);
+  st = validate_ws(workspace, workspace_bytes, gq_grad_norm_workspace_bytes(count), name);
+  if (st != GQ_OK) return st;
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return clip::launch(*info, grads, nullptr, false, sizes, dtypes, count, 0.0f, nullptr, workspace,
+                      norm, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gq_status gq_clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes,
+                        const int32_t* dtypes, int32_t count, float max_norm,
+                        const float* given_norm, float* norm, void* workspace,
+                        size_t workspace_bytes, gq_stream_t stream) {
+  const char* name = "gq_clip_grads";
+  gq_status st = validate_tensors(grads, sizes, dtypes, count, name);
+  if (st != GQ_OK) return st;
+  if (!(max_norm >= 0.0f))
+    return fail(GQ_ERR_INVALID_ARG, "%s: max_norm = %g", name, static_cast<double>(max_norm));
+  if (outs != nullptr) {
+    st = validate_tensors(const_cast<const void* const*>(outs), sizes, dtypes, count, name);
+    if (st != GQ_OK) return st;
+  }
+  if (given_norm != nullptr) {
+    if (!aligned(given_norm, 4))
+      return fail(GQ_ERR_INVALID_ARG, "%s: given_norm misaligned", name);
+    norm = nullptr;
+  } else {
+    if (norm == nullptr || !aligned(norm, 4))
+      return fail(GQ_ERR_INVALID_ARG, "%s: norm NULL or misaligned", name);
+    st = validate_ws(workspace, workspace_bytes, gq_grad_norm_workspace_bytes(count), name);
+    if (st != GQ_OK) return st;
+  }
+  st = clip::check_overlap(grads, outs, sizes, dtypes, count);
+  if (st != GQ_OK) return st;
+  const DeviceInfo* info = nullptr;
+  st = current_device(&info);
+  if (st != GQ_OK) return st;
+  return clip::launch(*info, grads, outs, true, sizes, dtypes, count, max_norm, given_norm,
+                      workspace, norm, reinterpret_cast<cudaStream_t>(stream));
+}
+
 gq_status gq_check_device_error(gq_stream_t stream) {
   const DeviceInfo* info = nullptr;
   gq_status st = current_device(&info);
@@ -751,7 +944,7 @@ const char* gq_status_string(gq_status status) {
 
 const char* gq_last_error(void) { return g_msg; }
 
-int gq_version(void) { return 300; }  // 0.3.0: moe_sort, dispatch, combine, block scaling, grouped_mm
+int gq_version(void) { return 400; }  // 0.4.0: gated feed-forward block, gradient norm and clipping
 
 gq_status gq_set_lag(int kind, int32_t lag) {
   if (kind != GQ_KIND_COLWISE && kind != GQ_KIND_ROWWISE_T)

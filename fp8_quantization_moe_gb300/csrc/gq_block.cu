@@ -25,19 +25,6 @@ constexpr int kUnit = 16;                    // columns per lane
 constexpr int kUnitsPerBlock = kBlock / kUnit;  // 8 lanes share a block
 constexpr int kThreads = 256;
 
-// Four e4m3 bytes from four fp32 values and one scale (see quant4).
-__device__ __forceinline__ uint32_t quant4f(float4 v, float s) {
-  uint32_t out;
-  asm("{\n\t.reg .b16 h0, h1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 h0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 h1, %4, %3;\n\t"
-      "mov.b32 %0, {h0, h1};\n\t}"
-      : "=r"(out)
-      : "f"(__fmul_rn(v.x, s)), "f"(__fmul_rn(v.y, s)), "f"(__fmul_rn(v.z, s)),
-        "f"(__fmul_rn(v.w, s)));
-  return out;
-}
-
 // Sixteen consecutive elements in registers.
 template <bool kF32>
 struct Unit;

@@ -407,6 +407,19 @@ __device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32_t w1, float s0,
   return out;
 }
 
+// Four e4m3 bytes from four fp32 values and one scale (see quant4).
+__device__ __forceinline__ uint32_t quant4f(float4 v, float s) {
+  uint32_t out;
+  asm("{\n\t.reg .b16 h0, h1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 h1, %4, %3;\n\t"
+      "mov.b32 %0, {h0, h1};\n\t}"
+      : "=r"(out)
+      : "f"(__fmul_rn(v.x, s)), "f"(__fmul_rn(v.y, s)), "f"(__fmul_rn(v.z, s)),
+        "f"(__fmul_rn(v.w, s)));
+  return out;
+}
+
 // Eight bf16 (one 16-byte chunk) times eight scales -> eight e4m3 bytes
 // (lowest column in the lowest byte).
 __device__ __forceinline__ uint2 quant8(uint4 v, const float* sc) {

@@ -158,6 +158,30 @@ gq_status launch(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa, 
                  const int32_t* offs, int32_t E, void* out, cudaStream_t stream);
 }  // namespace gmm
 
+namespace gated {
+gq_status launch_backward(const void* g, const void* pre, bool f32, int64_t rows, int64_t N,
+                          int64_t ld, int activation, void* out, void* q, float* scales, bool pow2,
+                          cudaStream_t stream);
+gq_status launch_forward(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa,
+                         const float* sa, int64_t M, const void* qb, const float* sb, int32_t N,
+                         int32_t K, int activation, const int32_t* offs, int32_t E, void* out,
+                         void* q, float* scales, void* pre, bool pow2, cudaStream_t stream);
+gq_status launch_grad(const DeviceInfo& info, const DebugKnobs& dbg, const void* qd,
+                      const float* sd, int64_t M, const void* qb, const float* sb, int32_t N,
+                      int32_t K, const int32_t* offs, int32_t E, void* out, cudaStream_t stream);
+}  // namespace gated
+
+namespace clip {
+size_t workspace_bytes(int32_t count);
+gq_status check_overlap(const void* const* in, void* const* out, const int64_t* sizes,
+                        const int32_t* dtypes, int32_t count);
+// The norm of the tensors, unless `given`, to `norm`, unless nullptr; with
+// `write` the tensors scaled to `most`, into `out` or in place.
+gq_status launch(const DeviceInfo& info, const void* const* in, void* const* out, bool write,
+                 const int64_t* sizes, const int32_t* dtypes, int32_t count, float most,
+                 const float* given, void* workspace, float* norm, cudaStream_t stream);
+}  // namespace clip
+
 // Writes the scale of an empty group -- 448 / 1e-12 (fp32), or its power
 // of two below with GQ_SCALE_POW2 -- into n scales: every group is empty
 // when the token extent is 0.

@@ -6,6 +6,10 @@
 * ``block_rows(x)``                  -- rows quantized per 1x128 block;
 * ``block_tiles(w)``                 -- stacked weights quantized per 128x128 block;
 * ``grouped_mm(qa, sa, qb, sb, offs)`` -- the grouped product of the two;
+* ``grouped_gated_mm(qa, sa, qb, sb, offs)`` -- both projections of a gated
+  feed-forward block, its activation and product;
+* ``gated_backward(g, pre)``         -- the gradients of the two projections;
+* ``grouped_gated_grad(qd, sd, qb, sb, offs)`` -- their grad_input;
 * ``combine(y, pos, weights)``       -- the weighted way back to the tokens;
 * ``combine_backward(g, y, pos, weights)`` -- its gradients.
 
@@ -21,7 +25,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._binding import GQ_DTYPE_BF16, GQ_DTYPE_F32, GQ_SCALE_POW2, _check, _empty_on, lib
+from ._binding import (GQ_ACT_GELU, GQ_ACT_SILU, GQ_DTYPE_BF16, GQ_DTYPE_F32, GQ_SCALE_POW2,
+                       _check, _empty_on, lib)
 
 BLOCK = 128
 _DTYPES = {torch.bfloat16: GQ_DTYPE_BF16, torch.float32: GQ_DTYPE_F32}
@@ -263,6 +268,156 @@ def grouped_mm(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.T
     _call("gq_grouped_mm", index, stream, lib().gq_grouped_mm, qa.data_ptr(), sa.data_ptr(), M,
           qb.data_ptr(), sb.data_ptr(), N, K, 1 if transpose_b else 0, offs.data_ptr(), E,
           out.data_ptr())
+    return out
+
+
+class GatedRows(NamedTuple):
+    """What the gated block's calls write: ``out`` rows unquantized, ``q``
+    e4m3 rows with float32 ``scales`` per 1x128 block, ``pre`` bf16 (M, 2, N),
+    the two projections; None for what was not asked for."""
+    out: Optional[torch.Tensor]
+    q: Optional[torch.Tensor]
+    scales: Optional[torch.Tensor]
+    pre: Optional[torch.Tensor]
+
+
+_ACTIVATIONS = {"silu": GQ_ACT_SILU, "gelu": GQ_ACT_GELU}
+_BF16 = (torch.bfloat16,)
+
+
+def _activation(name: str, activation: str) -> int:
+    code = _ACTIVATIONS.get(activation)
+    if code is None:
+        raise ValueError(f"{name}: activation must be 'silu' or 'gelu', not {activation!r}")
+    return code
+
+
+def _gated_outputs(name, shape, dtype, dev, plain, fp8, out, q, scales, empty):
+    """The buffers of a call's rows, allocated where they are asked for and not given."""
+    index = dev.index
+    if out is not None:
+        _need(out, name + ": out", len(shape), (dtype,), index, shape)
+    elif plain:
+        out = empty(shape, dtype=dtype, device=dev)
+    blocks = (*shape[:-1], _blocks(shape[-1]))
+    if q is not None:
+        _need(q, name + ": q", len(shape), _FP8, index, shape)
+    elif fp8 or scales is not None:
+        q = empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+    if scales is not None:
+        _need(scales, name + ": scales", len(shape), _F32, index, blocks)
+    elif q is not None:
+        scales = empty(blocks, dtype=torch.float32, device=dev)
+    if out is None and q is None:
+        raise ValueError(f"{name}: neither plain nor fp8 rows are asked for")
+    return out, q, scales
+
+
+def _gated_weights(name, qb, sb, offs):
+    _need(qb, name + ": qb", 4, _FP8)
+    E, two, N, K = qb.shape
+    if two != 2:
+        raise ValueError(f"{name}: qb must have two matrices per expert, not {two}")
+    index = qb.get_device()
+    _need(sb, name + ": sb", 4, _F32, index, (E, 2, _blocks(N), _blocks(K)))
+    _need(offs, name + ": offs", 1, _I32, index, (E,))
+    return E, N, K
+
+
+def grouped_gated_mm(qa: torch.Tensor, sa: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor,
+                     offs: torch.Tensor, *, activation: str = "silu", plain: bool = True,
+                     fp8: bool = False, keep: bool = False, out=None, q=None, scales=None,
+                     pre=None, pow2_scales: bool = False, stream=None) -> GatedRows:
+    """The gated feed-forward block of each expert: act(x) * u for the two
+    projections x = A @ W[g, 0].T and u = A @ W[g, 1].T of each group's rows.
+
+    qa e4m3 (M, K) with scales sa float32 (M, ceil(K / 128)) and offs int32
+    (E,) as in ``grouped_mm``; qb e4m3 (E, 2, N, K), gate before up, with
+    scales sb float32 (E, 2, ceil(N / 128), ceil(K / 128)): ``block_tiles`` of
+    the weights viewed as (2 * E, N, K).  activation: "silu", or "gelu" (its
+    tanh form).
+
+    Writes the bf16 rows (M, N) with ``plain`` or ``out``; the rows quantized
+    as ``block_rows`` does it, from fp32, with ``fp8``, ``q`` or ``scales``;
+    and both projections as bf16 (M, 2, N), for ``gated_backward``, with
+    ``keep`` or ``pre``.  ``plain=False, fp8=True`` is the form that the next
+    ``grouped_mm`` takes.  Rows behind the last end keep what the outputs
+    held.
+    """
+    name = "grouped_gated_mm"
+    E, N, K = _gated_weights(name, qb, sb, offs)
+    dev = qb.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
+    index = dev.index
+    act = _activation(name, activation)
+    _need(qa, name + ": qa", 2, _FP8, index)
+    M = qa.shape[0]
+    if qa.shape[1] != K:
+        raise ValueError(f"{name}: qa must have {K} columns, not {qa.shape[1]}")
+    _need(sa, name + ": sa", 2, _F32, index, (M, _blocks(K)))
+    out, q, scales = _gated_outputs(name, (M, N), torch.bfloat16, dev, plain, fp8, out, q, scales, empty)
+    if pre is not None:
+        _need(pre, name + ": pre", 3, _BF16, index, (M, 2, N))
+    elif keep:
+        pre = empty((M, 2, N), dtype=torch.bfloat16, device=dev)
+    _call("gq_grouped_gated_mm", index, stream, lib().gq_grouped_gated_mm, qa.data_ptr(),
+          sa.data_ptr(), M, qb.data_ptr(), sb.data_ptr(), N, K, act, offs.data_ptr(), E,
+          None if out is None else out.data_ptr(), None if q is None else q.data_ptr(),
+          None if q is None else scales.data_ptr(), None if pre is None else pre.data_ptr(),
+          GQ_SCALE_POW2 if pow2_scales else 0)
+    return GatedRows(out, q, scales, pre)
+
+
+def gated_backward(g: torch.Tensor, pre: torch.Tensor, *, activation: str = "silu",
+                   plain: bool = True, fp8: bool = False, out=None, q=None, scales=None,
+                   pow2_scales: bool = False, stream=None) -> GatedRows:
+    """The gradients of the two projections of ``grouped_gated_mm``: g (M, N),
+    possibly with a pitch, is the gradient of its rows, pre (M, 2, N) the
+    projections, both bf16 or both float32.  Returns GatedRows: out (M, 2, N)
+    of g's type (``plain`` or ``out``, which may be ``pre`` itself), q e4m3
+    (M, 2, N) and scales float32 (M, 2, ceil(N / 128)) for
+    ``grouped_gated_grad`` (``fp8``, ``q`` or ``scales``)."""
+    name = "gated_backward"
+    _need(g, name + ": g", 2, _FLOAT, contiguous=False)
+    M, N = g.shape
+    dev = g.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
+    pitch = _pitch(g, name + ": g")
+    act = _activation(name, activation)
+    _need(pre, name + ": pre", 3, (g.dtype,), dev.index, (M, 2, N))
+    out, q, scales = _gated_outputs(name, (M, 2, N), g.dtype, dev, plain, fp8, out, q, scales, empty)
+    _call("gq_gated_backward", dev.index, stream, lib().gq_gated_backward, g.data_ptr(),
+          pre.data_ptr(), _DTYPES[g.dtype], M, N, pitch, act,
+          None if out is None else out.data_ptr(), None if q is None else q.data_ptr(),
+          None if q is None else scales.data_ptr(), GQ_SCALE_POW2 if pow2_scales else 0)
+    return GatedRows(out, q, scales, None)
+
+
+def grouped_gated_grad(qd: torch.Tensor, sd: torch.Tensor, qb: torch.Tensor, sb: torch.Tensor,
+                       offs: torch.Tensor, *, out=None, stream=None) -> torch.Tensor:
+    """grad_input of ``grouped_gated_mm``: the sum of both projections'
+    products, D[:, 0] @ W[g, 0] + D[:, 1] @ W[g, 1] for the rows of each group.
+
+    qd e4m3 (M, 2, N) with scales sd float32 (M, 2, ceil(N / 128)) as
+    ``gated_backward`` gives them; qb, sb and offs as in ``grouped_gated_mm``.
+    Returns out bf16 (M, K).  Rows behind the last end keep ``out``.
+    """
+    name = "grouped_gated_grad"
+    E, N, K = _gated_weights(name, qb, sb, offs)
+    dev = qb.device
+    empty = torch.empty if stream is None else _empty_on(stream, dev.index)
+    index = dev.index
+    _need(qd, name + ": qd", 3, _FP8, index)
+    M = qd.shape[0]
+    if qd.shape[1:] != (2, N):
+        raise ValueError(f"{name}: qd must have shape {(M, 2, N)}, not {tuple(qd.shape)}")
+    _need(sd, name + ": sd", 3, _F32, index, (M, 2, _blocks(N)))
+    if out is None:
+        out = empty((M, K), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, name + ": out", 2, _BF16, index, (M, K))
+    _call("gq_grouped_gated_grad", index, stream, lib().gq_grouped_gated_grad, qd.data_ptr(),
+          sd.data_ptr(), M, qb.data_ptr(), sb.data_ptr(), N, K, offs.data_ptr(), E, out.data_ptr())
     return out
 
 

@@ -443,6 +443,128 @@ gq_status gq_grouped_mm(const void* qa, const float* sa, int64_t M, const void* 
                         int32_t n_groups, void* out, gq_stream_t stream);
 
 /*
+ * The gated feed-forward block of the experts.  Each expert has two matrices
+ * (N, K), stacked as [n_groups, 2, N, K]: the gate's and the up projection's.
+ * With A and W as in gq_grouped_mm, for every row m of group g
+ *     x[m][n] = sum over k of A[m][k] * W[g][0][n][k]
+ *     u[m][n] = sum over k of A[m][k] * W[g][1][n][k]
+ *     h[m][n] = act(x[m][n]) * u[m][n]
+ * x, u and h are formed in fp32 as in gq_grouped_mm; act(x) = x * sigma(z), sigma
+ * the logistic function, with
+ *     GQ_ACT_SILU   z = x
+ *     GQ_ACT_GELU   z = 2 sqrt(2 / pi) (x + 0.044715 x^3), the tanh form of gelu
+ * and act(x) = 0 where sigma has vanished (below about -88).
+ *
+ *   qa, sa, M, offs, n_groups   as in gq_grouped_mm.               (input)
+ *   qb       e4m3 [n_groups, 2, N, K], 16-byte aligned: the matrices as
+ *            gq_fp8_block_tiles quantizes 2 * n_groups of them.    (input)
+ *   sb       fp32 [n_groups, 2, ceil(N / 128), ceil(K / 128)].     (input)
+ *   M, N, K  M < 2^31; N and K multiples of 16, at most 2^22, K at least 16;
+ *            2 * n_groups * N < 2^31.
+ *   out      bf16 [M, N], 16-byte aligned, or NULL: h.            (output)
+ *   q, scales   e4m3 [M, N], 16-byte aligned, and fp32 [M, ceil(N / 128)], or
+ *            NULL: h quantized as gq_fp8_block_rows does it, from the fp32
+ *            values.  One of out and q is not NULL.               (output)
+ *   pre      bf16 [M, 2, N], 16-byte aligned, or NULL: x and u, for
+ *            gq_gated_backward.                                   (output)
+ *   flags    0 or GQ_SCALE_POW2.
+ *   stream   the CUDA stream to run on.  No workspace.
+ * Rows behind the last end are left untouched in every output.
+ */
+#define GQ_ACT_SILU 0
+#define GQ_ACT_GELU 1
+gq_status gq_grouped_gated_mm(const void* qa, const float* sa, int64_t M, const void* qb,
+                              const float* sb, int64_t N, int64_t K, int activation,
+                              const int32_t* offs, int32_t n_groups, void* out, void* q,
+                              float* scales, void* pre, uint32_t flags, gq_stream_t stream);
+
+/*
+ * The gradients of x and u from g, that of h:
+ *     dx = g * u * act'(x),  act'(x) = sigma + x * sigma * (1 - sigma) * dz/dx
+ *     du = g * act(x)
+ * in fp32, for every row (rows have no groups here).
+ *
+ *   g        bf16 or fp32 (dtype) [rows, N], rows ld elements apart, 16-byte
+ *            aligned, a row pitch multiple of 16 bytes.            (input)
+ *   pre      g's type [rows, 2, N], 16-byte aligned: x and u.      (input)
+ *   rows, N  N % 16 == 0, N <= 2^22; rows * ceil(N / 128) < 2^31.
+ *   out      g's type [rows, 2, N], 16-byte aligned, or NULL: dx and du.  It
+ *            may be pre itself, but overlap no input otherwise.   (output)
+ *   q, scales   e4m3 [rows, 2, N], 16-byte aligned, and fp32 [rows, 2,
+ *            ceil(N / 128)], or NULL: dx and du quantized as
+ *            gq_fp8_block_rows does it, from the fp32 values.  One of out and
+ *            q is not NULL.                                       (output)
+ *   flags    0 or GQ_SCALE_POW2.
+ *   stream   the CUDA stream to run on.  No workspace.
+ */
+gq_status gq_gated_backward(const void* g, const void* pre, int dtype, int64_t rows, int64_t N,
+                            int64_t ld, int activation, void* out, void* q, float* scales,
+                            uint32_t flags, gq_stream_t stream);
+
+/*
+ * grad_input of the two projections together:
+ *     out[m][k] = bf16( sum over n of dX[m][n] * W[g][0][n][k]
+ *                     + sum over n of dU[m][n] * W[g][1][n][k] )
+ * one contraction over 2 N columns, accumulated as in gq_grouped_mm.
+ *
+ *   qd       e4m3 [M, 2, N], 16-byte aligned: q of gq_gated_backward. (input)
+ *   sd       fp32 [M, 2, ceil(N / 128)].                           (input)
+ *   qb, sb, offs, n_groups   as in gq_grouped_gated_mm; N at least 16.
+ *   out      bf16 [M, K], 16-byte aligned; rows behind the last end are left
+ *            untouched.                                           (output)
+ *   stream   the CUDA stream to run on.  No workspace.
+ */
+gq_status gq_grouped_gated_grad(const void* qd, const float* sd, int64_t M, const void* qb,
+                                const float* sb, int64_t N, int64_t K, const int32_t* offs,
+                                int32_t n_groups, void* out, gq_stream_t stream);
+
+/*
+ * The norm over all elements of a list of tensors, sqrt(sum of x^2): squares
+ * summed in fp32 over at most 32 elements and in fp64 beyond, so that no
+ * finite fp32 or bf16 value overflows or vanishes on the way; the same result
+ * in every run.  A NaN or an infinity among the elements gives NaN or an
+ * infinity.  The three lists are arrays on the host and read before the call
+ * returns.
+ *
+ *   grads    device pointers, each aligned to its elements (not to more); NULL
+ *            for a tensor without elements.                        (input)
+ *   sizes    elements of each tensor, 2^42 at most in all.         (input)
+ *   dtypes   GQ_DTYPE_* of each tensor.                            (input)
+ *   count    tensors, 0 .. 2^20; the norm of none is 0.
+ *   norm     fp32, device.                                        (output)
+ *   workspace  device scratch of gq_grad_norm_workspace_bytes(count) bytes,
+ *            256-byte aligned; the call does not rely on its content.
+ *   stream   the CUDA stream to run on.
+ */
+size_t gq_grad_norm_workspace_bytes(int32_t count);
+gq_status gq_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes,
+                       int32_t count, float* norm, void* workspace, size_t workspace_bytes,
+                       gq_stream_t stream);
+
+/*
+ * The tensors scaled to a norm of at most max_norm:
+ *     y = x * (norm <= max_norm ? 1 : max_norm / norm)
+ * in fp32, rounded once to the tensor's type.  A NaN norm makes every element
+ * a NaN; an infinite one makes the finite elements zeros.  In place, a factor
+ * of 1 writes nothing.
+ *
+ *   grads, sizes, dtypes, count   as in gq_grad_norm.              (input)
+ *   outs     device pointers, each aligned to its elements, or NULL: in place.
+ *            An output may be its own tensor; overlaps between outputs, or of
+ *            an output with another tensor, are refused.          (output)
+ *   max_norm at least 0.
+ *   given_norm  fp32, device, or NULL: a norm to use instead of the tensors'
+ *            own (of more tensors than these, say); norm and workspace are
+ *            then ignored.                                         (input)
+ *   norm     fp32, device: the norm of the tensors.               (output)
+ *   workspace, stream   as in gq_grad_norm.
+ */
+gq_status gq_clip_grads(const void* const* grads, void* const* outs, const int64_t* sizes,
+                        const int32_t* dtypes, int32_t count, float max_norm,
+                        const float* given_norm, float* norm, void* workspace,
+                        size_t workspace_bytes, gq_stream_t stream);
+
+/*
  * Colwise scaling with no allocation at all, not even a caller workspace.
  * The pytorch/ao pages have no counterpart to this entry point; it exists for
  * callers that cannot obtain device memory at the point where they quantize
