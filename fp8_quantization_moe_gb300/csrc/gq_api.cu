@@ -152,12 +152,12 @@ gq_status encode_tiled_2d(CUtensorMap* map, CUtensorMapDataType dtype,
 gq_status encode_tiled_3d(CUtensorMap* map, CUtensorMapDataType dtype,
                           void* base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
                           uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0,
-                          uint32_t box1, CUtensorMapSwizzle swizzle) {
+                          uint32_t box1, CUtensorMapSwizzle swizzle, uint32_t box2) {
   std::call_once(g_encode_once, load_encode_fn);
   if (g_encode == nullptr) return g_encode_status;
   const cuuint64_t dims[3] = {dim0, dim1, dim2};
   const cuuint64_t strides[2] = {stride1_bytes, stride2_bytes};
-  const cuuint32_t box[3] = {box0, box1, 1};
+  const cuuint32_t box[3] = {box0, box1, box2};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = g_encode(map, dtype, 3, base, dims, strides, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
@@ -789,7 +789,7 @@ gq_status gq_grouped_gated_mm(const void* qa, const float* sa, int64_t M, const 
   const DeviceInfo* info = nullptr;
   st = current_device(&info);
   if (st != GQ_OK) return st;
-  return gated::launch_forward(*info, g_dbg, qa, sa, M, qb, sb, static_cast<int32_t>(N),
+  return gmm::launch_gated(*info, g_dbg, qa, sa, M, qb, sb, static_cast<int32_t>(N),
                                static_cast<int32_t>(K), activation, offs, n_groups, out, q, scales,
                                pre, (flags & GQ_SCALE_POW2) != 0,
                                reinterpret_cast<cudaStream_t>(stream));
@@ -812,7 +812,7 @@ gq_status gq_grouped_gated_grad(const void* qd, const float* sd, int64_t M, cons
   const DeviceInfo* info = nullptr;
   st = current_device(&info);
   if (st != GQ_OK) return st;
-  return gated::launch_grad(*info, g_dbg, qd, sd, M, qb, sb, static_cast<int32_t>(N),
+  return gmm::launch_gated_grad(*info, g_dbg, qd, sd, M, qb, sb, static_cast<int32_t>(N),
                             static_cast<int32_t>(K), offs, n_groups, out,
                             reinterpret_cast<cudaStream_t>(stream));
 }

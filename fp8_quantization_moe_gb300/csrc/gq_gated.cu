@@ -1,8 +1,6 @@
-// gq_gated.cu -- the gated feed-forward block of the experts: the backward
-// pass of its activation and product as one stream over the rows, and its
-// products.  Formulas in gq_gated.cuh.
-#include <cuda_fp8.h>
-
+// gq_gated.cu -- the backward pass of the gated feed-forward block's activation
+// and product, a stream over the rows (its grouped products are in
+// gq_grouped_mm.cu).  Formulas in gq_gated.cuh.
 #include "gq_gated.cuh"
 #include "gq_internal.h"
 
@@ -15,11 +13,6 @@ constexpr int kBlock = 128;
 constexpr int kUnit = 16;                       // columns per lane
 constexpr int kUnitsPerBlock = kBlock / kUnit;  // 8 lanes share a block
 constexpr int kThreads = 256;
-
-Act act_of(int activation) {
-  const float a = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-  return activation == GQ_ACT_GELU ? Act{a, a * 0.044715f} : Act{1.0f, 0.0f};
-}
 
 struct BackwardParams {
   const uint8_t* g;
@@ -134,116 +127,6 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BackwardParams
   }
 }
 
-// ------------------------------------------------------------- products --
-struct ProductParams {
-  const uint8_t* qa;
-  const float* sa;
-  const uint8_t* qb;
-  const float* sb;
-  const int32_t* offs;
-  uint16_t* out;
-  uint8_t* q;
-  float* scales;
-  uint16_t* pre;
-  int32_t M, N, K, E, nb_n, nb_k;
-  Act act;
-  bool pow2;
-};
-
-__device__ __forceinline__ float e4m3(uint8_t v) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
-}
-
-__device__ __forceinline__ uint16_t bf16_of(float v) {
-  return static_cast<uint16_t>(bf16x2_of(v, 0.0f) & 0xFFFFu);
-}
-
-// The group of row m, E if none.
-__device__ __forceinline__ int32_t group_of(const ProductParams& p, int32_t m) {
-  int32_t g = 0;
-  while (g < p.E && __ldg(p.offs + g) <= m) ++g;
-  return g;
-}
-
-// One thread per column of a row and 128-block of them.
-__global__ void __launch_bounds__(kBlock) forward_kernel(const ProductParams p) {
-  grid_wait();
-  __shared__ float red[kBlock / 32];
-  const int32_t m = blockIdx.x, g = group_of(p, m);
-  if (g == p.E) return;
-  const int32_t b = blockIdx.y, n = b * kBlock + threadIdx.x;
-  const bool in = n < p.N;
-  float v[2] = {0.0f, 0.0f};
-  if (in)
-    for (int h = 0; h < 2; ++h) {
-      const int64_t e = 2 * static_cast<int64_t>(g) + h;
-      const uint8_t* w = p.qb + (e * p.N + n) * p.K;
-      const uint8_t* a = p.qa + static_cast<int64_t>(m) * p.K;
-      for (int32_t kb = 0; kb < p.nb_k; ++kb) {
-        float s = 0.0f;
-        for (int32_t k = kb * kBlock; k < min(p.K, (kb + 1) * kBlock); ++k)
-          s = __fmaf_rn(e4m3(a[k]), e4m3(w[k]), s);
-        const float f = rcp_approx(p.sa[static_cast<int64_t>(m) * p.nb_k + kb]) *
-                        rcp_approx(p.sb[(e * p.nb_n + b) * p.nb_k + kb]);
-        v[h] = __fmaf_rn(s, f, v[h]);
-      }
-    }
-  const float h = act_value(v[0], sigma(act_z(p.act, v[0]))) * v[1];
-  const int64_t at = static_cast<int64_t>(m) * p.N + n;
-  if (in && p.pre != nullptr) {
-    p.pre[at + static_cast<int64_t>(m) * p.N] = bf16_of(v[0]);
-    p.pre[at + static_cast<int64_t>(m + 1) * p.N] = bf16_of(v[1]);
-  }
-  if (in && p.out != nullptr) p.out[at] = bf16_of(h);
-  if (p.q == nullptr) return;
-  float x = in ? fabsf(h) : 0.0f;
-  x = fmaxf(x, 0.0f);  // a NaN does not count
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  for (int i = 0; i < kBlock / 32; ++i) x = fmaxf(x, red[i]);
-  const float s = scale_from_amax_bits(__float_as_uint(x), p.pow2);
-  if (in) p.q[at] = static_cast<uint8_t>(quant4f(make_float4(h, h, h, h), s));
-  if (threadIdx.x == 0) p.scales[static_cast<int64_t>(m) * p.nb_n + b] = s;
-}
-
-__global__ void __launch_bounds__(kBlock) grad_kernel(const ProductParams p) {
-  grid_wait();
-  const int32_t m = blockIdx.x, g = group_of(p, m);
-  const int32_t b = blockIdx.y, k = b * kBlock + threadIdx.x;
-  if (g == p.E || k >= p.K) return;
-  float v = 0.0f;
-  for (int h = 0; h < 2; ++h) {
-    const int64_t e = 2 * static_cast<int64_t>(g) + h, r = 2 * static_cast<int64_t>(m) + h;
-    for (int32_t nb = 0; nb < p.nb_n; ++nb) {
-      float s = 0.0f;
-      for (int32_t n = nb * kBlock; n < min(p.N, (nb + 1) * kBlock); ++n)
-        s = __fmaf_rn(e4m3(p.qa[r * p.N + n]), e4m3(p.qb[(e * p.N + n) * p.K + k]), s);
-      const float f = rcp_approx(p.sa[r * p.nb_n + nb]) *
-                      rcp_approx(p.sb[(e * p.nb_n + nb) * p.nb_k + b]);
-      v = __fmaf_rn(s, f, v);
-    }
-  }
-  p.out[static_cast<int64_t>(m) * p.K + k] = bf16_of(v);
-}
-
-ProductParams params(const void* qa, const float* sa, int64_t M, const void* qb, const float* sb,
-                     int32_t N, int32_t K, const int32_t* offs, int32_t E) {
-  ProductParams p = {};
-  p.qa = static_cast<const uint8_t*>(qa);
-  p.sa = sa;
-  p.qb = static_cast<const uint8_t*>(qb);
-  p.sb = sb;
-  p.offs = offs;
-  p.M = static_cast<int32_t>(M);
-  p.N = N;
-  p.K = K;
-  p.E = E;
-  p.nb_n = (N + kBlock - 1) / kBlock;
-  p.nb_k = (K + kBlock - 1) / kBlock;
-  return p;
-}
-
 }  // namespace
 
 gq_status launch_backward(const void* g, const void* pre, bool f32, int64_t rows, int64_t N,
@@ -274,34 +157,6 @@ gq_status launch_backward(const void* g, const void* pre, bool f32, int64_t rows
   const int64_t grid = (blocks + kPer - 1) / kPer;
   return launch_chained("gated_backward: launch", f32 ? backward_kernel<true> : backward_kernel<false>,
                         dim3(static_cast<unsigned>(grid)), kThreads, 0, stream, 1, p);
-}
-
-gq_status launch_forward(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa,
-                         const float* sa, int64_t M, const void* qb, const float* sb, int32_t N,
-                         int32_t K, int activation, const int32_t* offs, int32_t E, void* out,
-                         void* q, float* scales, void* pre, bool pow2, cudaStream_t stream) {
-  (void)info;
-  (void)dbg;
-  ProductParams p = params(qa, sa, M, qb, sb, N, K, offs, E);
-  p.out = static_cast<uint16_t*>(out);
-  p.q = static_cast<uint8_t*>(q);
-  p.scales = scales;
-  p.pre = static_cast<uint16_t*>(pre);
-  p.act = act_of(activation);
-  p.pow2 = pow2;
-  return launch_chained("grouped_gated_mm: launch", forward_kernel,
-                        dim3(static_cast<unsigned>(M), p.nb_n), kBlock, 0, stream, 1, p);
-}
-
-gq_status launch_grad(const DeviceInfo& info, const DebugKnobs& dbg, const void* qd,
-                      const float* sd, int64_t M, const void* qb, const float* sb, int32_t N,
-                      int32_t K, const int32_t* offs, int32_t E, void* out, cudaStream_t stream) {
-  (void)info;
-  (void)dbg;
-  ProductParams p = params(qd, sd, M, qb, sb, N, K, offs, E);
-  p.out = static_cast<uint16_t*>(out);
-  return launch_chained("grouped_gated_grad: launch", grad_kernel,
-                        dim3(static_cast<unsigned>(M), p.nb_k), kBlock, 0, stream, 1, p);
 }
 
 }  // namespace gated

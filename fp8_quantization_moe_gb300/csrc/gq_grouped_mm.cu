@@ -80,6 +80,8 @@ struct Smem {
   uint64_t fac_full[kScaleRing];  // factors written (2 warps)
   uint64_t fac_empty[kScaleRing]; // factors read (8 warps)
   uint64_t drain;
+  uint64_t pair[4];               // kGated: both halves of a row have their maximum (2 warps)
+  float most[2][2][kRows];        // kGated: those maxima, by tile parity and half
   uint32_t tmem_base;
 };
 constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
@@ -111,12 +113,48 @@ __device__ __forceinline__ void swap_with(uint32_t& a, uint32_t& b, int lane) {
     b = got;
 }
 
-template <bool kT>
+// A store of this warp's rows: `out` points at column c of row (lane & ~3) of the
+// warp, rows `pitch` elements apart.  32 columns: four lanes exchange their
+// rows' 16-byte parts by shuffles, so that a store covers 64-byte runs of eight
+// rows.  (Staged in shared memory: 456 us instead of 452; sent from there by
+// TMA, with a stage less for the operands, 480; without an exchange 495;
+// exchanged by pairs of lanes 472, by eight lanes 465 against 465 here.)
+__device__ __forceinline__ void store_parts(uint32_t (&x)[4][4], uint8_t* out, int64_t pitch_bytes,
+                                            int32_t rows, bool c_ok, int lane) {
+  // x[part][word] of this lane's row
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    swap_with<1>(x[0][j], x[1][j], lane);
+    swap_with<1>(x[2][j], x[3][j], lane);
+    swap_with<2>(x[0][j], x[2][j], lane);
+    swap_with<2>(x[1][j], x[3][j], lane);
+  }
+  // x[k] is part lane & 3 of row (lane & ~3) + k
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if ((lane & ~3) + k < rows && c_ok)
+      *reinterpret_cast<uint4*>(out + k * pitch_bytes) = make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
+}
+
+__device__ __forceinline__ void store_bf16(const float (&v)[kChunk], uint16_t* out, int64_t pitch,
+                                           int32_t rows, bool c_ok, int lane) {
+  uint32_t x[4][4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[w][j] = bf16x2_of(v[8 * w + 2 * j], v[8 * w + 2 * j + 1]);
+  store_parts(x, reinterpret_cast<uint8_t*>(out), pitch * 2, rows, c_ok, lane);
+}
+
+template <int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap amap32,
                    const __grid_constant__ CUtensorMap wmap, const Params p) {
   // aligned by an offset, so that the compiler still knows the address space
+  constexpr bool kT = is_transposed(kForm);
+  // output columns of a tile; kGated: as many of each projection
+  constexpr int kTileCols = kForm == kGated ? kCols / 2 : kCols;
   extern __shared__ uint8_t smem_raw[];
   Smem& s = *reinterpret_cast<Smem*>(smem_raw + (-smem_addr(smem_raw) & 1023u));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
@@ -138,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.fac_empty[i], kEpiWarps);
     }
     mbar_init(&s.drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&s.pair[i], 2);
     fence_mbar_init();
   }
   grid_wait();
@@ -162,26 +201,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t st = 0, use = 0;  // stage, its use
       bool ok = true;
       for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-        const Tile t = tile_of(p, s.tiles, i, kRows, kCols, lane);
+        const Tile t = tile_of(p, s.tiles, i, kRows, kTileCols, lane);
         const int32_t boxes = boxes_of(t);
         const uint32_t bytes = 2 * kWHalf + static_cast<uint32_t>(boxes) * (kBoxRows * kBlock);
-        for (int32_t k = 0; k < p.inner; k += kBlock) {
+        for (int32_t kb = 0; kb < p.kbs; ++kb) {
+          const int32_t k = column_of<kForm>(p, kb), half = half_of<kForm>(p, kb);
           ok = mbar_wait_warp(done + st * 8, (use & 1) ^ 1u, wait_ns, p.err);
           if (!ok) break;
           if (elect_one()) {
             uint8_t* base = s.stage[st];
             uint64_t* bar = &s.full[st];
-            s.cols[st] = min(kCols, p.outer - t.c0);
+            s.cols[st] = min(kTileCols, p.outer - t.c0);
             mbar_arrive_expect_tx(bar, bytes);
             for (int h = 0; h < 2; ++h) {
-              const int32_t c = t.c0 + h * kCols / 2;
-              tma_load_3d(base + kABytes + h * kWHalf, &wmap, kT ? c : k, kT ? k : c, t.g, bar, pol);
+              const int32_t c = kForm == kGated ? t.c0 : t.c0 + h * kCols / 2;
+              const int32_t w = kForm == kGated ? 2 * t.g + h : kForm == kGatedGrad ? 2 * t.g + half : t.g;
+              tma_load_3d(base + kABytes + h * kWHalf, &wmap, kT ? c : k, kT ? k : c, w, bar, pol);
             }
+            auto load_rows = [&](const CUtensorMap* map, int32_t row) {
+              uint8_t* const to = base + row * kBlock;
+              if (kForm == kGatedGrad)
+                tma_load_3d(to, map, k, half, t.m0 + row, bar, pol);
+              else
+                tma_load_2d(to, map, k, t.m0 + row, bar, pol);
+            };
             if (boxes == kRows / kBoxRows)
-              tma_load_2d(base, &amap, k, t.m0, bar, pol);
+              load_rows(&amap, 0);
             else
-              for (int b = 0; b < boxes; ++b)
-                tma_load_2d(base + b * kBoxRows * kBlock, &amap32, k, t.m0 + b * kBoxRows, bar, pol);
+              for (int b = 0; b < boxes; ++b) load_rows(&amap32, b * kBoxRows);
           }
           __syncwarp();
           if (++st == kStages) {
@@ -208,7 +255,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true, issued = false;
         for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
           uint32_t idesc = 0;
-          for (int32_t left = p.inner; left > 0; left -= kBlock) {
+          bool apart = false;
+          for (int32_t kb = 0; kb < p.kbs; ++kb) {
+            const int32_t left = p.inner - column_of<kForm>(p, kb);
             // rows: K-major; weights: K-major rows of 128 bytes, or MN-major
             // (32 contraction rows = 4 KB, the column halves kWHalf apart)
             const uint32_t d = tmem + b * kCols, a0 = stage0 + st * kStageBytes;
@@ -217,19 +266,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_addr(full + st * 8, st_use & 1, wait_ns, p.err) &&
                  mbar_wait_addr(acc_empty + b * 8, (use & 1) ^ 1u, wait_ns, p.err);
             if (!ok) break;
-            if (left == p.inner) {
+            if (kb == 0) {
               // the tile's columns: a multiple of 16, as the MMA's N has to be
-              const uint32_t n = s.cols[st];
+              uint32_t n = s.cols[st];
+              if (kForm == kGated) {
+                // one MMA for both projections, or two where the tile is narrower
+                apart = n < kTileCols;
+                if (!apart) n = kCols;
+              }
               // D fp32, e4m3 x e4m3, B MN-major if transposed, N = n, M = 128
               idesc = (1u << 4) | (kT ? 1u << 16 : 0u) | ((n >> 3) << 17) | (8u << 24);
             }
             tc_fence_after();
             tc_mma_e4m3<false>(d, ad, wd, idesc);
+            if (kForm == kGated && apart)
+              tc_mma_e4m3<false>(d + kTileCols, ad, wd + (kWHalf >> 4), idesc);
 #pragma unroll
             for (int j = 1; j < kBlock / kSubK; ++j) {
               ad += kSubK >> 4;
               wd += wstep;
-              if (j * kSubK < left) tc_mma_e4m3<true>(d, ad, wd, idesc);
+              if (j * kSubK < left) {
+                tc_mma_e4m3<true>(d, ad, wd, idesc);
+                if (kForm == kGated && apart)
+                  tc_mma_e4m3<true>(d + kTileCols, ad, wd + (kWHalf >> 4), idesc);
+              }
             }
             tc_commit(&s.done[st]);
             issued = true;
@@ -256,18 +316,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // rows that exist are read (clamped to one row, the loads of all blocks
       // would queue up at a single L2 line).
       const int32_t first = (warp - kEpiWarps - 2) * 64 + lane;
-      float v[2][kScaleKb] = {}, w[2][kScaleKb];
+      float v[2][kScaleKb] = {}, ws[2][kScaleKb];
       int32_t i = blockIdx.x, kb = 0;
       Tile t = {};
       auto load = [&]() {  // the entry (tile i, 128-blocks kb ..)
-        if (kb == 0) t = tile_of(p, s.tiles, i, kRows, kCols, lane);
+        if (kb == 0) t = tile_of(p, s.tiles, i, kRows, kTileCols, lane);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float* sb = p.sb + t.g * p.sb_expert +
-                            static_cast<int64_t>(min(t.c0 / kBlock + h, p.sb_last)) * p.sb_c;
+          const int32_t w = kForm == kGated ? 2 * t.g + h : t.g;
+          const int32_t c = kForm == kGated ? t.c0 / kBlock : min(t.c0 / kBlock + h, p.sb_last);
+          const float* sb = p.sb + w * p.sb_expert + static_cast<int64_t>(c) * p.sb_c;
 #pragma unroll
           for (int u = 0; u < kScaleKb; ++u)
-            w[h][u] = __ldg(sb + static_cast<int64_t>(min(kb + u, p.kbs - 1)) * p.sb_k);
+            ws[h][u] = __ldg(sb + static_cast<int64_t>(min(kb + u, p.kbs - 1)) * p.sb_k);
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -294,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
 #pragma unroll
         for (int u = 0; u < kScaleKb; ++u) {
-          const float w0 = rcp_approx(w[0][u]), w1 = rcp_approx(w[1][u]);
+          const float w0 = rcp_approx(ws[0][u]), w1 = rcp_approx(ws[1][u]);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float ra = rcp_approx(v[j][u]);
@@ -320,7 +381,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // --------------------------------------------------------- epilogue --
     // Lane l of warp (q, hc) owns row 32 q + l of the tile and its columns
-    // [128 hc, 128 hc + 128), one scale block of the weights.  A turn (one
+    // [128 hc, 128 hc + 128), one scale block of the weights (kGated: [64 hc,
+    // 64 hc + 64) of both projections, one factor for each).  A turn (one
     // 128-block) has to be short against the MMAs, and shared memory, which
     // carries their operands, answers slowly: a turn's factor is read, its
     // MMAs' completion probed and its first 32 columns loaded during the turn
@@ -332,24 +394,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, hc = warp >> 2;
     const uint32_t done = smem_addr(s.done), fac_full = smem_addr(s.fac_full);
     const uint32_t acc_empty = smem_addr(s.acc_empty);
-    const uint32_t tmem0 = tmem + (static_cast<uint32_t>(32 * q) << 16) + hc * (kCols / 2);
-    const uint32_t fac = smem_addr(&s.factor[0][0][hc][32 * q + lane]);
+    constexpr int kMine = kTileCols / 2;  // output columns of this warp
+    const uint32_t tmem0 = tmem + (static_cast<uint32_t>(32 * q) << 16) + hc * kMine;
+    // where this warp's chunk ch begins in an accumulator
+    auto col = [](int ch) { return kForm == kGated ? (ch >> 1) * kTileCols + (ch & 1) * kChunk : ch * kChunk; };
+    const uint32_t fac = smem_addr(&s.factor[0][0][kForm == kGated ? 0 : hc][32 * q + lane]);
     const uint32_t tile = smem_addr(s.tile);
     constexpr uint32_t kFacKb = 2 * kRows * 4, kFacEntry = kScaleKb * kFacKb;
     uint32_t b = 0;               // accumulator
     uint32_t st = 0, use = 0;     // the stage whose MMAs filled it, its use
     uint32_t r = 0, fac_use = 0;  // entry of the factor ring, its use
     bool ready = false;           // the next MMAs are known to be complete
+    uint32_t pairs = 0;           // exchanges with the other half's warp so far
     bool hold = p.skip_arrival && blockIdx.x == 0;  // withhold the next release
     bool ok = true;
     for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
       ok = mbar_wait_warp(fac_full + r * 8, fac_use & 1, wait_ns, p.err);
       if (!ok) break;
       const uint4 ti = lds128_ordered(tile + r * 16);
-      float f = lds32_ordered(fac + r * kFacEntry);
+      float f = lds32_ordered(fac + r * kFacEntry), f1 = f;  // kGated: f1 is the up projection's
+      if (kForm == kGated) f1 = lds32_ordered(fac + r * kFacEntry + kRows * 4);
       const int32_t row0 = static_cast<int32_t>(ti.x) + 32 * q;
       const int32_t rows = static_cast<int32_t>(ti.y) - 32 * q;  // of this warp, if positive
-      const int32_t c = static_cast<int32_t>(ti.z) + hc * (kCols / 2);
+      const int32_t c = static_cast<int32_t>(ti.z) + hc * kMine;
       const bool mine = rows > 0 && c < p.outer;
       float acc[kChunks][kChunk];
 #pragma unroll
@@ -369,14 +436,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int32_t left = p.kbs; left > 0; --left) {
         const uint32_t tacc = tmem0 + b * kCols;
         if (mine) {
-          tmem_ld_32x32b_x32(tacc + kChunk, h1);
+          tmem_ld_32x32b_x32(tacc + col(1), h1);
           scale_add(acc[0], h0, f);
           tmem_ld_wait32(h1);
-          tmem_ld_32x32b_x32(tacc + 2 * kChunk, h0);
+          tmem_ld_32x32b_x32(tacc + col(2), h0);
           scale_add(acc[1], h1, f);
           tmem_ld_wait32(h0);
-          tmem_ld_32x32b_x32(tacc + 3 * kChunk, h1);
-          scale_add(acc[2], h0, f);
+          tmem_ld_32x32b_x32(tacc + col(3), h1);
+          scale_add(acc[2], h0, kForm == kGated ? f1 : f);
           tmem_ld_wait32(h1);
         }
         tc_fence_before();
@@ -404,6 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float next = lds32_ordered(fac + r * kFacEntry + e * kFacKb);
+        float next1 = next;
+        if (kForm == kGated) next1 = lds32_ordered(fac + r * kFacEntry + e * kFacKb + kRows * 4);
         if (left > 1) {
           if (!__all_sync(0xffffffffu, ready)) {
             ok = mbar_wait_warp(done + st * 8, use & 1, wait_ns, p.err);
@@ -412,46 +481,79 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (mine) {
             tmem_ld_32x32b_x32(tmem0 + b * kCols, h0);
-            scale_add(acc[3], h1, f);
+            scale_add(acc[3], h1, kForm == kGated ? f1 : f);
             tmem_ld_wait32(h0);
           }
         } else if (mine) {
-          scale_add(acc[3], h1, f);
+          scale_add(acc[3], h1, kForm == kGated ? f1 : f);
         }
         f = next;
+        f1 = next1;
       }
       if (!ok) break;
       if (!mine) continue;
-      // 32 columns at a time: four lanes exchange their rows' 16-byte parts by
-      // shuffles, so that a store covers 64-byte runs of eight rows.  (Staged in
-      // shared memory: 456 us instead of 452; sent from there by TMA, with a
-      // stage less for the operands, 480; without an exchange 495; exchanged by
-      // pairs of lanes 472, by eight lanes 465 against 465 here.)
       const int part = lane & 3;
-      uint16_t* orow = p.out + static_cast<int64_t>(row0 + (lane & ~3)) * p.outer + c + part * 8;
+      const int64_t row = row0 + (lane & ~3);
+      if (kForm != kGated) {
+        uint16_t* const orow = p.out + row * p.outer + c + part * 8;
 #pragma unroll
-      for (int ch = 0; ch < kChunks; ++ch) {
-        uint32_t x[4][4];  // [part][word] of this lane's row
+        for (int ch = 0; ch < kChunks; ++ch)
+          store_bf16(acc[ch], orow + ch * kChunk, p.outer, rows,
+                     c + ch * kChunk + part * 8 < p.outer, lane);  // outer % 16 == 0
+        continue;
+      }
+      // the projections, as they are
+      if (p.pre != nullptr) {
+        uint16_t* const prow = p.pre + row * 2 * p.outer + c + part * 8;
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+        for (int ch = 0; ch < kChunks; ++ch)
+          store_bf16(acc[ch], prow + (ch >> 1) * static_cast<int64_t>(p.outer) + (ch & 1) * kChunk,
+                     2 * static_cast<int64_t>(p.outer), rows,
+                     c + (ch & 1) * kChunk + part * 8 < p.outer, lane);
+      }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            x[w][j] = bf16x2_of(acc[ch][8 * w + 2 * j], acc[ch][8 * w + 2 * j + 1]);
+      for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) acc[ch][j] = gated_value(p, acc[ch][j], acc[ch + 2][j]);
+      if (p.out != nullptr) {
+        uint16_t* const orow = p.out + row * p.outer + c + part * 8;
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)
+          store_bf16(acc[ch], orow + ch * kChunk, p.outer, rows,
+                     c + ch * kChunk + part * 8 < p.outer, lane);
+      }
+      if (p.q == nullptr) continue;
+      // a 1x128 block is this warp's row and that of the warp of the other half
+      // of the columns: they exchange their maxima (a NaN does not count;
+      // columns past the last hold anything)
+      float most = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c + 16 * u < p.outer)  // outer % 16 == 0
+#pragma unroll
+          for (int j = 0; j < 16; ++j) most = fmaxf(most, fabsf(acc[u >> 1][(u & 1) * 16 + j]));
+      if (static_cast<int32_t>(ti.z) + kMine < p.outer) {
+        const uint32_t buf = smem_addr(&s.most[pairs & 1][0][32 * q + lane]);
+        sts32(buf + hc * kRows * 4, most);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.pair[q]);
+        ok = mbar_wait_warp(smem_addr(&s.pair[q]), pairs & 1, wait_ns, p.err);
+        if (!ok) break;
+        ++pairs;
+        most = fmaxf(most, lds32_ordered(buf + (hc ^ 1) * kRows * 4));
+      }
+      const float sc = scale_from_amax_bits(__float_as_uint(most), p.pow2);
+      uint32_t x[4][4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          swap_with<1>(x[0][j], x[1][j], lane);
-          swap_with<1>(x[2][j], x[3][j], lane);
-          swap_with<2>(x[0][j], x[2][j], lane);
-          swap_with<2>(x[1][j], x[3][j], lane);
+          const float* v = &acc[w >> 1][(w & 1) * 16 + 4 * j];
+          x[w][j] = quant4f(make_float4(v[0], v[1], v[2], v[3]), sc);
         }
-        // x[k] is part lane & 3 of row (lane & ~3) + k
-        const bool c_ok = c + ch * kChunk + part * 8 < p.outer;  // outer % 16 == 0
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((lane & ~3) + k < rows && c_ok)
-            *reinterpret_cast<uint4*>(orow + static_cast<int64_t>(k) * p.outer + ch * kChunk) =
-                make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]);
-      }
+      store_parts(x, p.q + row * p.outer + c + part * 16, p.outer, rows, c + part * 16 < p.outer, lane);
+      if (hc == 0 && lane < rows)
+        p.scales[static_cast<int64_t>(row0 + lane) * ((p.outer + kBlock - 1) / kBlock) + c / kBlock] = sc;
     }
     tc_fence_before();
   }
@@ -476,8 +578,10 @@ constexpr int kFewRows = 48;
 }  // namespace
 
 gq_status setup(DeviceInfo& info) {
-  for (const void* f : {reinterpret_cast<const void*>(product_kernel<false>),
-                        reinterpret_cast<const void*>(product_kernel<true>)}) {
+  for (const void* f : {reinterpret_cast<const void*>(product_kernel<kForward>),
+                        reinterpret_cast<const void*>(product_kernel<kTransposed>),
+                        reinterpret_cast<const void*>(product_kernel<kGated>),
+                        reinterpret_cast<const void*>(product_kernel<kGatedGrad>)}) {
     gq_status st = check_cuda(
         cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemBytes)),
@@ -490,14 +594,21 @@ gq_status setup(DeviceInfo& info) {
     if (a.numRegs * kThreads < 32 * (kEpiWarps * kEpiRegs + (kThreads / 32 - kEpiWarps) * kOtherRegs))
       return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: built with %d registers per thread", a.numRegs);
   }
-  return setup_few(info);
+  (void)info;
+  return setup_few();
 }
 
-gq_status launch(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa, const float* sa,
-                 int64_t M, const void* qb, const float* sb, int32_t N, int32_t K, bool transposed,
-                 const int32_t* offs, int32_t E, void* out, cudaStream_t stream) {
+namespace {
+
+// Parameters of a product of rows of `inner` columns with E matrices (N, K), or
+// pairs of them.
+Params params_of(const DeviceInfo& info, const DebugKnobs& dbg, int form, const float* sa,
+                 int64_t M, const float* sb, int32_t N, int32_t K, const int32_t* offs, int32_t E,
+                 void* out) {
   const int32_t nb_n = (N + kBlock - 1) / kBlock, nb_k = (K + kBlock - 1) / kBlock;
-  Params p;
+  const bool transposed = is_transposed(form);
+  Params p = {};
+  p.form = form;
   p.inner = transposed ? N : K;
   p.outer = transposed ? K : N;
   p.sa = sa;
@@ -507,41 +618,99 @@ gq_status launch(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa, 
   p.err = info.err_word;
   p.M = static_cast<int32_t>(M);
   p.E = E;
-  p.kbs = (p.inner + kBlock - 1) / kBlock;
-  p.tiles_c = (p.outer + kCols - 1) / kCols;
-  p.sb_expert = static_cast<int64_t>(nb_n) * nb_k;
+  p.kb_half = transposed ? nb_n : nb_k;
+  p.kbs = form == kGatedGrad ? 2 * p.kb_half : p.kb_half;
+  // the blocks of a pair of matrices follow each other along N, so that both
+  // halves of a contraction over N are one run of blocks
+  p.sb_expert = static_cast<int64_t>(nb_n) * nb_k * (form == kGatedGrad ? 2 : 1);
   p.sb_c = transposed ? 1 : nb_k;
   p.sb_k = transposed ? nb_k : 1;
   p.sb_last = (transposed ? nb_k : nb_n) - 1;
   p.sa_vec = p.kbs % kScaleKb == 0 && (reinterpret_cast<uintptr_t>(sa) & 15) == 0;
-  p.transposed = transposed;
   p.timeout_ns = dbg.timeout_ns;
   p.skip_arrival = dbg.skip_arrival;
-  if (M <= static_cast<int64_t>(kFewRows) * E) return launch_few(info, p, qa, qb, N, K, stream);
+  return p;
+}
 
-  const int64_t most = (M / kRows + (E < M ? E : M)) * p.tiles_c;  // tiles of any offsets
-  if (most > INT32_MAX)
+template <int kForm>
+gq_status launch_many(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,
+                      int32_t K, cudaStream_t stream) {
+  constexpr int kTileCols = kForm == kGated ? kCols / 2 : kCols;
+  p.tiles_c = (p.outer + kTileCols - 1) / kTileCols;
+  const int64_t most = (static_cast<int64_t>(p.M) / kRows + (p.E < p.M ? p.E : p.M)) * p.tiles_c;
+  if (most > INT32_MAX)  // tiles of any offsets
     return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: %lld tiles", static_cast<long long>(most));
   CUtensorMap amap, amap32, wmap;
   gq_status st = GQ_OK;
   for (CUtensorMap* m : {&amap, &amap32}) {
-    st = encode_tiled_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(qa),
-                         static_cast<uint64_t>(p.inner), static_cast<uint64_t>(M),
-                         static_cast<uint64_t>(p.inner), kBlock, m == &amap ? kRows : kBoxRows,
-                         CU_TENSOR_MAP_SWIZZLE_128B);
+    st = encode_rows(m, p, qa, m == &amap ? kRows : kBoxRows);
     if (st != GQ_OK) return st;
   }
-  // three dimensions: rows and columns past an expert's own read zeros, never
-  // the next expert's (a NaN there would survive the product with zero)
-  st = encode_tiled_3d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(qb),
-                       static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E),
-                       static_cast<uint64_t>(K), static_cast<uint64_t>(N) * K, kBlock, kBlock,
-                       CU_TENSOR_MAP_SWIZZLE_128B);
+  st = encode_weights(&wmap, p, qb, N, K);
   if (st != GQ_OK) return st;
   const unsigned grid = static_cast<unsigned>(most < info.sm_count ? most : info.sm_count);
-  const auto kernel = transposed ? product_kernel<true> : product_kernel<false>;
-  return launch_chained("grouped_mm: launch", kernel, dim3(grid), kThreads, kSmemBytes, stream, 1,
-                        amap, amap32, wmap, p);
+  return launch_chained("grouped_mm: launch", product_kernel<kForm>, dim3(grid), kThreads,
+                        kSmemBytes, stream, 1, amap, amap32, wmap, p);
+}
+
+template <int kForm>
+gq_status launch_form(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,
+                      int32_t K, cudaStream_t stream) {
+  if (p.M <= static_cast<int64_t>(kFewRows) * p.E)
+    return launch_few(info, p, qa, qb, N, K, stream);
+  return launch_many<kForm>(info, p, qa, qb, N, K, stream);
+}
+
+}  // namespace
+
+// Rows of the A operand: two dimensions, or for kGatedGrad three, so that a box
+// that ends behind the last column of one half reads zeros, not the other half.
+gq_status encode_rows(CUtensorMap* map, const Params& p, const void* qa, uint32_t rows) {
+  const uint64_t inner = static_cast<uint64_t>(p.inner), m = static_cast<uint64_t>(p.M);
+  if (p.form == kGatedGrad)
+    return encode_tiled_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(qa), inner, 2, m,
+                           inner, 2 * inner, kBlock, 1, CU_TENSOR_MAP_SWIZZLE_128B, rows);
+  return encode_tiled_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(qa), inner, m, inner,
+                         kBlock, rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Three dimensions: rows and columns past a matrix's own read zeros, never the
+// next matrix's (a NaN there would survive the product with zero).
+gq_status encode_weights(CUtensorMap* map, const Params& p, const void* qb, int32_t N, int32_t K) {
+  const uint64_t count = static_cast<uint64_t>(p.E) * (p.form >= kGated ? 2 : 1);
+  return encode_tiled_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(qb),
+                         static_cast<uint64_t>(K), static_cast<uint64_t>(N), count,
+                         static_cast<uint64_t>(K), static_cast<uint64_t>(N) * K, kBlock, kBlock,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+gq_status launch(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa, const float* sa,
+                 int64_t M, const void* qb, const float* sb, int32_t N, int32_t K, bool transposed,
+                 const int32_t* offs, int32_t E, void* out, cudaStream_t stream) {
+  Params p = params_of(info, dbg, transposed ? kTransposed : kForward, sa, M, sb, N, K, offs, E, out);
+  return transposed ? launch_form<kTransposed>(info, p, qa, qb, N, K, stream)
+                    : launch_form<kForward>(info, p, qa, qb, N, K, stream);
+}
+
+gq_status launch_gated(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa,
+                       const float* sa, int64_t M, const void* qb, const float* sb, int32_t N,
+                       int32_t K, int activation, const int32_t* offs, int32_t E, void* out,
+                       void* q, float* scales, void* pre, bool pow2, cudaStream_t stream) {
+  Params p = params_of(info, dbg, kGated, sa, M, sb, N, K, offs, E, out);
+  p.q = static_cast<uint8_t*>(q);
+  p.scales = scales;
+  p.pre = static_cast<uint16_t*>(pre);
+  p.act = gated::act_of(activation);
+  p.pow2 = pow2;
+  return launch_form<kGated>(info, p, qa, qb, N, K, stream);
+}
+
+gq_status launch_gated_grad(const DeviceInfo& info, const DebugKnobs& dbg, const void* qd,
+                            const float* sd, int64_t M, const void* qb, const float* sb, int32_t N,
+                            int32_t K, const int32_t* offs, int32_t E, void* out,
+                            cudaStream_t stream) {
+  Params p = params_of(info, dbg, kGatedGrad, sd, M, sb, N, K, offs, E, out);
+  return launch_form<kGatedGrad>(info, p, qd, qb, N, K, stream);
 }
 
 }  // namespace gmm

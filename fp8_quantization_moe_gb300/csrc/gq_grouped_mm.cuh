@@ -1,11 +1,12 @@
 // gq_grouped_mm.cuh -- what the two kernels of the grouped block-scaled
-// product share: parameters, and the list of tiles that the group ends give.
+// products share: the products' forms, parameters, and the list of tiles that
+// the group ends give.
 // A tile is (group, `rows` rows of it, `cols` output columns); within a group
 // the row tiles run fastest, so that blocks at work at the same time share
 // the weights of a column tile.
 #pragma once
 
-#include "gq_device.cuh"
+#include "gq_gated.cuh"
 #include "gq_internal.h"
 
 namespace gq {
@@ -14,6 +15,15 @@ namespace gmm {
 constexpr int kBlock = 128;  // contraction columns per scale, and per stage
 constexpr int kSubK = 32;    // contraction columns per MMA (kind::f8f6f4)
 
+// The products, W[g] being a group's matrix (N, K) or its two, W0 and W1.
+enum Form {
+  kForward,     // A W^T
+  kTransposed,  // A W
+  kGated,       // act(A W0^T) * (A W1^T), formed in the epilogue
+  kGatedGrad,   // A0 W0 + A1 W1, one contraction over both halves of A's rows
+};
+__host__ __device__ constexpr bool is_transposed(int form) { return form == kTransposed || form == kGatedGrad; }
+
 struct Params {
   const float* sa;
   const float* sb;
@@ -21,13 +31,20 @@ struct Params {
   uint16_t* out;
   unsigned* err;
   int32_t M, E, inner, outer;
-  int32_t kbs;           // 128-blocks of the contraction
+  int32_t kbs;           // 128-blocks of the contraction (kGatedGrad: of both halves)
+  int32_t kb_half;       // kGatedGrad: of one half
   int32_t tiles_c;       // tiles along the output columns
-  int64_t sb_expert;     // scales per expert
+  int64_t sb_expert;     // scales per matrix (kGatedGrad: per pair of them)
   int32_t sb_c, sb_k;    // scale strides along output and contraction blocks
   int32_t sb_last;       // last output block
   bool sa_vec;           // rows of sa are 16-byte aligned
-  bool transposed;
+  int32_t form;
+  // kGated: what the epilogue writes beside out, each may be nullptr
+  uint8_t* q;
+  float* scales;
+  uint16_t* pre;
+  gated::Act act;
+  bool pow2;
   uint64_t timeout_ns;
   int32_t skip_arrival;  // test hook: block 0 never frees its first accumulator
 };
@@ -86,6 +103,22 @@ __device__ __forceinline__ void build_tiles(const Params& p, int32_t rows, TileT
   }
 }
 
+// 128-block kb of the contraction: its first column, and the matrix or half of
+// the rows that it belongs to.
+template <int kForm>
+__device__ __forceinline__ int32_t half_of(const Params& p, int32_t kb) {
+  return kForm == kGatedGrad && kb >= p.kb_half ? 1 : 0;
+}
+template <int kForm>
+__device__ __forceinline__ int32_t column_of(const Params& p, int32_t kb) {
+  return (kb - (half_of<kForm>(p, kb) ? p.kb_half : 0)) * kBlock;
+}
+
+// kGated: h = act(x) u.
+__device__ __forceinline__ float gated_value(const Params& p, float x, float u) {
+  return gated::act_value(x, gated::sigma_approx(gated::act_z(p.act, x))) * u;
+}
+
 struct Tile {
   int32_t g, c0, m0, rows;  // group, first column, first row, rows of the group from there
 };
@@ -111,8 +144,10 @@ __device__ __forceinline__ Tile tile_of(const Params& p, const TileTable& s, int
 
 // The product of many rows per group (gq_grouped_mm.cu) and of few
 // (gq_grouped_mm_few.cu).
-gq_status setup_few(DeviceInfo& info);
-gq_status launch_few(const DeviceInfo& info, Params p, const void* qa, const void* qb, int32_t N,
+gq_status setup_few();
+gq_status encode_rows(CUtensorMap* map, const Params& p, const void* qa, uint32_t rows);
+gq_status encode_weights(CUtensorMap* map, const Params& p, const void* qb, int32_t N, int32_t K);
+gq_status launch_few(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,
                      int32_t K, cudaStream_t stream);
 
 }  // namespace gmm

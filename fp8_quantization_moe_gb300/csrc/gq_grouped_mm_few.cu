@@ -29,21 +29,33 @@ namespace gmm {
 namespace {
 
 constexpr int kCols = 128;     // output columns of a tile (the MMA's M)
-constexpr int kTok = 128;      // rows of a tile, at most (the MMA's N)
 constexpr int kUnit = 16;      // rows of a tile come in units
-constexpr int kWarpTok = 64;   // rows of an epilogue warp, at most
 constexpr int kWBytes = kCols * kBlock;   // 16 KB
 constexpr int kScaleKb = 4;    // 128-blocks per entry of the factor ring
 constexpr int kScaleRing = 4;
-constexpr int kStages = 6;
-constexpr int kStageBytes = kWBytes + kTok * kBlock;
-constexpr int kBufs = 512 / kTok;
-constexpr int kEpiWarps = 4 * (kTok / kWarpTok);
+constexpr int kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarps + 3) * 32;
 
+// kGated: a tile has the columns of both projections, two MMAs with the same
+// rows; half as many of these, so that TMEM holds four accumulators all the same.
+template <int kForm>
+struct Sizes {
+  static constexpr int kMats = kForm == kGated ? 2 : 1;
+  static constexpr int kTok = 128 / kMats;       // rows of a tile, at most (the MMA's N)
+  static constexpr int kWarpTok = kTok / 2;      // rows of an epilogue warp, at most
+  static constexpr int kStageBytes = kMats * kWBytes + kTok * kBlock;
+  static constexpr int kStages = kForm == kGated ? 5 : 6;
+  static constexpr int kAccCols = kMats * kTok;  // TMEM columns of an accumulator
+  static constexpr int kBufs = 512 / kAccCols;
+  static_assert(kEpiWarps == 4 * (kTok / kWarpTok), "two warps per lane quarter");
+};
+
+template <int kForm>
 struct Smem {
-  uint8_t stage[kStages][kStageBytes];
-  alignas(16) float factor[kScaleRing][kScaleKb][kTok];
+  using Z = Sizes<kForm>;
+  static constexpr int kStages = Z::kStages, kBufs = Z::kBufs;
+  uint8_t stage[kStages][Z::kStageBytes];
+  alignas(16) float factor[kScaleRing][kScaleKb][Z::kAccCols];  // kGated: of both matrices
   TileTable tiles;
   uint64_t full[kStages];
   uint64_t done[kStages];
@@ -51,13 +63,19 @@ struct Smem {
   uint64_t fac_full[kScaleRing];
   uint64_t fac_empty[kScaleRing];
   uint64_t drain;
+  uint64_t pair[2];              // kGated: the four warps of a row have their maxima
+  alignas(16) float most[2][2][Z::kWarpTok][4];  // kGated: those, by exchange parity, warps' rows
   uint32_t tmem_base;
 };
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "fits one SM's shared memory");
+template <int kForm>
+constexpr size_t smem_bytes() {
+  static_assert(sizeof(Smem<kForm>) + 1024 <= 227 * 1024, "fits one SM's shared memory");
+  return sizeof(Smem<kForm>) + 1024;
+}
 
+template <int kForm>
 __device__ __forceinline__ int32_t units_of(const Tile& t) {
-  return (min(t.rows, kTok) + kUnit - 1) / kUnit;
+  return (min(t.rows, Sizes<kForm>::kTok) + kUnit - 1) / kUnit;
 }
 
 // Positions in the rings, common to a tile's steps.
@@ -65,19 +83,113 @@ struct Rings {
   uint32_t b = 0;              // accumulator
   uint32_t st = 0, use = 0;    // stage, its use
   uint32_t r = 0, sc_use = 0;  // entry of the factor ring, its use
+  uint32_t shares = 0;         // kGated: exchanges of maxima so far
   bool hold = false;           // test hook: withhold the next release
 };
 
+// Rows of 128-columns' values in TMEM lanes (a lane is a column c) to bf16 rows:
+// two rows at a time, neighbouring lanes swap one value each, so that even lanes
+// hold two columns of the first row and odd lanes of the second; a store covers
+// 64 bytes of both.  `out` points at column (c & ~1) of row (lane & 1).
+template <int kN>
+__device__ __forceinline__ void store_bf16(const float (&v)[kN][kUnit], uint16_t* out, int64_t pitch,
+                                           int32_t rows, bool c_ok, int lane) {
+  const int32_t odd = lane & 1;
+#pragma unroll
+  for (int u = 0; u < kN; ++u)
+#pragma unroll
+    for (int j = 0; j < kUnit; j += 2) {
+      const float give = odd ? v[u][j] : v[u][j + 1];
+      const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+      const uint32_t w = odd ? bf16x2_of(got, v[u][j + 1]) : bf16x2_of(v[u][j], got);
+      if (u * kUnit + j + odd < rows && c_ok)
+        *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(u * kUnit + j) * pitch) = w;
+    }
+}
+
+// kGated: the rows of a tile, x and u (columns in lanes), to what is asked for.
+template <int kN>
+__device__ __forceinline__ bool gated_store(const Params& p, Smem<kGated>& s, const Tile& t, Rings& r,
+                                            float (&x)[kN][kUnit], float (&u)[kN][kUnit], int32_t j0,
+                                            int q, int lane, uint64_t wait_ns) {
+  const int32_t rows = t.rows - j0;
+  const int32_t c = t.c0 + 32 * q + lane, pair = c & ~1, odd = lane & 1;
+  const bool c_ok = pair < p.outer;  // outer % 16 == 0
+  const int64_t row = t.m0 + j0, n = p.outer;
+  if (p.pre != nullptr) {
+    uint16_t* const to = p.pre + (row + odd) * 2 * n + pair;
+    store_bf16(x, to, 2 * n, rows, c_ok, lane);
+    store_bf16(u, to + n, 2 * n, rows, c_ok, lane);
+  }
+#pragma unroll
+  for (int a = 0; a < kN; ++a)
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) x[a][j] = gated_value(p, x[a][j], u[a][j]);
+  if (p.out != nullptr) store_bf16(x, p.out + (row + odd) * n + pair, n, rows, c_ok, lane);
+  if (p.q == nullptr) return true;
+  // the maximum of a row over this warp's 32 columns, then over the four warps
+  // that hold its 128 (a NaN does not count; columns past the last hold anything)
+  const int g = j0 / Sizes<kGated>::kWarpTok;
+  float(*const most)[4] = s.most[r.shares & 1][g];
+#pragma unroll
+  for (int a = 0; a < kN; ++a) {
+    float m = 0.0f;  // of row `lane & 15`
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) {
+      float v = c < p.outer ? fmaxf(fabsf(x[a][j]), 0.0f) : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+      if ((lane & 15) == j) m = v;
+    }
+    if (lane < kUnit) sts32(smem_addr(&most[a * kUnit + lane][q]), m);
+  }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&s.pair[g]);
+  if (!mbar_wait_warp(smem_addr(&s.pair[g]), r.shares & 1, wait_ns, p.err)) return false;
+  ++r.shares;
+  const int32_t nb = (p.outer + kBlock - 1) / kBlock;
+#pragma unroll
+  for (int a = 0; a < kN; ++a)
+#pragma unroll
+    for (int j = 0; j < kUnit; j += 4) {
+      // four rows: a lane's bytes of its column, then by two exchanges of bytes the
+      // bytes of four columns of one row, lane & 3
+      uint32_t w = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 m = lds128_ordered(smem_addr(most[a * kUnit + j + k]));
+        const float top = fmaxf(fmaxf(__uint_as_float(m.x), __uint_as_float(m.y)),
+                                fmaxf(__uint_as_float(m.z), __uint_as_float(m.w)));
+        const float sc = scale_from_amax_bits(__float_as_uint(top), p.pow2);
+        const float v = x[a][j + k];
+        w |= (quant4f(make_float4(v, v, v, v), sc) & 0xFFu) << (8 * k);
+        if (q == 0 && lane == 0 && a * kUnit + j + k < rows)
+          p.scales[(row + a * kUnit + j + k) * nb + t.c0 / kBlock] = sc;
+      }
+      uint32_t o = __shfl_xor_sync(0xffffffffu, w, 1);
+      w = lane & 1 ? __byte_perm(w, o, 0x3715) : __byte_perm(w, o, 0x6240);
+      o = __shfl_xor_sync(0xffffffffu, w, 2);
+      w = lane & 2 ? __byte_perm(w, o, 0x3276) : __byte_perm(w, o, 0x5410);
+      const int32_t at = a * kUnit + j + (lane & 3);
+      if (at < rows && (c & ~3) < p.outer)
+        *reinterpret_cast<uint32_t*>(p.q + (row + at) * n + (c & ~3)) = w;
+    }
+  return true;
+}
+
 // A tile of which this warp has kU * 16 rows from row j0 on (kU = 0: none, it
 // only keeps step); false if a wait expired.
-template <int kU>
-__device__ __forceinline__ bool tile_body(const Params& p, Smem& s, const Tile& t, Rings& x,
+template <int kForm, int kU>
+__device__ __forceinline__ bool tile_body(const Params& p, Smem<kForm>& s, const Tile& t, Rings& x,
                                           uint32_t tmem0, int32_t j0, int q, int lane,
                                           uint64_t wait_ns) {
+  using Z = Sizes<kForm>;
   constexpr int kN = kU > 0 ? kU : 1;
-  float acc[kN][kUnit];
+  float acc[Z::kMats][kN][kUnit];
 #pragma unroll
-  for (int a = 0; a < kN * kUnit; ++a) acc[a / kUnit][a % kUnit] = 0.0f;
+  for (int i = 0; i < Z::kMats; ++i)
+#pragma unroll
+    for (int a = 0; a < kN * kUnit; ++a) acc[i][a / kUnit][a % kUnit] = 0.0f;
   const uint32_t done = smem_addr(s.done), fac_full = smem_addr(s.fac_full);
   const uint32_t factors = smem_addr(s.factor), acc_empty = smem_addr(s.acc_empty);
 #pragma unroll 1
@@ -86,32 +198,40 @@ __device__ __forceinline__ bool tile_body(const Params& p, Smem& s, const Tile& 
     if (e == 0 && !mbar_wait_warp(fac_full + x.r * 8, x.sc_use & 1, wait_ns, p.err)) return false;
     if (!mbar_wait_warp(done + x.st * 8, x.use & 1, wait_ns, p.err)) return false;
     tc_fence_after();
-    uint32_t h[kN][kUnit];
+    uint32_t h[Z::kMats][kN][kUnit];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) tmem_ld_32x32b_x16(tmem0 + x.b * kTok + j0 + u * kUnit, h[u]);
+    for (int i = 0; i < Z::kMats; ++i)
 #pragma unroll
-    for (int u = 0; u < kU; ++u) tmem_ld_wait16(h[u]);
+      for (int u = 0; u < kU; ++u)
+        tmem_ld_32x32b_x16(tmem0 + x.b * Z::kAccCols + i * Z::kTok + j0 + u * kUnit, h[i][u]);
+#pragma unroll
+    for (int i = 0; i < Z::kMats; ++i)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) tmem_ld_wait16(h[i][u]);
     tc_fence_before();
     __syncwarp();
     if (lane == 0 && !x.hold) mbar_arrive_addr(acc_empty + x.b * 8);
     x.hold = false;
-    const uint32_t fac = factors + ((x.r * kScaleKb + e) * kTok + j0) * 4;
+    const uint32_t fac = factors + ((x.r * kScaleKb + e) * Z::kAccCols + j0) * 4;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      uint4 f[4];
+    for (int i = 0; i < Z::kMats; ++i)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) f[v] = lds128_ordered(fac + (u * kUnit + 4 * v) * 4);
+      for (int u = 0; u < kU; ++u) {
+        uint4 f[4];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float w[4] = {__uint_as_float(f[v].x), __uint_as_float(f[v].y),
-                            __uint_as_float(f[v].z), __uint_as_float(f[v].w)};
+        for (int v = 0; v < 4; ++v) f[v] = lds128_ordered(fac + (i * Z::kTok + u * kUnit + 4 * v) * 4);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[u][4 * v + j] = __fmaf_rn(__uint_as_float(h[u][4 * v + j]), w[j], acc[u][4 * v + j]);
+        for (int v = 0; v < 4; ++v) {
+          const float w[4] = {__uint_as_float(f[v].x), __uint_as_float(f[v].y),
+                              __uint_as_float(f[v].z), __uint_as_float(f[v].w)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[i][u][4 * v + j] =
+                __fmaf_rn(__uint_as_float(h[i][u][4 * v + j]), w[j], acc[i][u][4 * v + j]);
+        }
       }
-    }
-    if (++x.b == kBufs) x.b = 0;
-    if (++x.st == kStages) {
+    if (++x.b == Z::kBufs) x.b = 0;
+    if (++x.st == Z::kStages) {
       x.st = 0;
       ++x.use;
     }
@@ -124,31 +244,27 @@ __device__ __forceinline__ bool tile_body(const Params& p, Smem& s, const Tile& 
       }
     }
   }
-  // Two rows at a time: neighbouring lanes swap one value each, so that even
-  // lanes hold two columns of the first row and odd lanes of the second;
-  // a store covers 64 bytes of both.
-  const int32_t c = t.c0 + 32 * q + (lane & ~1);
-  const int32_t odd = lane & 1;
-  uint16_t* dst = p.out + static_cast<int64_t>(t.m0 + j0 + odd) * p.outer + c;
-#pragma unroll
-  for (int u = 0; u < kU; ++u)
-#pragma unroll
-    for (int j = 0; j < kUnit; j += 2) {
-      const float give = odd ? acc[u][j] : acc[u][j + 1];
-      const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-      const uint32_t w = odd ? bf16x2_of(got, acc[u][j + 1]) : bf16x2_of(acc[u][j], got);
-      if (j0 + u * kUnit + j + odd < t.rows && c < p.outer)
-        *reinterpret_cast<uint32_t*>(dst + static_cast<int64_t>(u * kUnit + j) * p.outer) = w;
-    }
-  return true;
+  if constexpr (kU == 0) {
+    return true;
+  } else if constexpr (kForm == kGated) {
+    return gated_store<kU>(p, s, t, x, acc[0], acc[1], j0, q, lane, wait_ns);
+  } else {
+    const int32_t c = t.c0 + 32 * q + (lane & ~1);
+    store_bf16<kU>(acc[0], p.out + static_cast<int64_t>(t.m0 + j0 + (lane & 1)) * p.outer + c, p.outer,
+                   t.rows - j0, c < p.outer, lane);
+    return true;
+  }
 }
 
-template <bool kT>
+template <int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                const Params p) {
+  using Z = Sizes<kForm>;
+  constexpr bool kT = is_transposed(kForm);
+  constexpr int kTok = Z::kTok, kStages = Z::kStages, kBufs = Z::kBufs;
   extern __shared__ uint8_t smem_raw[];
-  Smem& s = *reinterpret_cast<Smem*>(smem_raw + (-smem_addr(smem_raw) & 1023u));
+  Smem<kForm>& s = *reinterpret_cast<Smem<kForm>*>(smem_raw + (-smem_addr(smem_raw) & 1023u));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   const uint64_t wait_ns = 4 * p.timeout_ns;
@@ -167,6 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.fac_empty[i], kEpiWarps);
     }
     mbar_init(&s.drain, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&s.pair[i], 4);
     fence_mbar_init();
   }
   grid_wait();
@@ -190,18 +307,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
       const Tile t = tile_of(p, s.tiles, i, kTok, kCols, lane);
-      const int32_t units = units_of(t);
-      const uint32_t bytes = kWBytes + units * (kUnit * kBlock);
-      for (int32_t k = 0; k < p.inner; k += kBlock) {
+      const int32_t units = units_of<kForm>(t);
+      const uint32_t bytes = Z::kMats * kWBytes + units * (kUnit * kBlock);
+      for (int32_t kb = 0; kb < p.kbs; ++kb) {
+        const int32_t k = column_of<kForm>(p, kb), half = half_of<kForm>(p, kb);
         ok = mbar_wait_warp(done + st * 8, (use & 1) ^ 1u, wait_ns, p.err);
         if (!ok) break;
         if (elect_one()) {
           uint8_t* base = s.stage[st];
           mbar_arrive_expect_tx(&s.full[st], bytes);
-          tma_load_3d(base, &wmap, kT ? t.c0 : k, kT ? k : t.c0, t.g, &s.full[st], pol_w);
-          for (int u = 0; u < units; ++u)
-            tma_load_2d(base + kWBytes + u * (kUnit * kBlock), &amap, k, t.m0 + u * kUnit,
-                        &s.full[st], pol_a);
+          for (int i = 0; i < Z::kMats; ++i) {
+            const int32_t w = kForm == kGated ? 2 * t.g + i : kForm == kGatedGrad ? 2 * t.g + half : t.g;
+            tma_load_3d(base + i * kWBytes, &wmap, kT ? t.c0 : k, kT ? k : t.c0, w, &s.full[st], pol_w);
+          }
+          for (int u = 0; u < units; ++u) {
+            uint8_t* const to = base + Z::kMats * kWBytes + u * (kUnit * kBlock);
+            if (kForm == kGatedGrad)
+              tma_load_3d(to, &amap, k, half, t.m0 + u * kUnit, &s.full[st], pol_a);
+            else
+              tma_load_2d(to, &amap, k, t.m0 + u * kUnit, &s.full[st], pol_a);
+          }
         }
         __syncwarp();
         if (++st == kStages) {
@@ -225,24 +350,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, issued = false;
     for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
       const Tile t = tile_of(p, s.tiles, i, kTok, kCols, lane);
-      const uint32_t n = __shfl_sync(0xffffffffu, units_of(t) * kUnit, 0);
+      const uint32_t n = __shfl_sync(0xffffffffu, units_of<kForm>(t) * kUnit, 0);
       // D fp32, e4m3 x e4m3, M = 128, A MN-major if transposed, N = n
       const uint32_t idesc = (1u << 4) | (kT ? 1u << 15 : 0u) | ((n >> 3) << 17) | (8u << 24);
-      for (int32_t left = p.inner; left > 0; left -= kBlock) {
+      for (int32_t kb = 0; kb < p.kbs; ++kb) {
+        const int32_t left = p.inner - column_of<kForm>(p, kb);
         ok = mbar_wait_warp(acc_empty + b * 8, (use & 1) ^ 1u, wait_ns, p.err) &&
              mbar_wait_warp(full + st * 8, st_use & 1, wait_ns, p.err);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t d = tmem + b * kTok, w0 = stage0 + st * kStageBytes;
-          uint64_t wd = operand_desc_sw128(w0);
-          uint64_t ad = operand_desc_sw128(w0 + kWBytes);
-          tc_mma_e4m3<false>(d, wd, ad, idesc);
+          const uint32_t d0 = tmem + b * Z::kAccCols, w0 = stage0 + st * Z::kStageBytes;
 #pragma unroll
-          for (int j = 1; j < kBlock / kSubK; ++j) {
-            wd += wstep;
-            ad += kSubK >> 4;
-            if (j * kSubK < left) tc_mma_e4m3<true>(d, wd, ad, idesc);
+          for (int i = 0; i < Z::kMats; ++i) {
+            const uint32_t d = d0 + i * kTok;
+            uint64_t wd = operand_desc_sw128(w0 + i * kWBytes);
+            uint64_t ad = operand_desc_sw128(w0 + Z::kMats * kWBytes);
+            tc_mma_e4m3<false>(d, wd, ad, idesc);
+#pragma unroll
+            for (int j = 1; j < kBlock / kSubK; ++j) {
+              wd += wstep;
+              ad += kSubK >> 4;
+              if (j * kSubK < left) tc_mma_e4m3<true>(d, wd, ad, idesc);
+            }
           }
           tc_commit(&s.done[st]);
         }
@@ -267,17 +397,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kEpiWarps + 2) {
     // ---------------------------------------------------------- factors --
     // the scales of an entry are loaded while the one before is worked on
-    float v[kTok / 32][kScaleKb] = {}, w[kScaleKb];
+    float v[kTok / 32][kScaleKb] = {}, w[Z::kMats][kScaleKb];
     int32_t i = blockIdx.x, kb = 0, rows = 0;
     Tile t = {};
     auto load = [&]() {  // the entry (tile i, 128-blocks kb ..)
       if (kb == 0) t = tile_of(p, s.tiles, i, kTok, kCols, lane);
       rows = min(t.rows, kTok);
-      const float* sb = p.sb + t.g * p.sb_expert +
-                        static_cast<int64_t>(min(t.c0 / kBlock, p.sb_last)) * p.sb_c;
 #pragma unroll
-      for (int u = 0; u < kScaleKb; ++u)
-        w[u] = __ldg(sb + static_cast<int64_t>(min(kb + u, p.kbs - 1)) * p.sb_k);
+      for (int m = 0; m < Z::kMats; ++m) {
+        const float* sb = p.sb + (kForm == kGated ? 2 * t.g + m : t.g) * p.sb_expert +
+                          static_cast<int64_t>(min(t.c0 / kBlock, p.sb_last)) * p.sb_c;
+#pragma unroll
+        for (int u = 0; u < kScaleKb; ++u)
+          w[m][u] = __ldg(sb + static_cast<int64_t>(min(kb + u, p.kbs - 1)) * p.sb_k);
+      }
 #pragma unroll
       for (int j = 0; j < kTok / 32; ++j) {
         if (lane + 32 * j >= rows) break;
@@ -299,13 +432,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     if (i < tiles) load();
     while (i < tiles) {
-      float f[kTok / 32][kScaleKb];
+      float f[Z::kMats][kTok / 32][kScaleKb];
 #pragma unroll
-      for (int u = 0; u < kScaleKb; ++u) {
-        const float rw = rcp_approx(w[u]);
+      for (int u = 0; u < kScaleKb; ++u)
 #pragma unroll
-        for (int j = 0; j < kTok / 32; ++j) f[j][u] = __fmul_rn(rcp_approx(v[j][u]), rw);
-      }
+        for (int m = 0; m < Z::kMats; ++m) {
+          const float rw = rcp_approx(w[m][u]);
+#pragma unroll
+          for (int j = 0; j < kTok / 32; ++j) f[m][j][u] = __fmul_rn(rcp_approx(v[j][u]), rw);
+        }
       const int32_t have = rows;
       kb += kScaleKb;
       if (kb >= p.kbs) {
@@ -319,7 +454,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < kTok / 32; ++j)
         if (lane + 32 * j < have)
 #pragma unroll
-          for (int u = 0; u < kScaleKb; ++u) s.factor[r][u][lane + 32 * j] = f[j][u];
+          for (int m = 0; m < Z::kMats; ++m)
+#pragma unroll
+            for (int u = 0; u < kScaleKb; ++u) s.factor[r][u][m * kTok + lane + 32 * j] = f[m][j][u];
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.fac_full[r]);
       if (++r == kScaleRing) {
@@ -331,18 +468,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------- epilogue --
     const int q = warp & 3;
     const uint32_t tmem0 = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    const int32_t j0 = (warp >> 2) * kWarpTok;
+    const int32_t j0 = (warp >> 2) * Z::kWarpTok;
+    constexpr int kMost = Z::kWarpTok / kUnit;
     Rings x;
     x.hold = p.skip_arrival && blockIdx.x == 0;
     bool ok = true;
     for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
       const Tile t = tile_of(p, s.tiles, i, kTok, kCols, lane);
-      switch (min(units_of(t) - j0 / kUnit, kWarpTok / kUnit)) {
-        case 4: ok = tile_body<4>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
-        case 3: ok = tile_body<3>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
-        case 2: ok = tile_body<2>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
-        case 1: ok = tile_body<1>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
-        default: ok = tile_body<0>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+      switch (min(units_of<kForm>(t) - j0 / kUnit, kMost)) {
+        case 4: ok = tile_body<kForm, (kMost < 4 ? kMost : 4)>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 3: ok = tile_body<kForm, (kMost < 3 ? kMost : 3)>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 2: ok = tile_body<kForm, 2>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 1: ok = tile_body<kForm, 1>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        default: ok = tile_body<kForm, 0>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
       }
     }
     tc_fence_before();
@@ -357,31 +495,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-gq_status setup_few(DeviceInfo& info) {
-  (void)info;
-  for (const void* f : {reinterpret_cast<const void*>(few_kernel<false>),
-                        reinterpret_cast<const void*>(few_kernel<true>)}) {
-    const gq_status st = check_cuda(
-        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmemBytes)),
-        "grouped_mm: shared memory size");
-    if (st != GQ_OK) return st;
-  }
-  return GQ_OK;
+namespace {
+
+template <int kForm>
+gq_status setup_form() {
+  return check_cuda(cudaFuncSetAttribute(few_kernel<kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem_bytes<kForm>())),
+                    "grouped_mm: shared memory size");
 }
 
-gq_status launch_few(const DeviceInfo& info, Params p, const void* qa, const void* qb,
-                     int32_t N, int32_t K, cudaStream_t stream) {
+template <int kForm>
+gq_status launch_form(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,
+                      int32_t K, cudaStream_t stream) {
+  constexpr int kTok = Sizes<kForm>::kTok;
   CUtensorMap amap, wmap;
-  gq_status st = encode_tiled_2d(&amap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(qa),
-                                 static_cast<uint64_t>(p.inner), static_cast<uint64_t>(p.M),
-                                 static_cast<uint64_t>(p.inner), kBlock, kUnit,
-                                 CU_TENSOR_MAP_SWIZZLE_128B);
+  gq_status st = encode_rows(&amap, p, qa, kUnit);
   if (st != GQ_OK) return st;
-  st = encode_tiled_3d(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<void*>(qb),
-                       static_cast<uint64_t>(K), static_cast<uint64_t>(N),
-                       static_cast<uint64_t>(p.E), static_cast<uint64_t>(K),
-                       static_cast<uint64_t>(N) * K, kBlock, kBlock, CU_TENSOR_MAP_SWIZZLE_128B);
+  st = encode_weights(&wmap, p, qb, N, K);
   if (st != GQ_OK) return st;
   p.tiles_c = (p.outer + kCols - 1) / kCols;
   const int64_t most =
@@ -389,9 +519,27 @@ gq_status launch_few(const DeviceInfo& info, Params p, const void* qa, const voi
   if (most > INT32_MAX)
     return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: %lld tiles", static_cast<long long>(most));
   const unsigned grid = static_cast<unsigned>(most < info.sm_count ? most : info.sm_count);
-  const auto kernel = p.transposed ? few_kernel<true> : few_kernel<false>;
-  return launch_chained("grouped_mm: launch", kernel, dim3(grid), kThreads, kSmemBytes, stream, 1,
-                        amap, wmap, p);
+  return launch_chained("grouped_mm: launch", few_kernel<kForm>, dim3(grid), kThreads,
+                        smem_bytes<kForm>(), stream, 1, amap, wmap, p);
+}
+
+}  // namespace
+
+gq_status setup_few() {
+  for (const gq_status st : {setup_form<kForward>(), setup_form<kTransposed>(), setup_form<kGated>(),
+                             setup_form<kGatedGrad>()})
+    if (st != GQ_OK) return st;
+  return GQ_OK;
+}
+
+gq_status launch_few(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,
+                     int32_t K, cudaStream_t stream) {
+  switch (p.form) {
+    case kForward: return launch_form<kForward>(info, p, qa, qb, N, K, stream);
+    case kTransposed: return launch_form<kTransposed>(info, p, qa, qb, N, K, stream);
+    case kGated: return launch_form<kGated>(info, p, qa, qb, N, K, stream);
+    default: return launch_form<kGatedGrad>(info, p, qa, qb, N, K, stream);
+  }
 }
 
 }  // namespace gmm

@@ -37,11 +37,11 @@ gq_status encode_tiled_2d(CUtensorMap* map, CUtensorMapDataType dtype,
                           uint64_t row_stride_bytes, uint32_t box0,
                           uint32_t box1, CUtensorMapSwizzle swizzle);
 
-// Encodes a 3-D tiled tensor map whose boxes are one deep along dim2.
+// Encodes a 3-D tiled tensor map.
 gq_status encode_tiled_3d(CUtensorMap* map, CUtensorMapDataType dtype,
                           void* base, uint64_t dim0, uint64_t dim1, uint64_t dim2,
                           uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t box0,
-                          uint32_t box1, CUtensorMapSwizzle swizzle);
+                          uint32_t box1, CUtensorMapSwizzle swizzle, uint32_t box2 = 1);
 
 // Records a message for gq_last_error() and returns `st`.
 gq_status fail(gq_status st, const char* fmt, ...);
@@ -156,19 +156,20 @@ gq_status setup(DeviceInfo& info);
 gq_status launch(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa, const float* sa,
                  int64_t M, const void* qb, const float* sb, int32_t N, int32_t K, bool transposed,
                  const int32_t* offs, int32_t E, void* out, cudaStream_t stream);
+gq_status launch_gated(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa,
+                       const float* sa, int64_t M, const void* qb, const float* sb, int32_t N,
+                       int32_t K, int activation, const int32_t* offs, int32_t E, void* out,
+                       void* q, float* scales, void* pre, bool pow2, cudaStream_t stream);
+gq_status launch_gated_grad(const DeviceInfo& info, const DebugKnobs& dbg, const void* qd,
+                            const float* sd, int64_t M, const void* qb, const float* sb, int32_t N,
+                            int32_t K, const int32_t* offs, int32_t E, void* out,
+                            cudaStream_t stream);
 }  // namespace gmm
 
 namespace gated {
 gq_status launch_backward(const void* g, const void* pre, bool f32, int64_t rows, int64_t N,
                           int64_t ld, int activation, void* out, void* q, float* scales, bool pow2,
                           cudaStream_t stream);
-gq_status launch_forward(const DeviceInfo& info, const DebugKnobs& dbg, const void* qa,
-                         const float* sa, int64_t M, const void* qb, const float* sb, int32_t N,
-                         int32_t K, int activation, const int32_t* offs, int32_t E, void* out,
-                         void* q, float* scales, void* pre, bool pow2, cudaStream_t stream);
-gq_status launch_grad(const DeviceInfo& info, const DebugKnobs& dbg, const void* qd,
-                      const float* sd, int64_t M, const void* qb, const float* sb, int32_t N,
-                      int32_t K, const int32_t* offs, int32_t E, void* out, cudaStream_t stream);
 }  // namespace gated
 
 namespace clip {

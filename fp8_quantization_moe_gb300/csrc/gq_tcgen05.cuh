@@ -242,6 +242,9 @@ __device__ __forceinline__ float lds32_ordered(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void sts32(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 // 16-byte shared load ordered after the warp's preceding shared stores.
 __device__ __forceinline__ uint4 lds128_ordered(uint32_t addr) {
   uint4 v;
