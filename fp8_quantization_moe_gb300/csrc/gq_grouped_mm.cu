@@ -1,15 +1,19 @@
-// gq_grouped_mm.cu -- the grouped product of block-quantized rows with
+// gq_grouped_mm.cu -- the grouped products of block-quantized rows with
 // block-quantized stacked weights, one expert per token group, on the
 // sm_103a tensor cores (tcgen05, TMEM accumulators, TMA operands):
 //   forward     out[m][n] = sum_k A[m][k] * W[e][n][k]
 //   transposed  out[m][k] = sum_n A[m][n] * W[e][n][k]
+//   gated       h[m][n] = act(sum_k A[m][k] W[e][0][n][k]) * sum_k A[m][k] W[e][1][n][k]
+//   gated grad  out[m][k] = sum_n A[m][0][n] W[e][0][n][k] + A[m][1][n] W[e][1][n][k]
 // with A = qa / sa (one scale per row and 128 contraction columns) and
 // W = qb / sb (one scale per 128x128 block).  Within a 128-block kb of the
 // contraction both scales are constant for a row m and 128 output columns c,
 //   out[m][c] = sum_kb ( 1/sa[m][kb] * 1/sb[e][c/128, kb] ) * P_kb[m][c],
 // P_kb the plain sum of the block's e4m3 products.  The tensor cores form
 // P_kb in TMEM (fp32); the epilogue warps read it, multiply by the factor
-// and add it to fp32 accumulators in registers, rounded to bf16 once.
+// and add it to fp32 accumulators in registers, rounded once.  The gated
+// tile is 128 columns of both projections, so that activation, product and
+// the 1x128 quantization need nothing but the tile.
 //
 // A block takes tiles of 128 rows x 256 output columns, 128 contraction
 // columns at a time.  The rows are the MMA's M operand, so that a TMEM lane
@@ -17,25 +21,31 @@
 // need every row's factor, and those loads alone -- shared memory returns 128
 // bytes a cycle -- would cost as much as the MMAs.
 //
-// What bounds it: the tensor cores work for 512 of a 128-block's 860 cycles.
-// With two accumulators, all of TMEM, the MMAs wait for the epilogue: without
-// its multiply-adds (half of the FMA pipe's time at the tensor cores' full
-// rate) a 128-block would take 720 cycles, without the stores 780: a tile's 64
-// KB leave the SM at 32 bytes a cycle, and for those 2000 cycles the MMAs run
-// ahead by two 128-blocks at most.  Without multiply-adds and TMEM loads 700 are
-// left, 188 above the MMAs; what of that the stores do not explain is not known.
-// 16,640 rows of 16 groups, K 4096 to N 8192: 460 us, 2.43 PFLOP/s; transposed,
-// 32,768 rows of 64 groups, N 2048 to K 4096: 265 us, 2.07 PFLOP/s; in a long
-// run, at the power limit's clock, 515 to 540 and 295 to 311 us.  Blocks in pairs
-// that share the weights' loads (cta_group::2) release accumulators across
-// blocks and pad the groups to 256 rows: 505 and 316 us when this kernel took
-// 485 and 284 (long runs 536 and 330 against 528 and 304); they were not
-// measured with what has made it faster since.
+// What bounds it, 16,640 rows in 16 groups (16 matrices of 8192 x 4096):
+// * a long run, the power limit: the clock falls to 1.5 GHz where it is 1.8 for
+//   a single call.  grad_input of the gated block 500 us (2.2 PFLOP/s), of which
+//   420 are left without multiply-adds, TMEM loads and stores;
+// * one call, 811 cycles a 128-block, 455 us: the MMAs are 512 and the operands
+//   770, 48 KB at the 64 bytes a cycle that L2 delivers to an SM.  A pair of
+//   blocks (cta_group::2) loads 32 KB per block, but its accumulators are
+//   released across blocks, and with two of them, all of TMEM, that round trip
+//   (1100 cycles: release, first MMA, completion, wake-up) takes the place of the
+//   loads: 860 cycles, and a group is padded to 256 rows.  Halves of the
+//   accumulators released apart (MMAs of N = 128): the same 460 and 490 us;
+//   two issuing warps, three barriers probed ahead: no faster.
+// * rows that are not whole lines, pairs of blocks (see kPairRows): 24,500 live
+//   rows of 40 experts, 1360 x 2064, gated to fp8: 264 -> 195 us, halves released
+//   apart 190.
+// The gated form adds 3200 cycles a tile for the stores of 112 KB (both rows
+// and projections, 32 bytes a cycle) and 2000 for the activation (two MUFU
+// operations a value): 16 x 2 x 4096 x 4096, everything written: 535 us, in a
+// long run 570; the plain product with the same matrices 471 and 509.
 //
 // One persistent block per SM; its warps:
-//   0-7   epilogue: lane quarter w % 4 (32 rows), column half w / 4;
+//   0-7   epilogue: lane quarter w % 4 (32 rows), column half w / 4 (gated: 64
+//         columns of both projections);
 //   8     TMA loads (one lane);
-//   9     TMEM allocation and the MMAs (one lane);
+//   9     TMEM allocation and the MMAs (one lane, of a pair the first block's);
 //   10-11 the factors 1/sa * 1/sb, 64 rows each, four 128-blocks at a time,
 //         into a ring in shared memory.
 // Every mbarrier wait is bounded; on expiry the error word is set, the warp
@@ -49,13 +59,11 @@ namespace gq {
 namespace gmm {
 namespace {
 
-constexpr int kRows = 128;        // rows of a tile
+constexpr int kRows = 128;        // rows of a tile, per block
 constexpr int kCols = 256;        // output columns of a tile
 constexpr int kBoxRows = 32;      // rows per TMA box where a tile has few
-constexpr int kStages = 4;
-constexpr int kABytes = kRows * kBlock;        // 16 KB
-constexpr int kWHalf = kCols / 2 * kBlock;     // 16 KB: 128 output columns
-constexpr int kStageBytes = kABytes + 2 * kWHalf;
+constexpr int kABytes = kRows * kBlock;      // 16 KB
+constexpr int kWHalf = kCols / 2 * kBlock;   // 16 KB: half of the output columns
 constexpr int kBufs = 2;          // accumulators in TMEM
 constexpr uint32_t kTmemCols = kBufs * kCols;
 constexpr int kEpiWarps = 8;      // two per TMEM lane quarter
@@ -68,28 +76,105 @@ constexpr int kScaleKb = 4;       // 128-blocks per entry of the factor ring
 constexpr int kScaleRing = 2;
 static_assert(kTmemCols == 512 && kChunks == 4, "two accumulators fill the TMEM");
 
+// Blocks that share a tile: one, with all of its output columns' weights, or
+// two (a pair, cta_group::2), each with half of them.
+template <int kBlocks>
 struct Smem {
+  static constexpr int kStages = kBlocks == 2 ? 6 : 4;
+  static constexpr int kStageBytes = kABytes + 2 / kBlocks * kWHalf;
   uint8_t stage[kStages][kStageBytes];  // 1024-byte aligned (swizzle atoms)
   float factor[kScaleRing][kScaleKb][2][kRows];  // of the tile's two column halves
-  int4 tile[kScaleRing];         // the entry's tile: first row, rows, first column
-  uint32_t cols[kStages];        // output columns of the stage's tile
+  int4 tile[kScaleRing];         // the entry's tile: first row and rows of this block, first column
+  int32_t cols[kStages];         // half_cols of the stage's tile
   TileTable tiles;
-  uint64_t full[kStages];         // the stage's loads
+  uint64_t full[kStages];         // the stage's loads in every block (the first block)
   uint64_t done[kStages];         // its MMAs are complete: the stage is free, the accumulator full
-  uint64_t acc_empty[kBufs];      // accumulator read (8 warps)
+  uint64_t acc_empty[kBufs];      // accumulator read (8 warps of every block; the first block)
   uint64_t fac_full[kScaleRing];  // factors written (2 warps)
   uint64_t fac_empty[kScaleRing]; // factors read (8 warps)
   uint64_t drain;
-  uint64_t pair[4];               // kGated: both halves of a row have their maximum (2 warps)
+  uint64_t share[4];              // kGated: both halves of a row have their maximum (2 warps)
   float most[2][2][kRows];        // kGated: those maxima, by tile parity and half
   uint32_t tmem_base;
 };
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "fits one SM's shared memory");
+template <int kBlocks>
+constexpr size_t smem_bytes() {
+  static_assert(sizeof(Smem<kBlocks>) + 1024 <= 227 * 1024, "fits one SM's shared memory");
+  return sizeof(Smem<kBlocks>) + 1024;
+}
 
-// TMA boxes of kBoxRows rows for a tile's rows (4: one box of kRows).
-__device__ __forceinline__ int32_t boxes_of(const Tile& t) {
-  return (min(t.rows, kRows) + kBoxRows - 1) / kBoxRows;
+// The tensor-core and TMA instructions for a block alone or in a pair.  `bar`
+// and acc_empty of a pair are the first block's, as shared::cluster addresses.
+template <int kBlocks>
+struct Group;
+
+template <>
+struct Group<1> {
+  static __device__ __forceinline__ uint32_t of_first(uint32_t addr) { return addr; }
+  static __device__ __forceinline__ void alloc(uint32_t* dst) {
+    tmem_alloc(dst, kTmemCols);
+    tmem_relinquish();
+  }
+  static __device__ __forceinline__ void dealloc(uint32_t addr) { tmem_dealloc(addr, kTmemCols); }
+  static __device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, int32_t x,
+                                                 int32_t y, uint32_t bar, uint64_t pol) {
+    tma_load_2d_addr(dst, map, x, y, bar, pol);
+  }
+  static __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int32_t x,
+                                                 int32_t y, int32_t z, uint32_t bar, uint64_t pol) {
+    tma_load_3d_addr(dst, map, x, y, z, bar, pol);
+  }
+  template <bool kAccumulate>
+  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    tc_mma_e4m3<kAccumulate>(d, a, b, idesc);
+  }
+  static __device__ __forceinline__ void commit(uint64_t* bar) { tc_commit(bar); }
+  static __device__ __forceinline__ void commit_first(uint64_t* bar) { tc_commit(bar); }
+  static __device__ __forceinline__ void release(uint32_t bar) { mbar_arrive_addr(bar); }
+  static __device__ __forceinline__ void sync() {}
+};
+
+template <>
+struct Group<2> {
+  static __device__ __forceinline__ uint32_t of_first(uint32_t addr) { return map_cluster(addr, 0); }
+  static __device__ __forceinline__ void alloc(uint32_t* dst) {
+    tmem_alloc_pair(dst, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  static __device__ __forceinline__ void dealloc(uint32_t addr) { tmem_dealloc_pair(addr, kTmemCols); }
+  static __device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, int32_t x,
+                                                 int32_t y, uint32_t bar, uint64_t pol) {
+    tma_load_2d_pair(dst, map, x, y, bar, pol);
+  }
+  static __device__ __forceinline__ void load_3d(void* dst, const CUtensorMap* map, int32_t x,
+                                                 int32_t y, int32_t z, uint32_t bar, uint64_t pol) {
+    tma_load_3d_pair(dst, map, x, y, z, bar, pol);
+  }
+  template <bool kAccumulate>
+  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    tc_mma_e4m3_pair<kAccumulate>(d, a, b, idesc);
+  }
+  static __device__ __forceinline__ void commit(uint64_t* bar) { tc_commit_pair(bar, 3); }
+  static __device__ __forceinline__ void commit_first(uint64_t* bar) { tc_commit_pair(bar, 1); }
+  static __device__ __forceinline__ void release(uint32_t bar) { mbar_arrive_cluster(bar); }
+  static __device__ __forceinline__ void sync() {
+    cluster_arrive();
+    cluster_wait();
+  }
+};
+
+// TMA boxes of kBoxRows rows for a block's rows (4: one box of kRows).
+__device__ __forceinline__ int32_t boxes_of(int32_t rows) {
+  return (max(min(rows, kRows), 0) + kBoxRows - 1) / kBoxRows;
+}
+
+// The MMA's N for a tile: its output columns, of a pair in equal halves of whole
+// 16s; kGated: 128 of each projection, what lies behind the last reads zeros.
+template <int kForm, int kBlocks>
+__device__ __forceinline__ int32_t mma_cols(const Params& p, int32_t c0) {
+  const int32_t left = p.outer - c0;
+  if (kForm == kGated || left >= kCols) return kCols;
+  return kBlocks == 2 ? (left + 31) / 32 * 32 : left;
 }
 
 // acc += h * f, h the bits of fp32 values, two at a time.  A packed multiply-
@@ -146,7 +231,7 @@ __device__ __forceinline__ void store_bf16(const float (&v)[kChunk], uint16_t* o
   store_parts(x, reinterpret_cast<uint8_t*>(out), pitch * 2, rows, c_ok, lane);
 }
 
-template <int kForm>
+template <int kForm, int kBlocks>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap amap32,
@@ -155,10 +240,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kT = is_transposed(kForm);
   // output columns of a tile; kGated: as many of each projection
   constexpr int kTileCols = kForm == kGated ? kCols / 2 : kCols;
+  constexpr int kTileRows = kBlocks * kRows;
+  using G = Group<kBlocks>;
+  constexpr int kStages = Smem<kBlocks>::kStages, kStageBytes = Smem<kBlocks>::kStageBytes;
   extern __shared__ uint8_t smem_raw[];
-  Smem& s = *reinterpret_cast<Smem*>(smem_raw + (-smem_addr(smem_raw) & 1023u));
+  Smem<kBlocks>& s = *reinterpret_cast<Smem<kBlocks>*>(smem_raw + (-smem_addr(smem_raw) & 1023u));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
+  const int32_t rank = kBlocks == 2 ? static_cast<int32_t>(cluster_rank()) : 0;
+  const int32_t groups = gridDim.x / kBlocks, group = blockIdx.x / kBlocks;
   const uint64_t wait_ns = 4 * p.timeout_ns;
 
   if (warp == kEpiWarps && lane == 0) {
@@ -170,24 +260,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.full[i], 1);
       mbar_init(&s.done[i], 1);
     }
-    for (int b = 0; b < kBufs; ++b) mbar_init(&s.acc_empty[b], kEpiWarps);
+    for (int b = 0; b < kBufs; ++b) mbar_init(&s.acc_empty[b], kBlocks * kEpiWarps);
     for (int i = 0; i < kScaleRing; ++i) {
       mbar_init(&s.fac_full[i], 2);
       mbar_init(&s.fac_empty[i], kEpiWarps);
     }
     mbar_init(&s.drain, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&s.pair[i], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&s.share[i], 2);
     fence_mbar_init();
   }
   grid_wait();
   if (warp == kEpiWarps) {
-    build_tiles(p, kRows, s.tiles, lane);
+    build_tiles(p, kTileRows, s.tiles, lane);
   } else if (warp == kEpiWarps + 1) {
-    tmem_alloc(&s.tmem_base, kTmemCols);
-    tmem_relinquish();
+    G::alloc(&s.tmem_base);
   }
   tc_fence_before();
   __syncthreads();
+  G::sync();  // the other block's barriers are ready as well
   tc_fence_after();
   const uint32_t tmem = s.tmem_base;
   const int32_t tiles = s.tiles.first[p.E] * p.tiles_c;  // below 2^31: the host checks
@@ -197,33 +287,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kEpiWarps) {
       // ---------------------------------------------------------- loads --
       const uint64_t pol = policy_evict_normal();
-      const uint32_t done = smem_addr(s.done);
+      const uint32_t done = smem_addr(s.done), full = G::of_first(smem_addr(s.full));
       uint32_t st = 0, use = 0;  // stage, its use
       bool ok = true;
-      for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
-        const Tile t = tile_of(p, s.tiles, i, kRows, kTileCols, lane);
-        const int32_t boxes = boxes_of(t);
-        const uint32_t bytes = 2 * kWHalf + static_cast<uint32_t>(boxes) * (kBoxRows * kBlock);
+      for (int32_t i = group; ok && i < tiles; i += groups) {
+        const Tile t = tile_of(p, s.tiles, i, kTileRows, kTileCols, lane);
+        const int32_t boxes = boxes_of(t.rows - rank * kRows), m0 = t.m0 + rank * kRows;
+        const int32_t cols = mma_cols<kForm, kBlocks>(p, t.c0);
+        int32_t rows32 = boxes;  // of all blocks
+        if (kBlocks == 2) rows32 = boxes_of(t.rows) + boxes_of(t.rows - kRows);
+        const uint32_t bytes = 2 * kWHalf + static_cast<uint32_t>(rows32) * (kBoxRows * kBlock);
         for (int32_t kb = 0; kb < p.kbs; ++kb) {
           const int32_t k = column_of<kForm>(p, kb), half = half_of<kForm>(p, kb);
           ok = mbar_wait_warp(done + st * 8, (use & 1) ^ 1u, wait_ns, p.err);
           if (!ok) break;
           if (elect_one()) {
             uint8_t* base = s.stage[st];
-            uint64_t* bar = &s.full[st];
-            s.cols[st] = min(kTileCols, p.outer - t.c0);
-            mbar_arrive_expect_tx(bar, bytes);
-            for (int h = 0; h < 2; ++h) {
-              const int32_t c = kForm == kGated ? t.c0 : t.c0 + h * kCols / 2;
+            const uint32_t bar = full + st * 8;
+            if (rank == 0) {  // the bytes of every block complete on the first one's barrier
+              s.cols[st] = cols;
+              mbar_arrive_expect_tx(&s.full[st], bytes);
+            }
+#pragma unroll
+            for (int j = 0; j < 2 / kBlocks; ++j) {
+              const int32_t h = kBlocks == 2 ? rank : j;  // which half of the columns
+              const int32_t c = kForm == kGated ? t.c0 : t.c0 + h * (kBlocks == 2 ? cols / 2 : kCols / 2);
               const int32_t w = kForm == kGated ? 2 * t.g + h : kForm == kGatedGrad ? 2 * t.g + half : t.g;
-              tma_load_3d(base + kABytes + h * kWHalf, &wmap, kT ? c : k, kT ? k : c, w, bar, pol);
+              G::load_3d(base + kABytes + j * kWHalf, &wmap, kT ? c : k, kT ? k : c, w, bar, pol);
             }
             auto load_rows = [&](const CUtensorMap* map, int32_t row) {
               uint8_t* const to = base + row * kBlock;
               if (kForm == kGatedGrad)
-                tma_load_3d(to, map, k, half, t.m0 + row, bar, pol);
+                G::load_3d(to, map, k, half, m0 + row, bar, pol);
               else
-                tma_load_2d(to, map, k, t.m0 + row, bar, pol);
+                G::load_2d(to, map, k, m0 + row, bar, pol);
             };
             if (boxes == kRows / kBoxRows)
               load_rows(&amap, 0);
@@ -237,61 +334,47 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // the block must not exit while a load is still writing its memory, also
+      // neither block may exit while a load is still writing its memory, also
       // after a wait that ran out; the MMAs that read it are waited for below
-      for (uint32_t u = 0; u < kStages; ++u) {
+      for (uint32_t u = 0; rank == 0 && u < kStages; ++u) {
         const uint32_t uses = use + (u < st ? 1 : 0);
         if (uses > 0) mbar_wait_warp(smem_addr(&s.full[u]), (uses - 1) & 1, wait_ns, p.err);
       }
     } else if (warp == kEpiWarps + 1) {
       // ----------------------------------------------------------- MMAs --
-      // One lane from here on, waits included: between the last release of an
-      // accumulator and the next MMA there is little else to issue.
-      if (elect_one()) {
+      // One lane of the first block from here on, waits included: between the
+      // last release of an accumulator and the next MMA there is little else to
+      // issue.
+      if (rank == 0 && elect_one()) {
         const uint32_t acc_empty = smem_addr(s.acc_empty), full = smem_addr(s.full);
         const uint32_t stage0 = smem_addr(s.stage);
         constexpr uint32_t wstep = kT ? (kSubK * kBlock) >> 4 : kSubK >> 4;
         uint32_t st = 0, st_use = 0, b = 0, use = 0;  // stage and accumulator, their uses
         bool ok = true, issued = false;
-        for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+        for (int32_t i = group; ok && i < tiles; i += groups) {
           uint32_t idesc = 0;
-          bool apart = false;
           for (int32_t kb = 0; kb < p.kbs; ++kb) {
             const int32_t left = p.inner - column_of<kForm>(p, kb);
             // rows: K-major; weights: K-major rows of 128 bytes, or MN-major
-            // (32 contraction rows = 4 KB, the column halves kWHalf apart)
+            // (32 contraction rows = 4 KB, one block's halves of the columns kWHalf apart)
             const uint32_t d = tmem + b * kCols, a0 = stage0 + st * kStageBytes;
             uint64_t ad = operand_desc_sw128(a0);
             uint64_t wd = operand_desc_sw128(a0 + kABytes, kWHalf);
             ok = mbar_wait_addr(full + st * 8, st_use & 1, wait_ns, p.err) &&
                  mbar_wait_addr(acc_empty + b * 8, (use & 1) ^ 1u, wait_ns, p.err);
             if (!ok) break;
-            if (kb == 0) {
-              // the tile's columns: a multiple of 16, as the MMA's N has to be
-              uint32_t n = s.cols[st];
-              if (kForm == kGated) {
-                // one MMA for both projections, or two where the tile is narrower
-                apart = n < kTileCols;
-                if (!apart) n = kCols;
-              }
-              // D fp32, e4m3 x e4m3, B MN-major if transposed, N = n, M = 128
-              idesc = (1u << 4) | (kT ? 1u << 16 : 0u) | ((n >> 3) << 17) | (8u << 24);
-            }
+            if (kb == 0)  // D fp32, e4m3 x e4m3, B MN-major if transposed, N, M
+              idesc = (1u << 4) | (kT ? 1u << 16 : 0u) | (static_cast<uint32_t>(kTileRows >> 4) << 24) |
+                      ((static_cast<uint32_t>(s.cols[st]) >> 3) << 17);
             tc_fence_after();
-            tc_mma_e4m3<false>(d, ad, wd, idesc);
-            if (kForm == kGated && apart)
-              tc_mma_e4m3<false>(d + kTileCols, ad, wd + (kWHalf >> 4), idesc);
+            G::template mma<false>(d, ad, wd, idesc);
 #pragma unroll
             for (int j = 1; j < kBlock / kSubK; ++j) {
               ad += kSubK >> 4;
               wd += wstep;
-              if (j * kSubK < left) {
-                tc_mma_e4m3<true>(d, ad, wd, idesc);
-                if (kForm == kGated && apart)
-                  tc_mma_e4m3<true>(d + kTileCols, ad, wd + (kWHalf >> 4), idesc);
-              }
+              if (j * kSubK < left) G::template mma<true>(d, ad, wd, idesc);
             }
-            tc_commit(&s.done[st]);
+            G::commit(&s.done[st]);
             issued = true;
             if (++b == kBufs) {
               b = 0;
@@ -305,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // every MMA is complete before the TMEM is freed
         if (issued) {
-          tc_commit(&s.drain);
+          G::commit_first(&s.drain);
           mbar_wait_addr(smem_addr(&s.drain), 0, wait_ns, p.err);
         }
       }
@@ -317,10 +400,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // would queue up at a single L2 line).
       const int32_t first = (warp - kEpiWarps - 2) * 64 + lane;
       float v[2][kScaleKb] = {}, ws[2][kScaleKb];
-      int32_t i = blockIdx.x, kb = 0;
+      int32_t i = group, kb = 0;
       Tile t = {};
       auto load = [&]() {  // the entry (tile i, 128-blocks kb ..)
-        if (kb == 0) t = tile_of(p, s.tiles, i, kRows, kTileCols, lane);
+        if (kb == 0) {
+          t = tile_of(p, s.tiles, i, kTileRows, kTileCols, lane);
+          t.m0 += rank * kRows;
+          t.rows -= rank * kRows;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int32_t w = kForm == kGated ? 2 * t.g + h : t.g;
@@ -373,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         kb += kScaleKb;
         if (kb >= p.kbs) {
           kb = 0;
-          i += gridDim.x;
+          i += groups;
         }
         if (i < tiles) load();
       }
@@ -393,11 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     setmaxnreg_inc<kEpiRegs>();
     const int q = warp & 3, hc = warp >> 2;
     const uint32_t done = smem_addr(s.done), fac_full = smem_addr(s.fac_full);
-    const uint32_t acc_empty = smem_addr(s.acc_empty);
+    const uint32_t acc_empty = G::of_first(smem_addr(s.acc_empty));
     constexpr int kMine = kTileCols / 2;  // output columns of this warp
     const uint32_t tmem0 = tmem + (static_cast<uint32_t>(32 * q) << 16) + hc * kMine;
     // where this warp's chunk ch begins in an accumulator
-    auto col = [](int ch) { return kForm == kGated ? (ch >> 1) * kTileCols + (ch & 1) * kChunk : ch * kChunk; };
+    auto col = [](int ch) {
+      return kForm == kGated ? (ch >> 1) * kTileCols + (ch & 1) * kChunk : ch * kChunk;
+    };
     const uint32_t fac = smem_addr(&s.factor[0][0][kForm == kGated ? 0 : hc][32 * q + lane]);
     const uint32_t tile = smem_addr(s.tile);
     constexpr uint32_t kFacKb = 2 * kRows * 4, kFacEntry = kScaleKb * kFacKb;
@@ -405,10 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t st = 0, use = 0;     // the stage whose MMAs filled it, its use
     uint32_t r = 0, fac_use = 0;  // entry of the factor ring, its use
     bool ready = false;           // the next MMAs are known to be complete
-    uint32_t pairs = 0;           // exchanges with the other half's warp so far
+    uint32_t shares = 0;          // exchanges with the other half's warp so far
     bool hold = p.skip_arrival && blockIdx.x == 0;  // withhold the next release
     bool ok = true;
-    for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+    for (int32_t i = group; ok && i < tiles; i += groups) {
       ok = mbar_wait_warp(fac_full + r * 8, fac_use & 1, wait_ns, p.err);
       if (!ok) break;
       const uint4 ti = lds128_ordered(tile + r * 16);
@@ -448,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && !hold) mbar_arrive_addr(acc_empty + b * 8);
+        if (lane == 0 && !hold) G::release(acc_empty + b * 8);
         hold = false;
         b ^= 1;
         if (++st == kStages) {
@@ -494,74 +583,67 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mine) continue;
       const int part = lane & 3;
       const int64_t row = row0 + (lane & ~3);
-      if (kForm != kGated) {
+      if constexpr (kForm != kGated) {
         uint16_t* const orow = p.out + row * p.outer + c + part * 8;
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch)
           store_bf16(acc[ch], orow + ch * kChunk, p.outer, rows,
                      c + ch * kChunk + part * 8 < p.outer, lane);  // outer % 16 == 0
-        continue;
-      }
-      // the projections, as they are
-      if (p.pre != nullptr) {
-        uint16_t* const prow = p.pre + row * 2 * p.outer + c + part * 8;
+      } else {
 #pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch)
-          store_bf16(acc[ch], prow + (ch >> 1) * static_cast<int64_t>(p.outer) + (ch & 1) * kChunk,
-                     2 * static_cast<int64_t>(p.outer), rows,
-                     c + (ch & 1) * kChunk + part * 8 < p.outer, lane);
-      }
+        for (int ch = 0; ch < 2; ++ch) {
+          const int32_t at = c + ch * kChunk + part * 8;
+          const bool in = at < p.outer;  // outer % 16 == 0
+          if (p.pre != nullptr) {  // the projections, as they are
+            uint16_t* const prow = p.pre + row * 2 * p.outer + at;
+            store_bf16(acc[ch], prow, 2 * static_cast<int64_t>(p.outer), rows, in, lane);
+            store_bf16(acc[ch + 2], prow + p.outer, 2 * static_cast<int64_t>(p.outer), rows, in, lane);
+          }
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch)
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) acc[ch][j] = gated_value(p, acc[ch][j], acc[ch + 2][j]);
-      if (p.out != nullptr) {
-        uint16_t* const orow = p.out + row * p.outer + c + part * 8;
+          for (int j = 0; j < kChunk; ++j) acc[ch][j] = gated_value(p, acc[ch][j], acc[ch + 2][j]);
+          if (p.out != nullptr) store_bf16(acc[ch], p.out + row * p.outer + at, p.outer, rows, in, lane);
+        }
+        if (p.q == nullptr) continue;
+        // a 1x128 block is this warp's row and that of the warp of the other half
+        // of the columns: they exchange their maxima (a NaN does not count; columns
+        // past the last are zeros)
+        float most = 0.0f;
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch)
-          store_bf16(acc[ch], orow + ch * kChunk, p.outer, rows,
-                     c + ch * kChunk + part * 8 < p.outer, lane);
-      }
-      if (p.q == nullptr) continue;
-      // a 1x128 block is this warp's row and that of the warp of the other half
-      // of the columns: they exchange their maxima (a NaN does not count;
-      // columns past the last hold anything)
-      float most = 0.0f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (c + 16 * u < p.outer)  // outer % 16 == 0
-#pragma unroll
-          for (int j = 0; j < 16; ++j) most = fmaxf(most, fabsf(acc[u >> 1][(u & 1) * 16 + j]));
-      if (static_cast<int32_t>(ti.z) + kMine < p.outer) {
-        const uint32_t buf = smem_addr(&s.most[pairs & 1][0][32 * q + lane]);
-        sts32(buf + hc * kRows * 4, most);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.pair[q]);
-        ok = mbar_wait_warp(smem_addr(&s.pair[q]), pairs & 1, wait_ns, p.err);
-        if (!ok) break;
-        ++pairs;
-        most = fmaxf(most, lds32_ordered(buf + (hc ^ 1) * kRows * 4));
-      }
-      const float sc = scale_from_amax_bits(__float_as_uint(most), p.pow2);
-      uint32_t x[4][4];
-#pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float* v = &acc[w >> 1][(w & 1) * 16 + 4 * j];
-          x[w][j] = quant4f(make_float4(v[0], v[1], v[2], v[3]), sc);
+          for (int j = 0; j < kChunk; ++j) most = fmaxf(most, fabsf(acc[ch][j]));
+        if (static_cast<int32_t>(ti.z) + kMine < p.outer) {
+          const uint32_t buf = smem_addr(&s.most[shares & 1][0][32 * q + lane]);
+          sts32(buf + hc * kRows * 4, most);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.share[q]);
+          ok = mbar_wait_warp(smem_addr(&s.share[q]), shares & 1, wait_ns, p.err);
+          if (!ok) break;
+          ++shares;
+          most = fmaxf(most, lds32_ordered(buf + (hc ^ 1) * kRows * 4));
         }
-      store_parts(x, p.q + row * p.outer + c + part * 16, p.outer, rows, c + part * 16 < p.outer, lane);
-      if (hc == 0 && lane < rows)
-        p.scales[static_cast<int64_t>(row0 + lane) * ((p.outer + kBlock - 1) / kBlock) + c / kBlock] = sc;
+        const float sc = scale_from_amax_bits(__float_as_uint(most), p.pow2);
+        uint32_t x[4][4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float* v = &acc[w >> 1][(w & 1) * 16 + 4 * j];
+            x[w][j] = quant4f(make_float4(v[0], v[1], v[2], v[3]), sc);
+          }
+        store_parts(x, p.q + row * p.outer + c + part * 16, p.outer, rows, c + part * 16 < p.outer, lane);
+        if (hc == 0 && lane < rows)
+          p.scales[static_cast<int64_t>(row0 + lane) * ((p.outer + kBlock - 1) / kBlock) + c / kBlock] = sc;
+      }
     }
     tc_fence_before();
   }
 
   __syncthreads();
+  G::sync();  // neither block leaves while the other may still signal it
   if (warp == kEpiWarps + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    G::dealloc(tmem);
   }
 }
 
@@ -572,29 +654,73 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   16 of 4096 x 4096           48/49 50/50 52/50 56/52   46/44 47/45 49/46 54/47
 //   8 of 8192 x 2048            25/27 26/27 28/28 33/29   22/31 23/32 25/32 28/33
 //   8 of 2048 x 8192            22/32 23/33 25/34 28/34   25/26 26/26 28/27 33/28
+// The gated form has half as many rows in a tile there: 64 pairs of 1024 x
+// 2048 at 16, 32 and 48 rows 53/50 55/51 63/52, of 1424 x 2064 69/69 80/73 87/76.
 // The rows are those of the buffer, also behind the last group's end.
-constexpr int kFewRows = 48;
+constexpr int kFewRows = 48, kFewRowsGated = 16;
+
+// Block pairs where rows of an operand begin anywhere in a 128-byte line (their
+// length is no multiple of 64 bytes): nearly each 128 bytes of a box are then two
+// lines for L2, and the operands' arrival binds; a pair has each line of the weights
+// loaded once for both blocks.  But it pads groups to 256 rows, so not for few,
+// nor where there are few tiles to share out.  In us, pairs / single blocks, uneven
+// groups of 64, 96, 128, 192 and 512 rows of 64 experts, 1424 x 2064:
+//   gated 102/85 105/103 109/116 134/156 251/342
+//   grad_input of it 93/86 97/107 114/126 138/162 280/375
+//   forward 92/85 97/105 103/121 130/159 274/354, transposed 90/78 92/96 104/113 118/144 234/330
+// With rows of whole lines (64 of 1024 x 2048, gated): 64/51 64/57 71/57 86/71
+// (200 rows) 127/120 (400), at 1040 rows of 16 x 2048 x 4096 232/238.
+constexpr int kPairRows = 96;
+constexpr int kPairTiles = 3;  // per SM
+
+}  // namespace
+
+namespace {
+
+template <int kForm, int kBlocks>
+gq_status setup_kernel() {
+  const auto kernel = product_kernel<kForm, kBlocks>;
+  gq_status st = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(smem_bytes<kBlocks>())),
+                            "grouped_mm: shared memory size");
+  if (st != GQ_OK) return st;
+  // a split above the launch's registers would wait for ever
+  cudaFuncAttributes a;
+  st = check_cuda(cudaFuncGetAttributes(&a, kernel), "grouped_mm: registers");
+  if (st != GQ_OK) return st;
+  if (a.numRegs * kThreads < 32 * (kEpiWarps * kEpiRegs + (kThreads / 32 - kEpiWarps) * kOtherRegs))
+    return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: built with %d registers per thread", a.numRegs);
+  return GQ_OK;
+}
+
+template <int kForm>
+gq_status setup_form() {
+  const gq_status st = setup_kernel<kForm, 1>();
+  return st != GQ_OK ? st : setup_kernel<kForm, 2>();
+}
 
 }  // namespace
 
 gq_status setup(DeviceInfo& info) {
-  for (const void* f : {reinterpret_cast<const void*>(product_kernel<kForward>),
-                        reinterpret_cast<const void*>(product_kernel<kTransposed>),
-                        reinterpret_cast<const void*>(product_kernel<kGated>),
-                        reinterpret_cast<const void*>(product_kernel<kGatedGrad>)}) {
-    gq_status st = check_cuda(
-        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmemBytes)),
-        "grouped_mm: shared memory size");
+  for (const gq_status st : {setup_form<kForward>(), setup_form<kTransposed>(), setup_form<kGated>(),
+                             setup_form<kGatedGrad>()})
     if (st != GQ_OK) return st;
-    // a split above the launch's registers would wait for ever
-    cudaFuncAttributes a;
-    st = check_cuda(cudaFuncGetAttributes(&a, f), "grouped_mm: registers");
-    if (st != GQ_OK) return st;
-    if (a.numRegs * kThreads < 32 * (kEpiWarps * kEpiRegs + (kThreads / 32 - kEpiWarps) * kOtherRegs))
-      return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: built with %d registers per thread", a.numRegs);
-  }
-  (void)info;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(info.sm_count / 2 * 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<2>();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const gq_status st = check_cuda(
+      cudaOccupancyMaxActiveClusters(&info.mm_pairs, product_kernel<kForward, 2>, &cfg),
+      "grouped_mm: resident block pairs");
+  if (st != GQ_OK) return st;
+  if (info.mm_pairs < 1) info.mm_pairs = 1;
   return setup_few();
 }
 
@@ -632,12 +758,13 @@ Params params_of(const DeviceInfo& info, const DebugKnobs& dbg, int form, const 
   return p;
 }
 
-template <int kForm>
+template <int kForm, int kBlocks>
 gq_status launch_many(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,
                       int32_t K, cudaStream_t stream) {
   constexpr int kTileCols = kForm == kGated ? kCols / 2 : kCols;
   p.tiles_c = (p.outer + kTileCols - 1) / kTileCols;
-  const int64_t most = (static_cast<int64_t>(p.M) / kRows + (p.E < p.M ? p.E : p.M)) * p.tiles_c;
+  const int64_t most =
+      (static_cast<int64_t>(p.M) / (kBlocks * kRows) + (p.E < p.M ? p.E : p.M)) * p.tiles_c;
   if (most > INT32_MAX)  // tiles of any offsets
     return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: %lld tiles", static_cast<long long>(most));
   CUtensorMap amap, amap32, wmap;
@@ -648,17 +775,23 @@ gq_status launch_many(const DeviceInfo& info, Params& p, const void* qa, const v
   }
   st = encode_weights(&wmap, p, qb, N, K);
   if (st != GQ_OK) return st;
-  const unsigned grid = static_cast<unsigned>(most < info.sm_count ? most : info.sm_count);
-  return launch_chained("grouped_mm: launch", product_kernel<kForm>, dim3(grid), kThreads,
-                        kSmemBytes, stream, 1, amap, amap32, wmap, p);
+  const int resident = kBlocks == 2 ? info.mm_pairs : info.sm_count;
+  const unsigned grid = kBlocks * static_cast<unsigned>(most < resident ? most : resident);
+  return launch_chained("grouped_mm: launch", product_kernel<kForm, kBlocks>, dim3(grid), kThreads,
+                        smem_bytes<kBlocks>(), stream, kBlocks, amap, amap32, wmap, p);
 }
 
 template <int kForm>
 gq_status launch_form(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,
                       int32_t K, cudaStream_t stream) {
-  if (p.M <= static_cast<int64_t>(kFewRows) * p.E)
-    return launch_few(info, p, qa, qb, N, K, stream);
-  return launch_many<kForm>(info, p, qa, qb, N, K, stream);
+  constexpr int kFew = kForm == kGated ? kFewRowsGated : kFewRows;
+  if (p.M <= static_cast<int64_t>(kFew) * p.E) return launch_few(info, p, qa, qb, N, K, stream);
+  constexpr int kTileCols = kForm == kGated ? kCols / 2 : kCols;
+  const int64_t tiles = static_cast<int64_t>(p.M) / kRows * ((p.outer + kTileCols - 1) / kTileCols);
+  if ((p.inner % 64 != 0 || K % 64 != 0) && p.M > static_cast<int64_t>(kPairRows) * p.E &&
+      tiles > static_cast<int64_t>(kPairTiles) * info.sm_count)
+    return launch_many<kForm, 2>(info, p, qa, qb, N, K, stream);
+  return launch_many<kForm, 1>(info, p, qa, qb, N, K, stream);
 }
 
 }  // namespace

@@ -21,6 +21,7 @@ struct DeviceInfo {
   int mx_ctas_per_sm = 0;
   int rows_ctas_per_sm = 0;
   int sort_cluster = 0;  // most blocks of the token sort
+  int mm_pairs = 0;      // block pairs of a grouped product resident at once
 };
 
 // Launch-time knobs (test hooks).

@@ -297,6 +297,74 @@ def test_forward_contains_nan(gq):
     assert bool(got.scales.isfinite().all())
 
 
+# Rows that are no multiple of 64 bytes, 100 of them per group and more, and
+# hundreds of tiles: the products of block pairs.
+PAIRS = [
+    # M, inner, outer, offs: groups that end within a pair's first and second block, a single
+    # row, an empty group, rows behind the last end
+    (6200, 144, 2576, [3000, 3001, 3001, 5200, 6100]),
+    (7424, 400, 2320, [256, 384, 640, 7400]),
+    (6144, 16, 4368, [6144]),
+    (9000, 1104, 1424, [90, 300, 5000, 9000]),
+]
+
+
+@pytest.mark.parametrize("M,inner,outer,offs", PAIRS)
+def test_pairs_of_blocks(gq, M, inner, outer, offs):
+    c = Case(M, outer, inner, offs, seed=10)
+    n = c.end
+    pre, epre, h, eh = c.forward("silu")
+    r = gq.grouped_gated_mm(*c.args(), fp8=True, keep=True)
+    gq.check_device_error()
+    check_bf16(r.out[:n], h[:n], eh[:n])
+    check_bf16(r.pre[:n], pre[:n], epre[:n])
+    check_quantized(r.q[:n], r.scales[:n], h[:n], eh[:n])
+    # the same projections by the plain product
+    w, sw = c.qb[:, 0].contiguous(), c.sb[:, 0].contiguous()
+    out = sentinel((M, outer), torch.bfloat16)
+    gq.grouped_mm(c.qa, c.sa, w, sw, c.offs, out=out)
+    check_bf16(out[:n], pre[:n, 0], epre[:n, 0])
+    assert untouched(out[n:])
+    again = gq.grouped_gated_mm(*c.args(), fp8=True, keep=True)
+    for a, b in zip(r, again):
+        assert torch.equal(a[:n].view(torch.uint8), b[:n].view(torch.uint8))
+
+
+@pytest.mark.parametrize("M,inner,outer,offs", PAIRS)
+def test_pairs_of_blocks_transposed(gq, M, inner, outer, offs):
+    c = Case(M, inner, outer, offs, seed=11)
+    n = c.end
+    out = sentinel((M, outer), torch.bfloat16)
+    gq.grouped_gated_grad(c.qd, c.sd, c.qb, c.sb, c.offs, out=out)
+    gq.check_device_error()
+    want, S = c.grad()
+    check_bf16(out[:n], want[:n], 2.0 ** -12 * S[:n])
+    assert untouched(out[n:])
+    w, sw = c.qb[:, 1].contiguous(), c.sb[:, 1].contiguous()
+    d, sd = c.qd[:, 1].contiguous(), c.sd[:, 1].contiguous()
+    out = gq.grouped_mm(d, sd, w, sw, c.offs, transpose_b=True)
+    for e, (s, t) in enumerate(c.bounds):
+        a, b = wide(d[s:t], sd[s:t], 1), wide(w[e], sw[e], 128)
+        check_bf16(out[s:t], a @ b, 2.0 ** -12 * (a.abs() @ b.abs()))
+
+
+def test_pairs_contain_nan(gq):
+    M, inner, outer, offs = PAIRS[0]
+    c = Case(M, outer, inner, offs, seed=12)
+    n = c.end
+    want = gq.grouped_gated_mm(*c.args(), keep=True)
+    qa, qb = c.qa.clone(), c.qb.clone()
+    qa.view(torch.uint8)[[5, 200, 3000]] = 0x7F
+    qa.view(torch.uint8)[6100:] = 0x7F  # behind the last end
+    qb.view(torch.uint8)[0, 1, outer - 1, 0] = 0x7F
+    got = gq.grouped_gated_mm(qa, c.sa, qb, c.sb, c.offs, keep=True)
+    hit = torch.zeros(M, outer, dtype=torch.bool, device=DEV)
+    hit[[5, 200, 3000]] = True
+    hit[:3000, outer - 1] = True
+    assert torch.equal(got.out[:n].isnan(), hit[:n])
+    assert torch.equal(got.out[:n][~hit[:n]], want.out[:n][~hit[:n]])
+
+
 # ---------------------------------------------------------------- backward --
 
 def backward_plain(g, pre, act):
@@ -448,6 +516,31 @@ def test_streams_and_graphs(gq, M, N, K, offs):
     for w, g1, g2 in zip(want, got, (*r, *b[:3], d)):
         assert torch.equal(w.view(torch.uint8), g1[:n].view(torch.uint8))
         assert torch.equal(w.view(torch.uint8), g2[:n].view(torch.uint8))
+
+
+@pytest.mark.parametrize("M,N,K,offs", [(12, 48, 656, [4, 12]), (600, 48, 400, [300, 600]),
+                                         (6200, 2576, 144, [3000, 6200])])
+def test_timeouts_are_reported_not_hung(gq, M, N, K, offs):
+    """A withheld accumulator release: every role leaves its loop after the
+    (shortened) limit, the call reports GQ_ERR_TIMEOUT, the next call is fine.
+    (Few rows, many, and pairs of blocks.)"""
+    c, t = Case(M, N, K, offs, seed=8), Case(M, K, N, offs, seed=9)
+    calls = [lambda: gq.grouped_gated_mm(*c.args(), fp8=True).q,
+             lambda: gq.grouped_gated_grad(t.qd, t.sd, t.qb, t.sb, t.offs)]
+    for call in calls:
+        want = call()
+        try:
+            gq.debug_set(skip_arrival=True, wait_timeout_ns=5_000_000)
+            # contractions of three 128-blocks and more: the third waits for the first accumulator
+            call()
+            with pytest.raises(gq.GQError) as e:
+                gq.check_device_error()
+            assert e.value.status == 4
+        finally:
+            gq.debug_set(False, 0)
+        got = call()
+        gq.check_device_error()
+        assert torch.equal(want.view(torch.uint8), got.view(torch.uint8))
 
 
 def test_empty(gq):
