@@ -4,16 +4,18 @@
 // Both are streams bound by HBM: the norm reads every element once, the
 // scaling reads and writes every element once more.
 //
-// The tensors are cut into chunks of kChunk elements; a block takes a
-// contiguous range of the chunks of all tensors and walks the table of
-// tensors, which comes with the launch's parameters: nothing is copied to the
-// device beforehand, so a call can be captured.
+// The tensors are cut into chunks of 16 KB; the blocks of the grid take them in
+// turn, each loading its next chunk before it works on the last (without that
+// the norm ran at 4.4 TB/s).  The scaling goes through the list backwards: what
+// the norm has read last is still in L2.  The table of the tensors comes with the
+// launch's parameters: nothing is copied to the device beforehand, so a call
+// can be captured.
 //
-// A thread sums the squares of up to 32 elements in fp32, eight to a partial
-// sum, and everything beyond that in fp64 (one fp64 addition for 32
-// elements), in an order that depends on the sizes alone: the result is the
-// same in every run.  Squares of values past 2^60, or all below 2^-40, would
-// leave fp32's range: such a thread squares in fp64.
+// A thread sums the squares of the 64 bytes that it has of a chunk in fp32, eight
+// elements to a partial sum, and everything beyond that in fp64, in an order
+// that depends on the sizes alone: the result is the same in every run.  Squares
+// of values past 2^60, or all below 2^-40, would leave fp32's range: such a
+// thread squares in fp64.
 #include <algorithm>
 #include <memory>
 #include <new>
@@ -27,8 +29,8 @@ namespace clip {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 32;                     // elements per thread and chunk
-constexpr int kChunk = kThreads * kPer;
+constexpr int kVecs = 4;                     // 16-byte vectors per thread and chunk
+constexpr int kChunk = kThreads * kVecs * 16;  // bytes
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostBlocks = 2048;            // partial sums per launch
 constexpr int64_t kF32Bit = int64_t(1) << 62;
@@ -45,52 +47,75 @@ struct Table {
 // Largest tables; 28 bytes an entry, below the 32 KB of a launch's parameters.
 constexpr int kSmall = 16, kLarge = 1024;
 
-// The chunks of one block, and the tensor of the current one.
+// A chunk: `size` bytes per element, `head` single elements up to the first
+// 16-byte boundary, `vecs` vectors, `tail` single elements behind them.
+struct Chunk {
+  const uint8_t* in;
+  uint8_t* out;
+  int32_t size, head, vecs, tail;
+};
+
 template <int kCap>
-struct Walk {
-  int32_t t = 0;
-  // the tensor of chunk c
-  __device__ __forceinline__ void find(const Table<kCap>& tab, int32_t c) {
-    int32_t lo = 0, hi = tab.count - 1;  // the last tensor whose first chunk is at or before c
-    while (lo < hi) {
-      const int32_t mid = (lo + hi + 1) >> 1;
-      if (tab.first[mid] <= c)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    t = lo;
+__device__ __forceinline__ Chunk chunk_of(const Table<kCap>& tab, int32_t c) {
+  int32_t lo = 0, hi = tab.count - 1;  // the last tensor whose first chunk is at or before c
+  while (lo < hi) {
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (tab.first[mid] <= c)
+      lo = mid;
+    else
+      hi = mid - 1;
   }
-};
-
-// A chunk's elements: `head` single ones up to the first 16-byte boundary,
-// `vecs` 16-byte vectors, `tail` single ones behind them.
-struct Span {
-  int32_t head, vecs, tail;
-};
-
-template <int kSize>
-__device__ __forceinline__ Span span_of(const uint8_t* p, int32_t n) {
-  constexpr int kVec = 16 / kSize;
-  Span s;
-  s.head = min(n, static_cast<int32_t>((-reinterpret_cast<uintptr_t>(p) & 15) / kSize));
-  s.vecs = (n - s.head) / kVec;
-  s.tail = n - s.head - s.vecs * kVec;
-  return s;
+  Chunk k;
+  k.size = (tab.size[lo] & kF32Bit) != 0 ? 4 : 2;
+  const int64_t at = static_cast<int64_t>(c - tab.first[lo]) * kChunk;
+  const int64_t left = (tab.size[lo] & ~kF32Bit) * k.size - at;
+  const int32_t bytes = left < kChunk ? static_cast<int32_t>(left) : kChunk;
+  k.in = tab.in[lo] + at;
+  k.out = tab.out[lo] + at;
+  const int32_t skip =
+      min(bytes, static_cast<int32_t>(-static_cast<uint32_t>(reinterpret_cast<uintptr_t>(k.in)) & 15u));
+  k.head = skip / k.size;
+  k.vecs = (bytes - skip) / 16;
+  k.tail = (bytes - skip) % 16 / k.size;
+  return k;
 }
 
-template <int kSize>
-__device__ __forceinline__ float load_one(const uint8_t* p) {
-  return kSize == 4 ? *reinterpret_cast<const float*>(p)
-                    : __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(p)) << 16);
+// This thread's part of a chunk: its vectors, and perhaps a single element.
+struct Part {
+  uint4 v[kVecs];
+  float one;
+};
+
+__device__ __forceinline__ float load_one(const uint8_t* p, int32_t size) {
+  return size == 4 ? *reinterpret_cast<const float*>(p)
+                   : __uint_as_float(uint32_t(*reinterpret_cast<const uint16_t*>(p)) << 16);
 }
 
-template <int kSize>
-__device__ __forceinline__ void store_one(uint8_t* p, float v) {
-  if (kSize == 4)
+__device__ __forceinline__ void store_one(uint8_t* p, int32_t size, float v) {
+  if (size == 4)
     *reinterpret_cast<float*>(p) = v;
   else
     *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(bf16x2_of(v, 0.0f) & 0xFFFFu);
+}
+
+// The place of this thread's single element in bytes, -1 if it has none: at most
+// seven at either end, two warps.
+__device__ __forceinline__ int32_t single_of(const Chunk& k) {
+  const int32_t lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) return lane < k.head ? lane * k.size : -1;
+  if (threadIdx.x >= 64 || lane >= k.tail) return -1;
+  return (k.head + lane) * k.size + k.vecs * 16;
+}
+
+__device__ __forceinline__ void load_part(Part& t, const Chunk& k) {
+  const uint4* const q = reinterpret_cast<const uint4*>(k.in + k.head * k.size);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int32_t i = threadIdx.x + j * kThreads;
+    t.v[j] = i < k.vecs ? q[i] : make_uint4(0u, 0u, 0u, 0u);
+  }
+  const int32_t at = single_of(k);
+  t.one = at >= 0 ? load_one(k.in + at, k.size) : 0.0f;
 }
 
 // The values of a 16-byte vector.
@@ -108,41 +133,32 @@ __device__ __forceinline__ void widen(float (&f)[16 / kSize], uint4 v) {
   }
 }
 
-// Sum of the squares of this thread's elements of a chunk.
+// Sum of the squares of a thread's part.
 template <int kSize>
-__device__ __forceinline__ double chunk_squares(const uint8_t* p, int32_t n) {
-  constexpr int kVec = 16 / kSize, kVecs = kPer / kVec;
-  const Span s = span_of<kSize>(p, n);
-  const uint4* const q = reinterpret_cast<const uint4*>(p + s.head * kSize);
-  uint4 v[kVecs];
+__device__ __forceinline__ double part_squares(const Part& t) {
+  constexpr int kVec = 16 / kSize;
+  float most = fabsf(t.one);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
-    const int32_t i = threadIdx.x + j * kThreads;
-    v[j] = i < s.vecs ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  // at most 7 + 7 single elements, two warps
-  float one = 0.0f;
-  const int32_t lane = threadIdx.x & 31;
-  if (threadIdx.x < 32 && lane < s.head) one = load_one<kSize>(p + lane * kSize);
-  if (threadIdx.x >= 32 && threadIdx.x < 64 && lane < s.tail)
-    one = load_one<kSize>(p + (s.head + s.vecs * kVec + lane) * kSize);
-  float most = fabsf(one);
+    if (kSize == 2) {  // NaN where all are
+      const uint32_t m = absmax_bf16x2(absmax_bf16x2(t.v[j].x, t.v[j].y), absmax_bf16x2(t.v[j].z, t.v[j].w));
+      most = fmaxf(most, __uint_as_float(amax_bits_of(m)));
+    } else {
+      float f[kVec];
+      widen<kSize>(f, t.v[j]);
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    float f[kVec];
-    widen<kSize>(f, v[j]);
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) most = fmaxf(most, fabsf(f[k]));
+      for (int k = 0; k < kVec; ++k) most = fmaxf(most, fabsf(f[k]));
+    }
   }
   if (most == 0.0f || (most >= 0x1p-40f && most <= 0x1p60f)) {  // a NaN is dropped by fmaxf
-    float sum = 0.0f;
+    float sum = t.one * t.one;
 #pragma unroll
     for (int j = 0; j < kVecs; j += 8 / kVec) {
-      float part = j == 0 ? one * one : 0.0f;
+      float part = 0.0f;
 #pragma unroll
       for (int h = 0; h < 8 / kVec; ++h) {
         float f[kVec];
-        widen<kSize>(f, v[j + h]);
+        widen<kSize>(f, t.v[j + h]);
 #pragma unroll
         for (int k = 0; k < kVec; ++k) part = __fmaf_rn(f[k], f[k], part);
       }
@@ -150,11 +166,11 @@ __device__ __forceinline__ double chunk_squares(const uint8_t* p, int32_t n) {
     }
     return sum;
   }
-  double sum = static_cast<double>(one) * one;
-#pragma unroll 1
+  double sum = static_cast<double>(t.one) * t.one;
+#pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     float f[kVec];
-    widen<kSize>(f, v[j]);
+    widen<kSize>(f, t.v[j]);
 #pragma unroll
     for (int k = 0; k < kVec; ++k) sum += static_cast<double>(f[k]) * f[k];
   }
@@ -173,29 +189,29 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return v;
 }
 
-// This block's range of the chunks.
-__device__ __forceinline__ void my_range(int32_t chunks, int32_t& from, int32_t& to) {
-  from = static_cast<int32_t>(static_cast<int64_t>(chunks) * blockIdx.x / gridDim.x);
-  to = static_cast<int32_t>(static_cast<int64_t>(chunks) * (blockIdx.x + 1) / gridDim.x);
-}
-
 template <int kCap>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     squares_kernel(const __grid_constant__ Table<kCap> tab, double* partial) {
   __shared__ double red[kWarps];
   grid_wait();
-  int32_t from, to;
-  my_range(tab.first[tab.count], from, to);
-  Walk<kCap> w;
-  w.find(tab, from);
+  const int32_t chunks = tab.first[tab.count], step = static_cast<int32_t>(gridDim.x);
+  int32_t c = static_cast<int32_t>(blockIdx.x);  // the grid is no larger than the chunks
+  Chunk k = chunk_of(tab, c);
+  Part t;
+  load_part(t, k);
   double sum = 0.0;
-  for (int32_t c = from; c < to; ++c) {
-    while (tab.first[w.t + 1] <= c) ++w.t;
-    const bool f32 = (tab.size[w.t] & kF32Bit) != 0;
-    const int64_t e = static_cast<int64_t>(c - tab.first[w.t]) * kChunk;
-    const int64_t left = (tab.size[w.t] & ~kF32Bit) - e;
-    const int32_t n = left < kChunk ? static_cast<int32_t>(left) : kChunk;
-    sum += f32 ? chunk_squares<4>(tab.in[w.t] + e * 4, n) : chunk_squares<2>(tab.in[w.t] + e * 2, n);
+  while (true) {
+    const int32_t size = k.size;
+    const bool more = c < chunks - step;
+    Part next = {};
+    if (more) {
+      c += step;
+      k = chunk_of(tab, c);
+      load_part(next, k);
+    }
+    sum += size == 4 ? part_squares<4>(t) : part_squares<2>(t);
+    if (!more) break;
+    t = next;
   }
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
@@ -217,41 +233,42 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <int kSize>
-__device__ __forceinline__ void scale_chunk(const uint8_t* p, uint8_t* o, int32_t n, float f) {
-  constexpr int kVec = 16 / kSize, kVecs = kPer / kVec;
-  if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) != 0) {
-    // no vector of the one is a vector of the other
-    for (int32_t i = threadIdx.x; i < n; i += kThreads)
-      store_one<kSize>(o + i * kSize, load_one<kSize>(p + i * kSize) * f);
-    return;
-  }
-  const Span s = span_of<kSize>(p, n);
-  const uint4* const q = reinterpret_cast<const uint4*>(p + s.head * kSize);
-  uint4* const d = reinterpret_cast<uint4*>(o + s.head * kSize);
-  uint4 v[kVecs];
+__device__ __forceinline__ uint4 scale_vec(uint4 v, float f) {
+  constexpr int kVec = 16 / kSize;
+  float x[kVec];
+  widen<kSize>(x, v);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    w[k] = kSize == 4 ? __float_as_uint(x[k] * f)
+                      : bf16x2_of(x[(2 * k) % kVec] * f, x[(2 * k + 1) % kVec] * f);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int kSize>
+__device__ __forceinline__ void store_part(const Part& t, const Chunk& k, float f) {
+  uint8_t* const to = k.out + k.head * kSize;
+  const bool vectors = (reinterpret_cast<uintptr_t>(to) & 15) == 0;
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int32_t i = threadIdx.x + j * kThreads;
-    if (i < s.vecs) v[j] = q[i];
-  }
+    if (i >= k.vecs) continue;
+    const uint4 v = scale_vec<kSize>(t.v[j], f);
+    if (vectors) {
+      __stcs(reinterpret_cast<uint4*>(to) + i, v);
+    } else {  // the tensor and its output lie differently in their 16 bytes
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    const int32_t i = threadIdx.x + j * kThreads;
-    if (i >= s.vecs) continue;
-    float x[kVec];
-    widen<kSize>(x, v[j]);
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[k] = kSize == 4 ? __float_as_uint(x[k] * f)
-                        : bf16x2_of(x[(2 * k) % kVec] * f, x[(2 * k + 1) % kVec] * f);
-    d[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int e = 0; e < 16 / kSize; ++e) {
+        if (kSize == 4)
+          reinterpret_cast<uint32_t*>(to)[i * 4 + e] = w[e % 4];
+        else
+          reinterpret_cast<uint16_t*>(to)[i * 8 + e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+      }
+    }
   }
-  const int32_t lane = threadIdx.x & 31;
-  int32_t at = -1;
-  if (threadIdx.x < 32 && lane < s.head) at = lane;
-  if (threadIdx.x >= 32 && threadIdx.x < 64 && lane < s.tail) at = s.head + s.vecs * kVec + lane;
-  if (at >= 0) store_one<kSize>(o + at * kSize, load_one<kSize>(p + at * kSize) * f);
+  const int32_t at = single_of(k);
+  if (at >= 0) store_one(k.out + at, kSize, t.one * f);
 }
 
 struct ClipParams {
@@ -260,35 +277,40 @@ struct ClipParams {
   float* norm;         // where the first block writes it, or nullptr
   float most;
   int32_t partials;
+  bool in_place;       // a factor of 1 writes nothing
 };
 
 template <int kCap>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     scale_kernel(const __grid_constant__ Table<kCap> tab, const ClipParams p) {
   __shared__ double red[kWarps];
+  const int32_t step = static_cast<int32_t>(gridDim.x);
+  int32_t c = tab.first[tab.count] - 1 - static_cast<int32_t>(blockIdx.x);  // at least 0
+  Chunk k = chunk_of(tab, c);
   grid_wait();
+  Part t;
+  load_part(t, k);
   const double norm = p.given != nullptr ? static_cast<double>(__ldg(p.given))
                                          : norm_of(p.partial, p.partials, red);
   if (p.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
   // a NaN is not below the limit: it becomes the factor
   const float f = norm <= p.most ? 1.0f : static_cast<float>(p.most / norm);
-  int32_t from, to;
-  my_range(tab.first[tab.count], from, to);
-  Walk<kCap> w;
-  w.find(tab, from);
-  for (int32_t c = from; c < to; ++c) {
-    while (tab.first[w.t + 1] <= c) ++w.t;
-    const uint8_t* in = tab.in[w.t];
-    uint8_t* out = tab.out[w.t];
-    if (f == 1.0f && in == out) continue;
-    const bool f32 = (tab.size[w.t] & kF32Bit) != 0;
-    const int64_t e = static_cast<int64_t>(c - tab.first[w.t]) * kChunk;
-    const int64_t left = (tab.size[w.t] & ~kF32Bit) - e;
-    const int32_t n = left < kChunk ? static_cast<int32_t>(left) : kChunk;
-    if (f32)
-      scale_chunk<4>(in + e * 4, out + e * 4, n, f);
+  if (f == 1.0f && p.in_place) return;
+  while (true) {
+    const Chunk last = k;
+    const bool more = c >= step;
+    Part next = {};
+    if (more) {
+      c -= step;
+      k = chunk_of(tab, c);
+      load_part(next, k);
+    }
+    if (last.size == 4)
+      store_part<4>(t, last, f);
     else
-      scale_chunk<2>(in + e * 2, out + e * 2, n, f);
+      store_part<2>(t, last, f);
+    if (!more) break;
+    t = next;
   }
 }
 
@@ -303,7 +325,8 @@ gq_status for_tables(const void* const* in, void* const* out, const int64_t* siz
     int64_t chunks = 0;
     for (; i < count && tab.count < kCap; ++i) {
       if (sizes[i] == 0) continue;
-      const int64_t more = (sizes[i] + kChunk - 1) / kChunk;
+      const int64_t bytes = sizes[i] * (dtypes[i] == GQ_DTYPE_F32 ? 4 : 2);
+      const int64_t more = (bytes + kChunk - 1) / kChunk;
       const int32_t t = tab.count++;
       tab.in[t] = static_cast<const uint8_t*>(in[i]);
       tab.out[t] = static_cast<uint8_t*>(out != nullptr ? out[i] : const_cast<void*>(in[i]));
@@ -344,7 +367,7 @@ gq_status run(const DeviceInfo& info, const void* const* in, void* const* out, b
   bool told = false;  // a launch of the scaling writes the norm
   if (write) {
     st = for_tables<kCap>(in, out, sizes, dtypes, count, [&](const Table<kCap>& tab) {
-      ClipParams p = {partial, given, told ? nullptr : norm, most, partials};
+      ClipParams p = {partial, given, told ? nullptr : norm, most, partials, out == nullptr};
       told = true;
       return launch_chained("clip_grads: launch", scale_kernel<kCap>,
                             dim3(grid_of(info, tab.first[tab.count])), kThreads, 0, stream, 1, tab, p);
