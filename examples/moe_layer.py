@@ -5,9 +5,9 @@ backward, on one GPU:
     y = a @ W2[e].T;             out[t] = sum over slots of weight * y
 
 Forward and input gradients use operands quantized per block of 128
-(dispatch_block, block_rows, block_tiles, grouped_mm); the weight gradients use
-operands quantized per token group (colwise, grouped_wgrad).  The gate between
-the two products is left to torch.
+(dispatch_block, block_rows, block_tiles, grouped_gated_mm, grouped_mm); the
+weight gradients use operands quantized per token group (colwise,
+grouped_wgrad) and are clipped to a largest norm before a step.
 
     python examples/moe_layer.py        # runs it and compares with 32 bits
 """
@@ -30,8 +30,20 @@ class Fp8MoELayer:
 
     def update(self, w13, w2):
         """Quantizes the weights (after an optimizer step); both products of a
-        step read the same copies, plain and transposed."""
-        self.w13, self.w2 = gq.block_tiles(w13), gq.block_tiles(w2)
+        step read the same copies, plain and transposed.  The gate's and the up
+        projection's rows of an expert are two matrices of it."""
+        E, F2, H = w13.shape
+        q, s = gq.block_tiles(w13.view(2 * E, F2 // 2, H))
+        self.w13 = q.view(E, 2, F2 // 2, H), s.view(E, 2, *s.shape[1:])
+        self.w2 = gq.block_tiles(w2)
+
+    def infer(self, x, ids, weights):
+        """forward without what a backward pass needs: the gated rows are
+        written quantized only."""
+        order = gq.sort_tokens(ids, self.experts)
+        qx, sx = gq.dispatch_block(x, order.pos)
+        a = gq.grouped_gated_mm(qx, sx, *self.w13, order.offs, plain=False, fp8=True)
+        return gq.combine(gq.grouped_mm(a.q, a.scales, *self.w2, order.offs), order.pos, weights)
 
     def forward(self, x, ids, weights):
         """x bf16 (T, H); ids (T, k) expert choices (others than 0 .. E-1 are
@@ -39,35 +51,31 @@ class Fp8MoELayer:
         backward pass needs."""
         order = gq.sort_tokens(ids, self.experts)
         qx, sx = gq.dispatch_block(x, order.pos)
-        h = gq.grouped_mm(qx, sx, *self.w13, order.offs)
-        a = gated(h)
-        y = gq.grouped_mm(*gq.block_rows(a), *self.w2, order.offs)
+        a = gq.grouped_gated_mm(qx, sx, *self.w13, order.offs, fp8=True, keep=True)
+        y = gq.grouped_mm(a.q, a.scales, *self.w2, order.offs)
         out = gq.combine(y, order.pos, weights)
-        return out, (x, weights, order, h, a, y)
+        return out, (x, weights, order, a.pre, a.out, y)
 
     def backward(self, g, saved):
         """g bf16 (T, H).  Returns the gradients of x, weights, w13 and w2."""
-        x, weights, order, h, a, y = saved
+        x, weights, order, pre, a, y = saved
         dy, dweights = gq.combine_backward(g, y, order.pos, weights)
         da = gq.grouped_mm(*gq.block_rows(dy), *self.w2, order.offs, transpose_b=True)
-        dh = gated_backward(h, da)
-        dx_rows = gq.grouped_mm(*gq.block_rows(dh), *self.w13, order.offs, transpose_b=True)
+        d = gq.gated_backward(da, pre, fp8=True)
+        dx_rows = gq.grouped_gated_grad(d.q, d.scales, *self.w13, order.offs)
         dx = gq.combine(dx_rows, order.pos)
         dw2 = weight_gradient(dy, a, order.offs)
-        dw13 = weight_gradient(dh, gq.dispatch(x, order.pos), order.offs)
+        dw13 = weight_gradient(d.out.flatten(1), gq.dispatch(x, order.pos), order.offs)
         return dx, dweights, dw13, dw2
 
-
-def gated(h):
-    left, right = h.float().chunk(2, dim=1)
-    return (torch.nn.functional.silu(left) * right).to(torch.bfloat16)
-
-
-def gated_backward(h, da):
-    left, right = h.float().chunk(2, dim=1)
-    da, s = da.float(), torch.sigmoid(left)
-    dleft = da * right * s * (1 + left * (1 - s))
-    return torch.cat([dleft, da * left * s], dim=1).to(torch.bfloat16)
+    def step(self, w13, w2, dw13, dw2, rate, max_norm):
+        """A step of gradient descent on the master weights with both gradients
+        clipped, in place, to a norm of max_norm together.  Returns their norm."""
+        norm = gq.clip_grads([dw13, dw2], max_norm)
+        w13.sub_(dw13, alpha=rate)
+        w2.sub_(dw2, alpha=rate)
+        self.update(w13, w2)
+        return norm
 
 
 def weight_gradient(grad, x, offs):
