@@ -56,7 +56,7 @@ SIGNATURES = {
     "gq_grouped_gated_mm": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, ctypes.c_int, _P, _I32, _P, _P, _P, _P, ctypes.c_uint32, _P]),
     "gq_grouped_gated_grad": (ctypes.c_int, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _I32, _P, _P]),
     "gq_gated_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_int, _P, _P, _P, ctypes.c_uint32, _P]),
-    "gq_grad_norm_workspace_bytes": (_SZ, [_I32]),
+    "gq_grad_norm_workspace_bytes": (_SZ, [_P, _P, _I32]),
     "gq_grad_norm": (ctypes.c_int, [_P, _P, _P, _I32, _P, _P, _SZ, _P]),
     "gq_clip_grads": (ctypes.c_int, [_P, _P, _P, _P, _I32, ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "gq_check_device_error": (ctypes.c_int, [_P]),

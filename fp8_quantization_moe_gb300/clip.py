@@ -68,14 +68,15 @@ def _address(a: array) -> int:
     return a.buffer_info()[0]
 
 
-def _norm_buffers(index: int, count: int, stream):
-    """The norm and the call's scratch.  The scratch is not kept: what is freed
-    here is handed out again on the same stream only, in that stream's order."""
+def _norm_buffers(index: int, sizes: array, codes: array, stream):
+    """The norm, and the call's scratch where it needs some.  The scratch is not
+    kept: what is freed here is handed out again on the same stream only, in that
+    stream's order."""
     empty = torch.empty if stream is None else _empty_on(stream, index)
     dev = torch.device("cuda", index)
-    size = lib().gq_grad_norm_workspace_bytes(count)
+    size = lib().gq_grad_norm_workspace_bytes(_address(sizes), _address(codes), len(sizes))
     return (empty((), dtype=torch.float32, device=dev),
-            empty(size, dtype=torch.uint8, device=dev), size)
+            empty(size, dtype=torch.uint8, device=dev) if size else None, size)
 
 
 def grad_norm(grads: Sequence[torch.Tensor], *, stream=None) -> torch.Tensor:
@@ -83,17 +84,18 @@ def grad_norm(grads: Sequence[torch.Tensor], *, stream=None) -> torch.Tensor:
 
     grads: contiguous bfloat16 or float32 CUDA tensors of one device, of any
     shapes, both types in one list too; a tensor may come more than once and
-    counts each time.  Squares are summed in fp32 over 32 elements and in fp64
-    beyond, in a fixed order; no finite value overflows on the way.  Returns
-    the norm, a float32 scalar on the device.
+    counts each time.  Squares are summed in fp32 over some 32 elements and in
+    fp64 beyond, in an order that goes by the sizes and the alignment; no finite
+    value overflows on the way.  Returns the norm, a float32 scalar on the device.
     """
     ptrs, sizes, codes, index = _lists("grad_norm", "grads", grads)
     if index < 0:
         raise ValueError("grad_norm: no tensors")
     count = len(ptrs)
-    norm, scratch, size = _norm_buffers(index, count, stream)
+    norm, scratch, size = _norm_buffers(index, sizes, codes, stream)
     _call("gq_grad_norm", index, stream, lib().gq_grad_norm, _address(ptrs), _address(sizes),
-          _address(codes), count, norm.data_ptr(), scratch.data_ptr(), size)
+          _address(codes), count, norm.data_ptr(),
+          None if scratch is None else scratch.data_ptr(), size)
     return norm
 
 
@@ -130,7 +132,7 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *,
         _need(norm, name + ": norm", 0, _F32, index)
         given = norm.data_ptr()
     else:
-        norm, scratch, size = _norm_buffers(index, count, stream)
+        norm, scratch, size = _norm_buffers(index, sizes, codes, stream)
     _call("gq_clip_grads", index, stream, lib().gq_clip_grads, _address(ptrs), outs,
           _address(sizes), _address(codes), count, max_norm, given, norm.data_ptr(),
           None if scratch is None else scratch.data_ptr(), size)

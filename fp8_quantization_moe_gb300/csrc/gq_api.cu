@@ -852,8 +852,11 @@ gq_status gq_gated_backward(const void* g, const void* pre, int dtype, int64_t r
                                 reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t gq_grad_norm_workspace_bytes(int32_t count) {
-  return count < 1 || count > kMaxTensors ? 0 : clip::workspace_bytes(count);
+size_t gq_grad_norm_workspace_bytes(const int64_t* sizes, const int32_t* dtypes, int32_t count) {
+  if (count < 1 || count > kMaxTensors || sizes == nullptr || dtypes == nullptr) return 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (sizes[i] < 0 || sizes[i] > kMaxElements) return 0;
+  return clip::workspace_bytes(sizes, dtypes, count);
 }
 
 gq_status gq_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes,
@@ -864,7 +867,7 @@ gq_status gq_grad_norm(const void* const* grads, const int64_t* sizes, const int
   if (st != GQ_OK) return st;
   if (norm == nullptr || !aligned(norm, 4))
     return fail(GQ_ERR_INVALID_ARG, "%s: norm NULL or misaligned", name);
-  st = validate_ws(workspace, workspace_bytes, gq_grad_norm_workspace_bytes(count), name);
+  st = validate_ws(workspace, workspace_bytes, gq_grad_norm_workspace_bytes(sizes, dtypes, count), name);
   if (st != GQ_OK) return st;
   const DeviceInfo* info = nullptr;
   st = current_device(&info);
@@ -893,7 +896,7 @@ gq_status gq_clip_grads(const void* const* grads, void* const* outs, const int64
   } else {
     if (norm == nullptr || !aligned(norm, 4))
       return fail(GQ_ERR_INVALID_ARG, "%s: norm NULL or misaligned", name);
-    st = validate_ws(workspace, workspace_bytes, gq_grad_norm_workspace_bytes(count), name);
+    st = validate_ws(workspace, workspace_bytes, gq_grad_norm_workspace_bytes(sizes, dtypes, count), name);
     if (st != GQ_OK) return st;
   }
   st = clip::check_overlap(grads, outs, sizes, dtypes, count);

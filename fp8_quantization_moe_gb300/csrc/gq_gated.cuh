@@ -32,12 +32,34 @@ __device__ __forceinline__ float act_z(Act p, float x) {
 // overflow it gives 0.
 __device__ __forceinline__ float sigma(float z) { return rcp_approx(1.0f + expf(-z)); }
 
-// The same from the hardware's power of two, whose argument adds |z| 2^-23: for
-// values that are sums of rounded products anyway.
-__device__ __forceinline__ float sigma_approx(float z) {
-  float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
-  return rcp_approx(1.0f + e);
+// x := act(x) * u for several values, two at a time, with sigma from the
+// hardware's power of two, whose argument adds |z| 2^-23: for values that are
+// sums of rounded products anyway.  a x + b x^3 may overflow to the infinity that
+// it stands for; x is held at fp32's lowest value, so that an infinity times a
+// vanished sigma is no NaN (a NaN comes through sigma).
+// Measured, 38,000 rows, K 224 to N 3680, gelu to fp8: 204 us, of which 70 are
+// this; one value at a time 231; a reciprocal shared by two values, against the
+// special function unit's 16 results a cycle, with a branch for the far ones, 274.
+template <int kN>
+__device__ __forceinline__ void gate(Act p, float (&x)[kN], const float (&u)[kN]) {
+  const float a = p.a * -1.4426950408889634f, b = p.b * -1.4426950408889634f;
+#pragma unroll
+  for (int j = 0; j < kN; j += 2) {
+    float k[2] = {a, a}, z[2], e[2], d[2], s[2];
+    if (b != 0.0f) {
+      float q[2];
+      mul2(q[0], q[1], x[j], x[j + 1], x[j], x[j + 1]);
+      fma2(k[0], k[1], __float_as_uint(q[0]), __float_as_uint(q[1]), b);
+    }
+    mul2(z[0], z[1], x[j], x[j + 1], k[0], k[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e[i]) : "f"(z[i]));
+    add2(d[0], d[1], e[0], e[1], 1.0f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s[i] = rcp_approx(d[i]);
+    mul2(s[0], s[1], s[0], s[1], fmaxf(x[j], -0x1.fffffep127f), fmaxf(x[j + 1], -0x1.fffffep127f));
+    mul2(x[j], x[j + 1], s[0], s[1], u[j], u[j + 1]);
+  }
 }
 
 // act(x) from x and sigma(z): its limit 0 where sigma has vanished.

@@ -599,8 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             store_bf16(acc[ch], prow, 2 * static_cast<int64_t>(p.outer), rows, in, lane);
             store_bf16(acc[ch + 2], prow + p.outer, 2 * static_cast<int64_t>(p.outer), rows, in, lane);
           }
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) acc[ch][j] = gated_value(p, acc[ch][j], acc[ch + 2][j]);
+          gated::gate(p.act, acc[ch], acc[ch + 2]);
           if (p.out != nullptr) store_bf16(acc[ch], p.out + row * p.outer + at, p.outer, rows, in, lane);
         }
         if (p.q == nullptr) continue;

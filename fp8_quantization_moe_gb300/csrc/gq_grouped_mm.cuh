@@ -114,11 +114,6 @@ __device__ __forceinline__ int32_t column_of(const Params& p, int32_t kb) {
   return (kb - (half_of<kForm>(p, kb) ? p.kb_half : 0)) * kBlock;
 }
 
-// kGated: h = act(x) u.
-__device__ __forceinline__ float gated_value(const Params& p, float x, float u) {
-  return gated::act_value(x, gated::sigma_approx(gated::act_z(p.act, x))) * u;
-}
-
 struct Tile {
   int32_t g, c0, m0, rows;  // group, first column, first row, rows of the group from there
 };

@@ -122,9 +122,7 @@ __device__ __forceinline__ bool gated_store(const Params& p, Smem<kGated>& s, co
     store_bf16(u, to + n, 2 * n, rows, c_ok, lane);
   }
 #pragma unroll
-  for (int a = 0; a < kN; ++a)
-#pragma unroll
-    for (int j = 0; j < kUnit; ++j) x[a][j] = gated_value(p, x[a][j], u[a][j]);
+  for (int a = 0; a < kN; ++a) gated::gate(p.act, x[a], u[a]);
   if (p.out != nullptr) store_bf16(x, p.out + (row + odd) * n + pair, n, rows, c_ok, lane);
   if (p.q == nullptr) return true;
   // the maximum of a row over this warp's 32 columns, then over the four warps

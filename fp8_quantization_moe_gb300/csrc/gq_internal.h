@@ -174,7 +174,7 @@ gq_status launch_backward(const void* g, const void* pre, bool f32, int64_t rows
 }  // namespace gated
 
 namespace clip {
-size_t workspace_bytes(int32_t count);
+size_t workspace_bytes(const int64_t* sizes, const int32_t* dtypes, int32_t count);
 gq_status check_overlap(const void* const* in, void* const* out, const int64_t* sizes,
                         const int32_t* dtypes, int32_t count);
 // The norm of the tensors, unless `given`, to `norm`, unless nullptr; with

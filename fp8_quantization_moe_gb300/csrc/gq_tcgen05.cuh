@@ -37,6 +37,11 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+  return v;
+}
 // ------------------------------------------- barriers by shared address --
 // True in one lane of a converged warp.  The tensor-core and TMA instructions
 // take warp-uniform operands: under this predicate the compiler knows that a
@@ -303,6 +308,21 @@ __device__ __forceinline__ void fma2(float& a0, float& a1, uint32_t h0, uint32_t
       "fma.rn.f32x2 a, h, f, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
       : "+f"(a0), "+f"(a1)
       : "r"(h0), "r"(h1), "f"(f));
+}
+// (d0, d1) = (a0 * b0, a1 * b1) and (a0 + c, a1 + c), IEEE fp32.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float c) {
+  asm("{\n\t.reg .b64 a, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 c, {%4, %4};\n\t"
+      "add.rn.f32x2 d, a, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(c));
 }
 // Two fp32 values as bf16x2, the first in the lower half.
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {

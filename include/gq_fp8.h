@@ -520,9 +520,9 @@ gq_status gq_grouped_gated_grad(const void* qd, const float* sd, int64_t M, cons
 
 /*
  * The norm over all elements of a list of tensors, sqrt(sum of x^2): squares
- * summed in fp32 over at most 32 elements and in fp64 beyond, so that no
+ * summed in fp32 over at most 33 elements and in fp64 beyond, so that no
  * finite fp32 or bf16 value overflows or vanishes on the way; the same result
- * in every run.  A NaN or an infinity among the elements gives NaN or an
+ * in every run for tensors that lie alike within 16 bytes.  A NaN or an infinity among the elements gives NaN or an
  * infinity.  The three lists are arrays on the host and read before the call
  * returns.
  *
@@ -532,11 +532,12 @@ gq_status gq_grouped_gated_grad(const void* qd, const float* sd, int64_t M, cons
  *   dtypes   GQ_DTYPE_* of each tensor.                            (input)
  *   count    tensors, 0 .. 2^20; the norm of none is 0.
  *   norm     fp32, device.                                        (output)
- *   workspace  device scratch of gq_grad_norm_workspace_bytes(count) bytes,
- *            256-byte aligned; the call does not rely on its content.
+ *   workspace  device scratch of gq_grad_norm_workspace_bytes(sizes, dtypes,
+ *            count) bytes, 256-byte aligned, or NULL where that is 0 (up to 16
+ *            tensors of 1 MiB in all); the call does not rely on its content.
  *   stream   the CUDA stream to run on.
  */
-size_t gq_grad_norm_workspace_bytes(int32_t count);
+size_t gq_grad_norm_workspace_bytes(const int64_t* sizes, const int32_t* dtypes, int32_t count);
 gq_status gq_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes,
                        int32_t count, float* norm, void* workspace, size_t workspace_bytes,
                        gq_stream_t stream);

@@ -92,18 +92,25 @@ TENSORS = [
 @pytest.mark.parametrize("t,status", TENSORS)
 def test_grad_norm_lists(gq, t, status):
     p, s, d, n = lists(*t)
-    size = gq.lib().gq_grad_norm_workspace_bytes(n)
+    size = 1 << 20
     assert gq.lib().gq_grad_norm(p, s, d, n, A16, A16, size, None) == status
     assert gq.lib().gq_clip_grads(p, None, s, d, n, 1.0, None, A16, A16, size, None) == status
 
 
 def test_grad_norm_refusals(gq):
     L = gq.lib()
-    p, s, d, n = lists([A16], [4], [0])
-    size = L.gq_grad_norm_workspace_bytes(n)
+    p, s, d, n = lists([A16], [1 << 20], [0])
+    bytes_of = L.gq_grad_norm_workspace_bytes
+    size = bytes_of(s, d, n)
     assert size > 0 and size % 8 == 0
-    assert L.gq_grad_norm_workspace_bytes(0) == 0 and L.gq_grad_norm_workspace_bytes(-1) == 0
-    assert L.gq_grad_norm_workspace_bytes((1 << 20) + 1) == 0
+    assert bytes_of(s, d, 0) == 0 and bytes_of(s, d, -1) == 0 and bytes_of(s, d, (1 << 20) + 1) == 0
+    assert bytes_of(None, d, n) == 0 and bytes_of(s, None, n) == 0
+    # one cluster: 16 tensors, 1 MiB in chunks of 16 KB
+    few = lists([A16] * 16, [1 << 13] * 16, [1] * 16)
+    assert bytes_of(few[1], few[2], 16) == 0
+    assert bytes_of(*lists([A16], [1 << 19], [0])[1:]) == 0 and bytes_of(*lists([A16], [(1 << 19) + 1], [0])[1:]) > 0
+    assert bytes_of(*lists([A16] * 17, [1] * 17, [1] * 17)[1:]) > 0
+    assert bytes_of(*lists([A16], [0], [0])[1:]) > 0
     assert L.gq_grad_norm(p, s, d, -1, A16, A16, size, None) == 1
     assert L.gq_grad_norm(None, s, d, n, A16, A16, size, None) == 1
     assert L.gq_grad_norm(p, None, d, n, A16, A16, size, None) == 1
@@ -135,7 +142,7 @@ def test_overlaps(gq, grads, outs, sizes):
     n = len(grads)
     p, s, d, _ = lists(grads, sizes, [0] * n)
     o = None if outs is None else (ctypes.c_void_p * n)(*outs)
-    size = gq.lib().gq_grad_norm_workspace_bytes(n)
+    size = 1 << 20
     assert gq.lib().gq_clip_grads(p, o, s, d, n, 1.0, None, A16, A16, size, None) == 1
     assert b"overlap" in gq.lib().gq_last_error()
 

@@ -37,6 +37,17 @@ def draw(gen, n, dtype, shift=0, scale=1.0):
     return t[shift:]
 
 
+def like(t):
+    """A copy that lies as t does in its 16 bytes: the order of the sum, and with
+    it the norm's last bit, goes by the sizes and by that."""
+    size = t.element_size()
+    c = torch.empty(t.numel() + 16, dtype=t.dtype, device=DEV)
+    at = (t.data_ptr() - c.data_ptr()) % 16 // size
+    c = c[at:at + t.numel()]
+    assert t.numel() == 0 or c.data_ptr() % 16 == t.data_ptr() % 16
+    return c.copy_(t)
+
+
 LISTS = [
     [(1, torch.float32, 0)],
     [(1, torch.bfloat16, 3)],
@@ -48,6 +59,12 @@ LISTS = [
     [(i * 7919 % 5000, torch.float32 if i % 3 else torch.bfloat16, i % 4) for i in range(1025)],
     [(3, torch.bfloat16, i % 8) for i in range(2100)],
     [(40_000_003, torch.bfloat16, 1), (11_000_001, torch.float32, 1)],
+    # the largest lists of one cluster, and just past them
+    [(262144, torch.float32, 0)],
+    [(262144, torch.float32, 3), (1, torch.bfloat16, 0)],
+    [(32768, torch.bfloat16, i % 8) for i in range(16)],
+    [(30000, torch.bfloat16, i % 8) for i in range(17)],
+    [(70000, torch.float32, 1), (70001, torch.bfloat16, 3)],
 ]
 
 
@@ -67,7 +84,7 @@ def test_norm_and_clip(gq, sizes):
         before = [t.clone() for t in ts]
         got = gq.clip_grads(ts, most, out=views)
         assert torch.equal(got, norm)
-        placed = [t.clone() for t in ts]  # and in place
+        placed = [like(t) for t in ts]  # and in place
         assert torch.equal(gq.clip_grads(placed, most), norm)
         for i, (t, b, v, o, p) in enumerate(zip(ts, before, views, outs, placed)):
             assert torch.equal(t, b)  # the inputs of a call with outputs stay
@@ -185,16 +202,16 @@ def test_refusals(gq):
 def test_streams_and_graphs(gq):
     gen = torch.Generator(device=DEV).manual_seed(8)
     ts = [draw(gen, 300_001, torch.bfloat16, 1), draw(gen, 5000, torch.float32)]
-    want = [t.clone() for t in ts]
+    want = [like(t) for t in ts]
     norm = gq.clip_grads(want, 1.0)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    got = [t.clone() for t in ts]
+    got = [like(t) for t in ts]
     side.wait_stream(torch.cuda.current_stream())
     n1 = gq.clip_grads(got, 1.0, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(n1, norm) and all(torch.equal(a, b) for a, b in zip(got, want))
-    work, outs = [t.clone() for t in ts], [torch.empty_like(t) for t in ts]
+    work, outs = [like(t) for t in ts], [torch.empty_like(t) for t in ts]
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     other = torch.cuda.CUDAGraph()
