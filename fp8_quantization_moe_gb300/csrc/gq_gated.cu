@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BackwardParams
 #pragma unroll
   for (int j = 0; j < kUnit; ++j) {
     const float s = sigma(act_z(p.act, x[j]));
-    const float dx = g[j] * u[j] * act_slope(p.act, x[j], s);
+    // the slope first: where it is 0, g u may be past fp32's range
+    const float dx = g[j] * act_slope(p.act, x[j], s) * u[j];
     u[j] = g[j] * act_value(x[j], s);
     x[j] = dx;
   }

@@ -480,7 +480,7 @@ gq_status gq_grouped_gated_mm(const void* qa, const float* sa, int64_t M, const 
 
 /*
  * The gradients of x and u from g, that of h:
- *     dx = g * u * act'(x),  act'(x) = sigma + x * sigma * (1 - sigma) * dz/dx
+ *     dx = g * act'(x) * u,  act'(x) = sigma + x * sigma * (1 - sigma) * dz/dx
  *     du = g * act(x)
  * in fp32, for every row (rows have no groups here).
  *
@@ -489,7 +489,8 @@ gq_status gq_grouped_gated_mm(const void* qa, const float* sa, int64_t M, const 
  *   pre      g's type [rows, 2, N], 16-byte aligned: x and u.      (input)
  *   rows, N  N % 16 == 0, N <= 2^22; rows * ceil(N / 128) < 2^31.
  *   out      g's type [rows, 2, N], 16-byte aligned, or NULL: dx and du.  It
- *            may be pre itself, but overlap no input otherwise.   (output)
+ *            may be pre itself, but no output overlaps an input otherwise.
+ *                                                                 (output)
  *   q, scales   e4m3 [rows, 2, N], 16-byte aligned, and fp32 [rows, 2,
  *            ceil(N / 128)], or NULL: dx and du quantized as
  *            gq_fp8_block_rows does it, from the fp32 values.  One of out and

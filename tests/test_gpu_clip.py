@@ -98,6 +98,20 @@ def test_norm_and_clip(gq, sizes):
                 assert torch.equal(p, t)
 
 
+def test_past_2_31_elements(gq):
+    n = 2 ** 31 + 12_345
+    t = torch.zeros(n + 1, dtype=torch.bfloat16, device=DEV)[1:]
+    at = [0, 5, 2 ** 30, 2 ** 31 - 1, 2 ** 31, n - 1]
+    t[at] = 2.0
+    want = 2.0 * math.sqrt(len(at))
+    assert abs(float(gq.grad_norm([t])) - want) <= NORM_TOL * want
+    o = torch.empty(n, dtype=torch.bfloat16, device=DEV)
+    gq.clip_grads([t], want / 2, out=[o])  # a factor of a half
+    assert o[at].tolist() == [1.0] * len(at) and int((o != 0).sum()) == len(at)
+    gq.clip_grads([t], want / 2)
+    assert torch.equal(t, o)
+
+
 def test_norm_is_the_same_every_time(gq):
     gen = torch.Generator(device=DEV).manual_seed(3)
     ts = [draw(gen, 3_000_001, torch.bfloat16, 1), draw(gen, 777_777, torch.float32, 2)]

@@ -456,6 +456,18 @@ def test_backward_extremes(gq, dtype, act):
     assert bool(gq.gated_backward(g, nan, activation=act).out.isnan().all())
 
 
+def test_backward_order_of_factors(gq):
+    """A product of g and u past fp32's range beside a slope that makes up for it."""
+    pre = torch.tensor([[[-100.0] * 8 + [-50.0] * 8, [1e30] * 16]], device=DEV)
+    g = torch.full((1, 16), 1e30, device=DEV)
+    out = gq.gated_backward(g, pre).out[0]
+    x = pre[0, 0].double()
+    sig = torch.sigmoid(x)
+    want = 1e30 * sig * (1 + x * (1 - sig)) * 1e30  # -50: -9e39, past the range; -100: 0 in fp32
+    assert bool((out[0, :8] == 0).all()) and bool((want[8:] < -3.5e38).all())
+    assert bool((out[0, 8:] == float("-inf")).all())
+
+
 def test_backward_blocks_with_nan_and_inf(gq):
     """As block_rows: a NaN does not count, an infinity makes the scale 0."""
     gen = torch.Generator(device=DEV).manual_seed(5)
@@ -557,6 +569,69 @@ def test_empty(gq):
     out = sentinel((4, 48), torch.bfloat16)
     gq.grouped_gated_mm(z(4, 32), z(4, 1, dtype=f), z(2, 2, 48, 32), z(2, 2, 1, 1, dtype=f), offs, out=out)
     assert untouched(out)
+
+
+def test_many_experts(gq):
+    """As many experts as a call takes, most of them without rows."""
+    E, M = 1024, 3000
+    g = torch.Generator(device=DEV).manual_seed(13)
+    offs = torch.randint(0, M + 1, (E,), device=DEV, generator=g).sort().values.tolist()
+    for rows, ends in ((M, offs), (40, [min(o // 75, 40) for o in offs])):  # many rows and few
+        c = Case(rows, 48, 144, ends, seed=14)
+        n = c.end
+        pre, epre, h, eh = c.forward("gelu")
+        r = gq.grouped_gated_mm(*c.args(), activation="gelu", fp8=True, keep=True)
+        check_bf16(r.out[:n], h[:n], eh[:n])
+        check_bf16(r.pre[:n], pre[:n], epre[:n])
+        check_quantized(r.q[:n], r.scales[:n], h[:n], eh[:n])
+        want, S = c.grad()
+        check_bf16(gq.grouped_gated_grad(c.qd, c.sd, c.qb, c.sb, c.offs)[:n], want[:n], 2.0 ** -12 * S[:n])
+
+
+@pytest.mark.parametrize("K", [16, 48])
+def test_past_2_31_elements(gq, K):
+    """Outputs of more than 2^31 elements; K of 48: no multiple of 64, block pairs."""
+    M, N = 140_000, 16384
+    g = torch.Generator(device=DEV).manual_seed(15)
+    qa, sa = codes(g, M, K), scales(g, M, 1)
+    qb, sb = codes(g, 2, 2, N, K), scales(g, 2, 2, N // 128, 1)
+    offs = torch.tensor([70_001, M], dtype=torch.int32, device=DEV)
+    r = gq.grouped_gated_mm(qa, sa, qb, sb, offs, fp8=True, keep=True)
+    rows = torch.tensor([0, 3, 65535, 65536, 70_000, 70_001, 131_071, 131_072, M - 2, M - 1], device=DEV)
+    a = wide(qa[rows], sa[rows], 1)
+    e = (rows >= 70_001).long()
+    pre, S = (torch.stack([torch.stack([f(wide(qb[i, j], sb[i, j], 128)) @ f(x) for j in range(2)])
+                           for x, i in zip(a, e.tolist())]) for f in (lambda v: v, torch.abs))
+    epre = 2.0 ** -12 * S
+    check_bf16(r.pre[rows], pre, epre)
+    x, u = pre[:, 0], pre[:, 1]
+    sig = torch.sigmoid(x)
+    eh = (1.13 * epre[:, 0] * (u.abs() + epre[:, 1]) + (x * sig).abs() * epre[:, 1]
+          + ((x.abs() + 8) * 2.0 ** -22 + 3 * 2.0 ** -24) * (x * sig * u).abs() + 2.0 ** -126 * (x * u).abs())
+    check_bf16(r.out[rows], x * sig * u, eh)
+    check_quantized(r.q[rows], r.scales[rows], x * sig * u, eh)
+    del r
+    # the same sizes the other way round
+    qd, sd = codes(g, M, 2, K), scales(g, M, 2, 1)
+    wb, swb = codes(g, 2, 2, K, N), scales(g, 2, 2, 1, N // 128)
+    out = gq.grouped_gated_grad(qd, sd, wb, swb, offs)
+    gq.check_device_error()
+    for i, row in zip(e.tolist(), rows.tolist()):
+        d = wide(qd[row], sd[row], 1)
+        w = [wide(wb[i, j], swb[i, j], 128) for j in range(2)]
+        want, size = sum(d[j] @ w[j] for j in range(2)), sum(d[j].abs() @ w[j].abs() for j in range(2))
+        check_bf16(out[row], want, 2.0 ** -12 * size)
+
+
+def test_backward_past_2_31_elements(gq):
+    M, N = 70_000, 16384
+    g = torch.empty(M, N, dtype=torch.bfloat16, device=DEV).normal_()
+    pre = torch.empty(M, 2, N, dtype=torch.bfloat16, device=DEV).normal_()
+    r = gq.gated_backward(g, pre, fp8=True)
+    for row in (0, 32767, 32768, 65535, 65536, M - 1):
+        one = gq.gated_backward(g[row:row + 1].clone(), pre[row:row + 1].clone(), fp8=True)
+        for a, b in zip(r[:3], one[:3]):
+            assert torch.equal(a[row:row + 1].view(torch.uint8), b.view(torch.uint8))
 
 
 def test_refusals(gq):
