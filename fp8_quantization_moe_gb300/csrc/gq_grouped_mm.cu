@@ -358,8 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // rows: K-major; weights: K-major rows of 128 bytes, or MN-major
             // (32 contraction rows = 4 KB, one block's halves of the columns kWHalf apart)
             const uint32_t d = tmem + b * kCols, a0 = stage0 + st * kStageBytes;
-            uint64_t ad = operand_desc_sw128(a0);
-            uint64_t wd = operand_desc_sw128(a0 + kABytes, kWHalf);
+            const uint64_t ad = operand_desc_sw128(a0), wd = operand_desc_sw128(a0 + kABytes, kWHalf);
             ok = mbar_wait_addr(full + st * 8, st_use & 1, wait_ns, p.err) &&
                  mbar_wait_addr(acc_empty + b * 8, (use & 1) ^ 1u, wait_ns, p.err);
             if (!ok) break;
@@ -368,11 +367,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                       ((static_cast<uint32_t>(s.cols[st]) >> 3) << 17);
             tc_fence_after();
             G::template mma<false>(d, ad, wd, idesc);
+            if (left >= kBlock) {
 #pragma unroll
-            for (int j = 1; j < kBlock / kSubK; ++j) {
-              ad += kSubK >> 4;
-              wd += wstep;
-              if (j * kSubK < left) G::template mma<true>(d, ad, wd, idesc);
+              for (int j = 1; j < kBlock / kSubK; ++j)
+                G::template mma<true>(d, ad + j * (kSubK >> 4), wd + j * wstep, idesc);
+            } else {
+#pragma unroll 1
+              for (int j = 1; j * kSubK < left; ++j)
+                G::template mma<true>(d, ad + j * (kSubK >> 4), wd + j * wstep, idesc);
             }
             G::commit(&s.done[st]);
             issued = true;
