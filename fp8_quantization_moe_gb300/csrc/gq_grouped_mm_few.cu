@@ -99,6 +99,7 @@ __device__ __forceinline__ void store_bf16(const float (&v)[kN][kUnit], uint16_t
   for (int u = 0; u < kN; ++u)
 #pragma unroll
     for (int j = 0; j < kUnit; j += 2) {
+      if (u * kUnit + j >= rows) continue;  // a unit's rows may end early
       const float give = odd ? v[u][j] : v[u][j + 1];
       const float got = __shfl_xor_sync(0xffffffffu, give, 1);
       const uint32_t w = odd ? bf16x2_of(got, v[u][j + 1]) : bf16x2_of(v[u][j], got);
@@ -134,6 +135,7 @@ __device__ __forceinline__ bool gated_store(const Params& p, Smem<kGated>& s, co
     float m = 0.0f;  // of row `lane & 15`
 #pragma unroll
     for (int j = 0; j < kUnit; ++j) {
+      if (a * kUnit + j >= rows) continue;
       float v = c < p.outer ? fmaxf(fabsf(x[a][j]), 0.0f) : 0.0f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -150,6 +152,7 @@ __device__ __forceinline__ bool gated_store(const Params& p, Smem<kGated>& s, co
   for (int a = 0; a < kN; ++a)
 #pragma unroll
     for (int j = 0; j < kUnit; j += 4) {
+      if (a * kUnit + j >= rows) continue;
       // four rows: a lane's bytes of its column, then by two exchanges of bytes the
       // bytes of four columns of one row, lane & 3
       uint32_t w = 0;
