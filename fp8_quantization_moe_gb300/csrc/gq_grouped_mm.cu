@@ -23,8 +23,9 @@
 //
 // What bounds it, 16,640 rows in 16 groups (16 matrices of 8192 x 4096):
 // * a long run, the power limit: the clock falls to 1.5 GHz where it is 1.8 for
-//   a single call.  grad_input of the gated block 500 us (2.2 PFLOP/s), of which
-//   420 are left without multiply-adds, TMEM loads and stores;
+//   a single call.  grad_input of the gated block 480 to 515 us (2.2 to 2.3
+//   PFLOP/s), by the card; where it took 506, 418 were left without
+//   multiply-adds, TMEM loads and stores;
 // * one call, 811 cycles a 128-block, 455 us: the MMAs are 512 and the operands
 //   770, 48 KB at the 64 bytes a cycle that L2 delivers to an SM.  A pair of
 //   blocks (cta_group::2) loads 32 KB per block, but its accumulators are
@@ -32,14 +33,14 @@
 //   (1100 cycles: release, first MMA, completion, wake-up) takes the place of the
 //   loads: 860 cycles, and a group is padded to 256 rows.  Halves of the
 //   accumulators released apart (MMAs of N = 128): the same 460 and 490 us;
-//   two issuing warps, three barriers probed ahead: no faster.
+//   two issuing warps, three barriers probed ahead: no faster;
 // * rows that are not whole lines, pairs of blocks (see kPairRows): 24,500 live
-//   rows of 40 experts, 1360 x 2064, gated to fp8: 264 -> 195 us, halves released
-//   apart 190.
-// The gated form adds 3200 cycles a tile for the stores of 112 KB (both rows
-// and projections, 32 bytes a cycle) and 2000 for the activation (two MUFU
-// operations a value): 16 x 2 x 4096 x 4096, everything written: 535 us, in a
-// long run 570; the plain product with the same matrices 471 and 509.
+//   rows of 40 experts, 1360 x 2064, gated to fp8: 264 us alone, 163 to 190 in
+//   pairs.
+// The gated form adds 3500 cycles a tile for the stores of 112 KB (both rows
+// and projections, 32 bytes a cycle) and 1600 for the activation: 16 x 2 x 4096 x
+// 4096, everything written: 525 us, in a long run 545 to 570; the plain product
+// with the same matrices 467 and 490 to 530.
 //
 // One persistent block per SM; its warps:
 //   0-7   epilogue: lane quarter w % 4 (32 rows), column half w / 4 (gated: 64
@@ -85,7 +86,7 @@ struct Smem {
   uint8_t stage[kStages][kStageBytes];  // 1024-byte aligned (swizzle atoms)
   float factor[kScaleRing][kScaleKb][2][kRows];  // of the tile's two column halves
   int4 tile[kScaleRing];         // the entry's tile: first row and rows of this block, first column
-  int32_t cols[kStages];         // half_cols of the stage's tile
+  int32_t cols[kStages];         // mma_cols of the stage's tile
   TileTable tiles;
   uint64_t full[kStages];         // the stage's loads in every block (the first block)
   uint64_t done[kStages];         // its MMAs are complete: the stage is free, the accumulator full
@@ -198,8 +199,8 @@ __device__ __forceinline__ void swap_with(uint32_t& a, uint32_t& b, int lane) {
     b = got;
 }
 
-// A store of this warp's rows: `out` points at column c of row (lane & ~3) of the
-// warp, rows `pitch` elements apart.  32 columns: four lanes exchange their
+// Stores 64 bytes of each of this warp's rows, `out` pointing at this lane's part
+// of them in row (lane & ~3): four lanes exchange their
 // rows' 16-byte parts by shuffles, so that a store covers 64-byte runs of eight
 // rows.  (Staged in shared memory: 456 us instead of 452; sent from there by
 // TMA, with a stage less for the operands, 480; without an exchange 495;

@@ -5,6 +5,10 @@
 // 2048 to N 4096: 14.3 us, of which 9.9 us are the weights and most of the
 // rest the launch, the first loads and the last tile.
 //
+// In the gated form a tile has 128 columns of both projections and up to 64 rows:
+// one token to eight of 64 experts, 2 x 2048 x 4096, 134 MB: 24.6 us, of which the
+// loads take 21.4; 512 rows of 64 experts, 2 x 1424 x 2064: 58.3 us, 6.5 TB/s.
+//
 // Here the weights are the MMA's M operand (128 output columns) and the rows
 // its N operand, up to 128 of them in steps of 16: an MMA costs as many cycles
 // as there are rows, and four accumulators keep the tensor cores, the epilogue

@@ -624,9 +624,9 @@ int gq_version(void);
  *          amax-complete signal of the (first row band, first group) unit
  *          (waiters: the warps that would cast it), or, in a call that
  *          splits units, the count of the first split unit's first part
- *          (waiters: the other parts); grouped_wgrad and grouped_mm: the
- *          release of thread block 0's first TMEM accumulator (waiter: the
- *          block's MMA warp);
+ *          (waiters: the other parts); grouped_wgrad, grouped_mm and the
+ *          gated block's products: the release of thread block 0's first TMEM
+ *          accumulator (waiter: the block's MMA warp);
  *   bit 1  rowwise_t never splits units across blocks (results are the
  *          same; the path a call takes when it does not find all of its
  *          blocks resident).

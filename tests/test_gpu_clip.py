@@ -177,6 +177,15 @@ def test_given_norm(gq):
     assert float(norm) == 50.0
 
 
+def test_no_tensors(gq):
+    """The C call takes an empty list: its norm is 0."""
+    norm = torch.full((), 7.0, device=DEV)
+    assert gq.lib().gq_grad_norm(None, None, None, 0, norm.data_ptr(), None, 0, None) == 0
+    assert gq.lib().gq_clip_grads(None, None, None, None, 0, 1.0, None, norm.data_ptr(), None, 0, None) == 0
+    torch.cuda.synchronize()
+    assert float(norm) == 0.0
+
+
 def test_norm_counts_a_tensor_as_often_as_it_comes(gq):
     t = torch.full((1000,), 2.0, device=DEV)
     assert abs(float(gq.grad_norm([t, t, t[10:20]])) - math.sqrt(4 * 2010)) <= NORM_TOL * 90
