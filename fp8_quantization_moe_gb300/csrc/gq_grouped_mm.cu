@@ -723,7 +723,7 @@ gq_status setup(DeviceInfo& info) {
       "grouped_mm: resident block pairs");
   if (st != GQ_OK) return st;
   if (info.mm_pairs < 1) info.mm_pairs = 1;
-  return setup_few();
+  return setup_few(info);
 }
 
 namespace {

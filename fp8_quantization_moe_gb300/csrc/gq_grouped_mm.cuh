@@ -139,7 +139,7 @@ __device__ __forceinline__ Tile tile_of(const Params& p, const TileTable& s, int
 
 // The product of many rows per group (gq_grouped_mm.cu) and of few
 // (gq_grouped_mm_few.cu).
-gq_status setup_few();
+gq_status setup_few(DeviceInfo& info);
 gq_status encode_rows(CUtensorMap* map, const Params& p, const void* qa, uint32_t rows);
 gq_status encode_weights(CUtensorMap* map, const Params& p, const void* qb, int32_t N, int32_t K);
 gq_status launch_few(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,

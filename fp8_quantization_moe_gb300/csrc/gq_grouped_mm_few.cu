@@ -37,6 +37,7 @@ constexpr int kUnit = 16;      // rows of a tile come in units
 constexpr int kWBytes = kCols * kBlock;   // 16 KB
 constexpr int kScaleKb = 4;    // 128-blocks per entry of the factor ring
 constexpr int kScaleRing = 4;
+constexpr int kMostParts = 8;  // blocks that share a tile, at most
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (kEpiWarps + 3) * 32;
 
@@ -53,6 +54,10 @@ struct Sizes {
   static constexpr int kBufs = 512 / kAccCols;
   static_assert(kEpiWarps == 4 * (kTok / kWarpTok), "two warps per lane quarter");
 };
+// Accumulators in use: of a split tile three, so that also a block with one entry of
+// four 128-blocks waits for a release, and notices one that does not come.
+template <int kForm, bool kSplit>
+constexpr uint32_t kBufsOf = kSplit ? 3 : Sizes<kForm>::kBufs;
 
 template <int kForm>
 struct Smem {
@@ -82,6 +87,28 @@ __device__ __forceinline__ int32_t units_of(const Tile& t) {
   return (min(t.rows, Sizes<kForm>::kTok) + kUnit - 1) / kUnit;
 }
 
+// Where the tiles are too few for the SMs, `parts` blocks, a cluster, share one:
+// each forms the sum of a run of the contraction's 128-blocks, and the first
+// block adds the others' sums from their shared memory, in order.  (One tile a
+// cluster: the launch sees to it.)
+struct Split {
+  int32_t rank, parts;
+  int32_t kb0, kb1;  // this block's 128-blocks, from a whole entry of the factor ring on
+};
+
+template <bool kSplit>
+__device__ __forceinline__ Split split_of(const Params& p) {
+  Split v = {0, 1, 0, p.kbs};
+  if (kSplit) {
+    v.rank = static_cast<int32_t>(cluster_rank());
+    v.parts = static_cast<int32_t>(cluster_size());
+    const int32_t entries = (p.kbs + kScaleKb - 1) / kScaleKb;
+    v.kb0 = entries * v.rank / v.parts * kScaleKb;
+    v.kb1 = min(p.kbs, entries * (v.rank + 1) / v.parts * kScaleKb);
+  }
+  return v;
+}
+
 // Positions in the rings, common to a tile's steps.
 struct Rings {
   uint32_t b = 0;              // accumulator
@@ -89,6 +116,7 @@ struct Rings {
   uint32_t r = 0, sc_use = 0;  // entry of the factor ring, its use
   uint32_t shares = 0;         // kGated: exchanges of maxima so far
   bool hold = false;           // test hook: withhold the next release
+  bool joined = false;         // split: this warp has met the cluster's barrier
 };
 
 // Rows of 128-columns' values in TMEM lanes (a lane is a column c) to bf16 rows:
@@ -184,10 +212,10 @@ __device__ __forceinline__ bool gated_store(const Params& p, Smem<kGated>& s, co
 
 // A tile of which this warp has kU * 16 rows from row j0 on (kU = 0: none, it
 // only keeps step); false if a wait expired.
-template <int kForm, int kU>
-__device__ __forceinline__ bool tile_body(const Params& p, Smem<kForm>& s, const Tile& t, Rings& x,
-                                          uint32_t tmem0, int32_t j0, int q, int lane,
-                                          uint64_t wait_ns) {
+template <int kForm, bool kSplit, int kU>
+__device__ __forceinline__ bool tile_body(const Params& p, const Split& part, Smem<kForm>& s,
+                                          const Tile& t, Rings& x, uint32_t tmem0, int32_t j0,
+                                          int q, int lane, uint64_t wait_ns) {
   using Z = Sizes<kForm>;
   constexpr int kN = kU > 0 ? kU : 1;
   float acc[Z::kMats][kN][kUnit];
@@ -198,7 +226,7 @@ __device__ __forceinline__ bool tile_body(const Params& p, Smem<kForm>& s, const
   const uint32_t done = smem_addr(s.done), fac_full = smem_addr(s.fac_full);
   const uint32_t factors = smem_addr(s.factor), acc_empty = smem_addr(s.acc_empty);
 #pragma unroll 1
-  for (int32_t kb = 0; kb < p.kbs; ++kb) {
+  for (int32_t kb = part.kb0; kb < part.kb1; ++kb) {
     const uint32_t e = kb % kScaleKb;
     if (e == 0 && !mbar_wait_warp(fac_full + x.r * 8, x.sc_use & 1, wait_ns, p.err)) return false;
     if (!mbar_wait_warp(done + x.st * 8, x.use & 1, wait_ns, p.err)) return false;
@@ -235,18 +263,64 @@ __device__ __forceinline__ bool tile_body(const Params& p, Smem<kForm>& s, const
                 __fmaf_rn(__uint_as_float(h[i][u][4 * v + j]), w[j], acc[i][u][4 * v + j]);
         }
       }
-    if (++x.b == Z::kBufs) x.b = 0;
+    if (++x.b == kBufsOf<kForm, kSplit>) x.b = 0;
     if (++x.st == Z::kStages) {
       x.st = 0;
       ++x.use;
     }
-    if (e == kScaleKb - 1 || kb == p.kbs - 1) {
+    if (e == kScaleKb - 1 || kb == part.kb1 - 1) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.fac_empty[x.r]);
       if (++x.r == kScaleRing) {
         x.r = 0;
         ++x.sc_use;
       }
+    }
+  }
+  if constexpr (kSplit) {
+    // The stages are free: all MMAs of the block are complete.  Four rows of a
+    // column are one 16-byte word.
+    const uint32_t own = smem_addr(s.stage) + (j0 / 4 * kCols + 32 * q + lane) * 16;
+    constexpr uint32_t kQuad = kCols * 16, kMat = Z::kTok / 4 * kQuad;
+    if (part.rank > 0)
+#pragma unroll
+      for (int a = 0; a < kU * kUnit; a += 4)
+        if (j0 + a < t.rows)
+#pragma unroll
+          for (int i = 0; i < Z::kMats; ++i) {
+            const float* v = &acc[i][a / kUnit][a % kUnit];
+            sts128(own + i * kMat + a / 4 * kQuad,
+                   make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                              __float_as_uint(v[3])));
+          }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    x.joined = true;
+    if (part.rank > 0) return true;
+    uint32_t from[kMostParts - 1];
+#pragma unroll
+    for (int r = 1; r < kMostParts; ++r) from[r - 1] = map_cluster(own, min(r, part.parts - 1));
+#pragma unroll
+    for (int a = 0; a < kU * kUnit; a += 4) {
+      if (j0 + a >= t.rows) continue;
+      // of every block at once (a missing one's place: the last one's again), added in order
+      uint4 v[Z::kMats][kMostParts - 1];
+#pragma unroll
+      for (int r = 0; r < kMostParts - 1; ++r)
+#pragma unroll
+        for (int i = 0; i < Z::kMats; ++i) v[i][r] = ld_cluster_128(from[r] + i * kMat + a / 4 * kQuad);
+#pragma unroll
+      for (int r = 0; r < kMostParts - 1; ++r)
+        if (r < part.parts - 1)
+#pragma unroll
+          for (int i = 0; i < Z::kMats; ++i) {
+            float* o = &acc[i][a / kUnit][a % kUnit];
+            o[0] += __uint_as_float(v[i][r].x);
+            o[1] += __uint_as_float(v[i][r].y);
+            o[2] += __uint_as_float(v[i][r].z);
+            o[3] += __uint_as_float(v[i][r].w);
+          }
     }
   }
   if constexpr (kU == 0) {
@@ -261,17 +335,20 @@ __device__ __forceinline__ bool tile_body(const Params& p, Smem<kForm>& s, const
   }
 }
 
-template <int kForm>
+template <int kForm, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     few_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                const Params p) {
   using Z = Sizes<kForm>;
   constexpr bool kT = is_transposed(kForm);
-  constexpr int kTok = Z::kTok, kStages = Z::kStages, kBufs = Z::kBufs;
+  constexpr int kTok = Z::kTok, kStages = Z::kStages;
+  constexpr uint32_t kBufs = kBufsOf<kForm, kSplit>;
   extern __shared__ uint8_t smem_raw[];
   Smem<kForm>& s = *reinterpret_cast<Smem<kForm>*>(smem_raw + (-smem_addr(smem_raw) & 1023u));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
+  const Split part = split_of<kSplit>(p);
+  const int32_t groups = gridDim.x / part.parts, group = blockIdx.x / part.parts;
   const uint64_t wait_ns = 4 * p.timeout_ns;
 
   if (warp == kEpiWarps && lane == 0) {
@@ -282,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.full[i], 1);
       mbar_init(&s.done[i], 1);
     }
-    for (int b = 0; b < kBufs; ++b) mbar_init(&s.acc_empty[b], kEpiWarps);
+    for (uint32_t b = 0; b < kBufs; ++b) mbar_init(&s.acc_empty[b], kEpiWarps);
     for (int i = 0; i < kScaleRing; ++i) {
       mbar_init(&s.fac_full[i], 1);
       mbar_init(&s.fac_empty[i], kEpiWarps);
@@ -304,17 +381,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s.tmem_base;
   const int32_t tiles = s.tiles.first[p.E] * p.tiles_c;  // below 2^31: the host checks
 
+  bool joined = false;
   if (warp == kEpiWarps) {
     // ------------------------------------------------------------ loads --
     const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
     const uint32_t done = smem_addr(s.done);
     uint32_t st = 0, use = 0;
     bool ok = true;
-    for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+    for (int32_t i = group; ok && i < tiles; i += groups) {
       const Tile t = tile_of(p, s.tiles, i, kTok, kCols, lane);
       const int32_t units = units_of<kForm>(t);
       const uint32_t bytes = Z::kMats * kWBytes + units * (kUnit * kBlock);
-      for (int32_t kb = 0; kb < p.kbs; ++kb) {
+      for (int32_t kb = part.kb0; kb < part.kb1; ++kb) {
         const int32_t k = column_of<kForm>(p, kb), half = half_of<kForm>(p, kb);
         ok = mbar_wait_warp(done + st * 8, (use & 1) ^ 1u, wait_ns, p.err);
         if (!ok) break;
@@ -353,12 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t wstep = kT ? (kSubK * kBlock) >> 4 : kSubK >> 4;
     uint32_t st = 0, st_use = 0, b = 0, use = 0;
     bool ok = true, issued = false;
-    for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+    for (int32_t i = group; ok && i < tiles; i += groups) {
       const Tile t = tile_of(p, s.tiles, i, kTok, kCols, lane);
       const uint32_t n = __shfl_sync(0xffffffffu, units_of<kForm>(t) * kUnit, 0);
       // D fp32, e4m3 x e4m3, M = 128, A MN-major if transposed, N = n
       const uint32_t idesc = (1u << 4) | (kT ? 1u << 15 : 0u) | ((n >> 3) << 17) | (8u << 24);
-      for (int32_t kb = 0; kb < p.kbs; ++kb) {
+      for (int32_t kb = part.kb0; kb < part.kb1; ++kb) {
         const int32_t left = p.inner - column_of<kForm>(p, kb);
         ok = mbar_wait_warp(acc_empty + b * 8, (use & 1) ^ 1u, wait_ns, p.err) &&
              mbar_wait_warp(full + st * 8, st_use & 1, wait_ns, p.err);
@@ -403,10 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------- factors --
     // the scales of an entry are loaded while the one before is worked on
     float v[kTok / 32][kScaleKb] = {}, w[Z::kMats][kScaleKb];
-    int32_t i = blockIdx.x, kb = 0, rows = 0;
+    int32_t i = group, kb = part.kb0, rows = 0;
     Tile t = {};
     auto load = [&]() {  // the entry (tile i, 128-blocks kb ..)
-      if (kb == 0) t = tile_of(p, s.tiles, i, kTok, kCols, lane);
+      if (kb == part.kb0) t = tile_of(p, s.tiles, i, kTok, kCols, lane);
       rows = min(t.rows, kTok);
 #pragma unroll
       for (int m = 0; m < Z::kMats; ++m) {
@@ -448,9 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       const int32_t have = rows;
       kb += kScaleKb;
-      if (kb >= p.kbs) {
-        kb = 0;
-        i += gridDim.x;
+      if (kb >= part.kb1) {
+        kb = part.kb0;
+        i += groups;
       }
       if (i < tiles) load();
       ok = mbar_wait_warp(empty + r * 8, (use & 1) ^ 1u, wait_ns, p.err);
@@ -478,17 +556,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     Rings x;
     x.hold = p.skip_arrival && blockIdx.x == 0;
     bool ok = true;
-    for (int32_t i = blockIdx.x; ok && i < tiles; i += gridDim.x) {
+    for (int32_t i = group; ok && i < tiles; i += groups) {
       const Tile t = tile_of(p, s.tiles, i, kTok, kCols, lane);
       switch (min(units_of<kForm>(t) - j0 / kUnit, kMost)) {
-        case 4: ok = tile_body<kForm, (kMost < 4 ? kMost : 4)>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
-        case 3: ok = tile_body<kForm, (kMost < 3 ? kMost : 3)>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
-        case 2: ok = tile_body<kForm, 2>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
-        case 1: ok = tile_body<kForm, 1>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
-        default: ok = tile_body<kForm, 0>(p, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 4: ok = tile_body<kForm, kSplit, (kMost < 4 ? kMost : 4)>(p, part, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 3: ok = tile_body<kForm, kSplit, (kMost < 3 ? kMost : 3)>(p, part, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 2: ok = tile_body<kForm, kSplit, 2>(p, part, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        case 1: ok = tile_body<kForm, kSplit, 1>(p, part, s, t, x, tmem0, j0, q, lane, wait_ns); break;
+        default: ok = tile_body<kForm, kSplit, 0>(p, part, s, t, x, tmem0, j0, q, lane, wait_ns); break;
       }
     }
     tc_fence_before();
+    joined = x.joined;
+  }
+  if (kSplit) {
+    // Every thread meets the cluster's barrier twice: with the sums written, and
+    // with them read, before a block that holds some may leave.
+    __syncwarp();
+    if (!joined) {
+      cluster_arrive();
+      cluster_wait();
+    }
+    cluster_arrive();
+    cluster_wait();
   }
 
   __syncthreads();
@@ -502,11 +592,41 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-template <int kForm>
-gq_status setup_form() {
-  return check_cuda(cudaFuncSetAttribute(few_kernel<kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+// The gated forms share tiles; the plain products add their 128-blocks in one
+// order, whatever the sizes, as they always have.
+constexpr bool may_split(int form) { return form == kGated || form == kGatedGrad; }
+
+template <int kForm, bool kSplit>
+gq_status setup_kernel() {
+  return check_cuda(cudaFuncSetAttribute(few_kernel<kForm, kSplit>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem_bytes<kForm>())),
                     "grouped_mm: shared memory size");
+}
+
+template <int kForm>
+gq_status setup_form() {
+  const gq_status st = setup_kernel<kForm, false>();
+  if constexpr (may_split(kForm))
+    if (st == GQ_OK) return setup_kernel<kForm, true>();
+  return st;
+}
+
+// Blocks per tile, at most a portable cluster's: as many as are resident at once
+// if every group has rows, each with an entry of the factor ring at least.  In
+// us, one block / as many as this gives:
+//   one token to 8 of 128, gated, 2 x 768 x 2048     10.9 / 10.3
+//   to 2 of 8, 2 x 2048 x 4096                       16.4 / 10.9
+//   to one of 16, 2 x 1024 x 8192                    27.8 / 9.2
+//   to 2 of 8, 2 x 768 x 2048                        10.1 / 7.0
+//   to 2 of 8, grad_input, 2 x 4096 x 2048           20.9 / 9.7
+//   16 rows of one expert, gated, 2 x 2048 x 4096    18.3 / 12.8
+// (With two entries each at least the fourth takes 8.0, with four each 10.1.)
+int32_t parts_of(const DeviceInfo& info, const Params& p, int64_t most) {
+  const int32_t entries = (p.kbs + kScaleKb - 1) / kScaleKb;
+  int32_t n = 0;
+  while (n < 3 && most <= info.mm_split[n + 1] && (2 << n) <= entries) ++n;
+  return 1 << n;
 }
 
 template <int kForm>
@@ -523,17 +643,41 @@ gq_status launch_form(const DeviceInfo& info, Params& p, const void* qa, const v
       (static_cast<int64_t>(p.M) / kTok + (p.E < p.M ? p.E : p.M)) * p.tiles_c;  // any offsets
   if (most > INT32_MAX)
     return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: %lld tiles", static_cast<long long>(most));
+  if constexpr (may_split(kForm)) {
+    const int32_t parts = parts_of(info, p, most);
+    if (parts > 1)
+      return launch_chained("grouped_mm: launch", few_kernel<kForm, true>,
+                            dim3(static_cast<unsigned>(most * parts)), kThreads,
+                            smem_bytes<kForm>(), stream, parts, amap, wmap, p);
+  }
   const unsigned grid = static_cast<unsigned>(most < info.sm_count ? most : info.sm_count);
-  return launch_chained("grouped_mm: launch", few_kernel<kForm>, dim3(grid), kThreads,
+  return launch_chained("grouped_mm: launch", few_kernel<kForm, false>, dim3(grid), kThreads,
                         smem_bytes<kForm>(), stream, 1, amap, wmap, p);
 }
 
 }  // namespace
 
-gq_status setup_few() {
+gq_status setup_few(DeviceInfo& info) {
   for (const gq_status st : {setup_form<kForward>(), setup_form<kTransposed>(), setup_form<kGated>(),
                              setup_form<kGatedGrad>()})
     if (st != GQ_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<kGated>();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  for (int n = 1; n < 4; ++n) {
+    attr.val.clusterDim.x = 1u << n;
+    cfg.gridDim = dim3(static_cast<unsigned>((info.sm_count >> n) << n));
+    const gq_status st = check_cuda(
+        cudaOccupancyMaxActiveClusters(&info.mm_split[n], few_kernel<kGated, true>, &cfg),
+        "grouped_mm: resident clusters");
+    if (st != GQ_OK) return st;
+  }
   return GQ_OK;
 }
 

@@ -22,6 +22,7 @@ struct DeviceInfo {
   int rows_ctas_per_sm = 0;
   int sort_cluster = 0;  // most blocks of the token sort
   int mm_pairs = 0;      // block pairs of a grouped product resident at once
+  int mm_split[4] = {};  // its clusters of 1, 2, 4, 8 blocks that split a contraction
 };
 
 // Launch-time knobs (test hooks).

@@ -348,6 +348,48 @@ def test_pairs_of_blocks_transposed(gq, M, inner, outer, offs):
         check_bf16(out[s:t], a @ b, 2.0 ** -12 * (a.abs() @ b.abs()))
 
 
+# Few rows, long contractions and few tiles: two, four and eight blocks share a tile.
+SPLIT = [
+    # M, inner, outer, offs
+    (1, 1040, 272, [1]),
+    (3, 2064, 144, [0, 1, 1, 3]),
+    (13, 4112, 128, [13]),
+    (40, 4096, 16, [9, 40]),
+    (30, 2000, 1040, [10, 28]),       # rows behind the last end
+    (16, 6160, 400, [16, 3, 16, 20]),
+]
+
+
+@pytest.mark.parametrize("M,inner,outer,offs", SPLIT)
+def test_blocks_that_share_a_tile(gq, M, inner, outer, offs):
+    c, t = Case(M, outer, inner, offs, seed=16), Case(M, inner, outer, offs, seed=17)
+    n = c.end
+    pre, epre, h, eh = c.forward("gelu")
+    out = sentinel((M, outer), torch.bfloat16)
+    r = gq.grouped_gated_mm(*c.args(), activation="gelu", out=out, fp8=True, keep=True)
+    gq.check_device_error()
+    check_bf16(out[:n], h[:n], eh[:n])
+    check_bf16(r.pre[:n], pre[:n], epre[:n])
+    check_quantized(r.q[:n], r.scales[:n], h[:n], eh[:n])
+    assert untouched(out[n:])
+    w, sw = c.qb[:, 0].contiguous(), c.sb[:, 0].contiguous()
+    check_bf16(gq.grouped_mm(c.qa, c.sa, w, sw, c.offs)[:n], pre[:n, 0], epre[:n, 0])
+    want, S = t.grad()
+    got = gq.grouped_gated_grad(t.qd, t.sd, t.qb, t.sb, t.offs)
+    check_bf16(got[:n], want[:n], 2.0 ** -12 * S[:n])
+    w, sw = t.qb[:, 1].contiguous(), t.sb[:, 1].contiguous()
+    d, sd = t.qd[:, 1].contiguous(), t.sd[:, 1].contiguous()
+    back = gq.grouped_mm(d, sd, w, sw, t.offs, transpose_b=True)
+    for e, (a, b) in enumerate(t.bounds):
+        v, x = wide(d[a:b], sd[a:b], 1), wide(w[e], sw[e], 128)
+        check_bf16(back[a:b], v @ x, 2.0 ** -12 * (v.abs() @ x.abs()))
+    for _ in range(20):  # the same bits whichever block comes first
+        again = gq.grouped_gated_mm(*c.args(), activation="gelu", fp8=True, keep=True)
+        assert torch.equal(again.q[:n].view(torch.uint8), r.q[:n].view(torch.uint8))
+        assert torch.equal(again.pre[:n], r.pre[:n])
+        assert torch.equal(gq.grouped_gated_grad(t.qd, t.sd, t.qb, t.sb, t.offs)[:n], got[:n])
+
+
 def test_pairs_contain_nan(gq):
     M, inner, outer, offs = PAIRS[0]
     c = Case(M, outer, inner, offs, seed=12)
@@ -530,12 +572,12 @@ def test_streams_and_graphs(gq, M, N, K, offs):
         assert torch.equal(w.view(torch.uint8), g2[:n].view(torch.uint8))
 
 
-@pytest.mark.parametrize("M,N,K,offs", [(12, 48, 656, [4, 12]), (600, 48, 400, [300, 600]),
-                                         (6200, 2576, 144, [3000, 6200])])
+@pytest.mark.parametrize("M,N,K,offs", [(12, 5008, 656, [4, 12]), (600, 48, 400, [300, 600]),
+                                         (6200, 2576, 144, [3000, 6200]), (5, 4112, 4112, [5])])
 def test_timeouts_are_reported_not_hung(gq, M, N, K, offs):
     """A withheld accumulator release: every role leaves its loop after the
     (shortened) limit, the call reports GQ_ERR_TIMEOUT, the next call is fine.
-    (Few rows, many, and pairs of blocks.)"""
+    (Few rows, many, pairs of blocks, and blocks that share a tile's contraction.)"""
     c, t = Case(M, N, K, offs, seed=8), Case(M, K, N, offs, seed=9)
     calls = [lambda: gq.grouped_gated_mm(*c.args(), fp8=True).q,
              lambda: gq.grouped_gated_grad(t.qd, t.sd, t.qb, t.sb, t.offs)]
