@@ -88,12 +88,16 @@ __device__ __forceinline__ int32_t units_of(const Tile& t) {
 }
 
 // Where the tiles are too few for the SMs, `parts` blocks, a cluster, share one:
-// each forms the sum of a run of the contraction's 128-blocks, and the first
-// block adds the others' sums from their shared memory, in order.  (One tile a
-// cluster: the launch sees to it.)
+// each forms the sum of a run of the contraction's 128-blocks and leaves it in its
+// shared memory; then each adds and writes every parts-th four rows, the sums in
+// the blocks' order.  (One tile a cluster: the launch sees to it.)
 struct Split {
   int32_t rank, parts;
   int32_t kb0, kb1;  // this block's 128-blocks, from a whole entry of the factor ring on
+  // whether the four rows from `row` of a tile on are this block's to write
+  __device__ __forceinline__ bool mine(int32_t row) const {
+    return ((row >> 2) & (parts - 1)) == rank;
+  }
 };
 
 template <bool kSplit>
@@ -125,13 +129,13 @@ struct Rings {
 // 64 bytes of both.  `out` points at column (c & ~1) of row (lane & 1).
 template <int kN>
 __device__ __forceinline__ void store_bf16(const float (&v)[kN][kUnit], uint16_t* out, int64_t pitch,
-                                           int32_t rows, bool c_ok, int lane) {
+                                           int32_t rows, bool c_ok, const Split& part, int lane) {
   const int32_t odd = lane & 1;
 #pragma unroll
   for (int u = 0; u < kN; ++u)
 #pragma unroll
     for (int j = 0; j < kUnit; j += 2) {
-      if (u * kUnit + j >= rows) continue;  // a unit's rows may end early
+      if (u * kUnit + j >= rows || !part.mine(u * kUnit + j)) continue;  // rows may end early
       const float give = odd ? v[u][j] : v[u][j + 1];
       const float got = __shfl_xor_sync(0xffffffffu, give, 1);
       const uint32_t w = odd ? bf16x2_of(got, v[u][j + 1]) : bf16x2_of(v[u][j], got);
@@ -142,7 +146,8 @@ __device__ __forceinline__ void store_bf16(const float (&v)[kN][kUnit], uint16_t
 
 // kGated: the rows of a tile, x and u (columns in lanes), to what is asked for.
 template <int kN>
-__device__ __forceinline__ bool gated_store(const Params& p, Smem<kGated>& s, const Tile& t, Rings& r,
+__device__ __forceinline__ bool gated_store(const Params& p, const Split& part, Smem<kGated>& s,
+                                            const Tile& t, Rings& r,
                                             float (&x)[kN][kUnit], float (&u)[kN][kUnit], int32_t j0,
                                             int q, int lane, uint64_t wait_ns) {
   const int32_t rows = t.rows - j0;
@@ -151,12 +156,12 @@ __device__ __forceinline__ bool gated_store(const Params& p, Smem<kGated>& s, co
   const int64_t row = t.m0 + j0, n = p.outer;
   if (p.pre != nullptr) {
     uint16_t* const to = p.pre + (row + odd) * 2 * n + pair;
-    store_bf16(x, to, 2 * n, rows, c_ok, lane);
-    store_bf16(u, to + n, 2 * n, rows, c_ok, lane);
+    store_bf16(x, to, 2 * n, rows, c_ok, part, lane);
+    store_bf16(u, to + n, 2 * n, rows, c_ok, part, lane);
   }
 #pragma unroll
   for (int a = 0; a < kN; ++a) gated::gate(p.act, x[a], u[a]);
-  if (p.out != nullptr) store_bf16(x, p.out + (row + odd) * n + pair, n, rows, c_ok, lane);
+  if (p.out != nullptr) store_bf16(x, p.out + (row + odd) * n + pair, n, rows, c_ok, part, lane);
   if (p.q == nullptr) return true;
   // the maximum of a row over this warp's 32 columns, then over the four warps
   // that hold its 128 (a NaN does not count; columns past the last hold anything)
@@ -167,7 +172,7 @@ __device__ __forceinline__ bool gated_store(const Params& p, Smem<kGated>& s, co
     float m = 0.0f;  // of row `lane & 15`
 #pragma unroll
     for (int j = 0; j < kUnit; ++j) {
-      if (a * kUnit + j >= rows) continue;
+      if (a * kUnit + j >= rows || !part.mine(a * kUnit + j)) continue;
       float v = c < p.outer ? fmaxf(fabsf(x[a][j]), 0.0f) : 0.0f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -184,7 +189,7 @@ __device__ __forceinline__ bool gated_store(const Params& p, Smem<kGated>& s, co
   for (int a = 0; a < kN; ++a)
 #pragma unroll
     for (int j = 0; j < kUnit; j += 4) {
-      if (a * kUnit + j >= rows) continue;
+      if (a * kUnit + j >= rows || !part.mine(a * kUnit + j)) continue;
       // four rows: a lane's bytes of its column, then by two exchanges of bytes the
       // bytes of four columns of one row, lane & 3
       uint32_t w = 0;
@@ -282,55 +287,56 @@ __device__ __forceinline__ bool tile_body(const Params& p, const Split& part, Sm
     // column are one 16-byte word.
     const uint32_t own = smem_addr(s.stage) + (j0 / 4 * kCols + 32 * q + lane) * 16;
     constexpr uint32_t kQuad = kCols * 16, kMat = Z::kTok / 4 * kQuad;
-    if (part.rank > 0)
 #pragma unroll
-      for (int a = 0; a < kU * kUnit; a += 4)
-        if (j0 + a < t.rows)
+    for (int a = 0; a < kU * kUnit; a += 4)
+      if (j0 + a < t.rows && !part.mine(a))
 #pragma unroll
-          for (int i = 0; i < Z::kMats; ++i) {
-            const float* v = &acc[i][a / kUnit][a % kUnit];
-            sts128(own + i * kMat + a / 4 * kQuad,
-                   make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                              __float_as_uint(v[3])));
-          }
+        for (int i = 0; i < Z::kMats; ++i) {
+          const float* v = &acc[i][a / kUnit][a % kUnit];
+          sts128(own + i * kMat + a / 4 * kQuad,
+                 make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                            __float_as_uint(v[3])));
+        }
     __syncwarp();
     cluster_arrive();
     cluster_wait();
     x.joined = true;
-    if (part.rank > 0) return true;
-    uint32_t from[kMostParts - 1];
+    uint32_t from[kMostParts];
 #pragma unroll
-    for (int r = 1; r < kMostParts; ++r) from[r - 1] = map_cluster(own, min(r, part.parts - 1));
+    for (int r = 0; r < kMostParts; ++r) from[r] = map_cluster(own, min(r, part.parts - 1));
 #pragma unroll
     for (int a = 0; a < kU * kUnit; a += 4) {
-      if (j0 + a >= t.rows) continue;
-      // of every block at once (a missing one's place: the last one's again), added in order
-      uint4 v[Z::kMats][kMostParts - 1];
+      if (j0 + a >= t.rows || !part.mine(a)) continue;
 #pragma unroll
-      for (int r = 0; r < kMostParts - 1; ++r)
+      for (int i = 0; i < Z::kMats; ++i) {
+        // of every block at once (of a missing one the last one's again), added in order
+        uint4 v[kMostParts];
 #pragma unroll
-        for (int i = 0; i < Z::kMats; ++i) v[i][r] = ld_cluster_128(from[r] + i * kMat + a / 4 * kQuad);
+        for (int r = 0; r < kMostParts; ++r) v[r] = ld_cluster_128(from[r] + i * kMat + a / 4 * kQuad);
+        float* const o = &acc[i][a / kUnit][a % kUnit];
+        float sum[4] = {};
 #pragma unroll
-      for (int r = 0; r < kMostParts - 1; ++r)
-        if (r < part.parts - 1)
-#pragma unroll
-          for (int i = 0; i < Z::kMats; ++i) {
-            float* o = &acc[i][a / kUnit][a % kUnit];
-            o[0] += __uint_as_float(v[i][r].x);
-            o[1] += __uint_as_float(v[i][r].y);
-            o[2] += __uint_as_float(v[i][r].z);
-            o[3] += __uint_as_float(v[i][r].w);
+        for (int r = 0; r < kMostParts; ++r)
+          if (r < part.parts) {
+            const bool here = r == part.rank;  // in registers, not in shared memory
+            sum[0] += here ? o[0] : __uint_as_float(v[r].x);
+            sum[1] += here ? o[1] : __uint_as_float(v[r].y);
+            sum[2] += here ? o[2] : __uint_as_float(v[r].z);
+            sum[3] += here ? o[3] : __uint_as_float(v[r].w);
           }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = sum[k];
+      }
     }
   }
   if constexpr (kU == 0) {
     return true;
   } else if constexpr (kForm == kGated) {
-    return gated_store<kU>(p, s, t, x, acc[0], acc[1], j0, q, lane, wait_ns);
+    return gated_store<kU>(p, part, s, t, x, acc[0], acc[1], j0, q, lane, wait_ns);
   } else {
     const int32_t c = t.c0 + 32 * q + (lane & ~1);
     store_bf16<kU>(acc[0], p.out + static_cast<int64_t>(t.m0 + j0 + (lane & 1)) * p.outer + c, p.outer,
-                   t.rows - j0, c < p.outer, lane);
+                   t.rows - j0, c < p.outer, part, lane);
     return true;
   }
 }
@@ -615,13 +621,14 @@ gq_status setup_form() {
 // Blocks per tile, at most a portable cluster's: as many as are resident at once
 // if every group has rows, each with an entry of the factor ring at least.  In
 // us, one block / as many as this gives:
-//   one token to 8 of 128, gated, 2 x 768 x 2048     10.9 / 10.3
-//   to 2 of 8, 2 x 2048 x 4096                       16.4 / 10.9
-//   to one of 16, 2 x 1024 x 8192                    27.8 / 9.2
-//   to 2 of 8, 2 x 768 x 2048                        10.1 / 7.0
+//   one token to 8 of 128, gated, 2 x 768 x 2048     10.9 / 10.2
+//   to 2 of 8, 2 x 2048 x 4096                       16.4 / 11.0
+//   to one of 16, 2 x 1024 x 8192                    27.8 / 9.0
+//   to 2 of 8, 2 x 768 x 2048                        10.1 / 6.9
 //   to 2 of 8, grad_input, 2 x 4096 x 2048           20.9 / 9.7
-//   16 rows of one expert, gated, 2 x 2048 x 4096    18.3 / 12.8
-// (With two entries each at least the fourth takes 8.0, with four each 10.1.)
+//   16 rows of one expert, gated, 2 x 2048 x 4096    18.3 / 11.1
+// (With two entries each at least the fourth takes 8.0, with four each 10.1;
+// with the sums added and written by the first block alone the last takes 12.9.)
 int32_t parts_of(const DeviceInfo& info, const Params& p, int64_t most) {
   const int32_t entries = (p.kbs + kScaleKb - 1) / kScaleKb;
   int32_t n = 0;
@@ -639,8 +646,8 @@ gq_status launch_form(const DeviceInfo& info, Params& p, const void* qa, const v
   st = encode_weights(&wmap, p, qb, N, K);
   if (st != GQ_OK) return st;
   p.tiles_c = (p.outer + kCols - 1) / kCols;
-  const int64_t most =
-      (static_cast<int64_t>(p.M) / kTok + (p.E < p.M ? p.E : p.M)) * p.tiles_c;  // any offsets
+  const int64_t filled = p.E < p.M ? p.E : p.M;  // groups that have rows, at most
+  const int64_t most = (p.M + filled * (kTok - 1)) / kTok * p.tiles_c;  // tiles of any offsets
   if (most > INT32_MAX)
     return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: %lld tiles", static_cast<long long>(most));
   if constexpr (may_split(kForm)) {
