@@ -42,7 +42,8 @@
 // 4096, everything written: 525 us, in a long run 545 to 570; the plain product
 // with the same matrices 467 and 490 to 530.
 //
-// One persistent block per SM; its warps:
+// One persistent block per SM -- or, where the gated forms have few tiles, a cluster
+// per tile (see Split and kSplitKbs) -- whose warps are:
 //   0-7   epilogue: lane quarter w % 4 (32 rows), column half w / 4 (gated: 64
 //         columns of both projections);
 //   8     TMA loads (one lane);
@@ -73,8 +74,8 @@ constexpr int kEpiRegs = 232;     // registers per thread after the split:
 constexpr int kOtherRegs = 40;    // what the block was launched with, no more
 constexpr int kChunk = 32;        // columns per step of the epilogue
 constexpr int kChunks = kCols / 2 / kChunk;
-constexpr int kScaleKb = 4;       // 128-blocks per entry of the factor ring
 constexpr int kScaleRing = 2;
+constexpr int kMostParts = 4;     // blocks that share a tile's contraction, at most
 static_assert(kTmemCols == 512 && kChunks == 4, "two accumulators fill the TMEM");
 
 // Blocks that share a tile: one, with all of its output columns' weights, or
@@ -232,7 +233,7 @@ __device__ __forceinline__ void store_bf16(const float (&v)[kChunk], uint16_t* o
   store_parts(x, reinterpret_cast<uint8_t*>(out), pitch * 2, rows, c_ok, lane);
 }
 
-template <int kForm, int kBlocks>
+template <int kForm, int kBlocks, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ CUtensorMap amap,
                    const __grid_constant__ CUtensorMap amap32,
@@ -248,8 +249,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem<kBlocks>& s = *reinterpret_cast<Smem<kBlocks>*>(smem_raw + (-smem_addr(smem_raw) & 1023u));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
+  static_assert(kBlocks == 1 || !kSplit, "a cluster is a pair or shares a contraction");
   const int32_t rank = kBlocks == 2 ? static_cast<int32_t>(cluster_rank()) : 0;
-  const int32_t groups = gridDim.x / kBlocks, group = blockIdx.x / kBlocks;
+  const Split part = split_of<kSplit>(p);
+  const int32_t sharing = kBlocks * part.parts;
+  const int32_t groups = gridDim.x / sharing, group = blockIdx.x / sharing;
   const uint64_t wait_ns = 4 * p.timeout_ns;
 
   if (warp == kEpiWarps && lane == 0) {
@@ -283,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s.tmem_base;
   const int32_t tiles = s.tiles.first[p.E] * p.tiles_c;  // below 2^31: the host checks
 
+  bool joined = false;  // split: this warp has met the cluster's barrier
   if (warp >= kEpiWarps) {
     setmaxnreg_dec<kOtherRegs>();
     if (warp == kEpiWarps) {
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int32_t rows32 = boxes;  // of all blocks
         if (kBlocks == 2) rows32 = boxes_of(t.rows) + boxes_of(t.rows - kRows);
         const uint32_t bytes = 2 * kWHalf + static_cast<uint32_t>(rows32) * (kBoxRows * kBlock);
-        for (int32_t kb = 0; kb < p.kbs; ++kb) {
+        for (int32_t kb = part.kb0; kb < part.kb1; ++kb) {
           const int32_t k = column_of<kForm>(p, kb), half = half_of<kForm>(p, kb);
           ok = mbar_wait_warp(done + st * 8, (use & 1) ^ 1u, wait_ns, p.err);
           if (!ok) break;
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true, issued = false;
         for (int32_t i = group; ok && i < tiles; i += groups) {
           uint32_t idesc = 0;
-          for (int32_t kb = 0; kb < p.kbs; ++kb) {
+          for (int32_t kb = part.kb0; kb < part.kb1; ++kb) {
             const int32_t left = p.inner - column_of<kForm>(p, kb);
             // rows: K-major; weights: K-major rows of 128 bytes, or MN-major
             // (32 contraction rows = 4 KB, one block's halves of the columns kWHalf apart)
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_addr(full + st * 8, st_use & 1, wait_ns, p.err) &&
                  mbar_wait_addr(acc_empty + b * 8, (use & 1) ^ 1u, wait_ns, p.err);
             if (!ok) break;
-            if (kb == 0)  // D fp32, e4m3 x e4m3, B MN-major if transposed, N, M
+            if (kb == part.kb0)  // D fp32, e4m3 x e4m3, B MN-major if transposed, N, M
               idesc = (1u << 4) | (kT ? 1u << 16 : 0u) | (static_cast<uint32_t>(kTileRows >> 4) << 24) |
                       ((static_cast<uint32_t>(s.cols[st]) >> 3) << 17);
             tc_fence_after();
@@ -403,10 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // would queue up at a single L2 line).
       const int32_t first = (warp - kEpiWarps - 2) * 64 + lane;
       float v[2][kScaleKb] = {}, ws[2][kScaleKb];
-      int32_t i = group, kb = 0;
+      int32_t i = group, kb = part.kb0;
       Tile t = {};
       auto load = [&]() {  // the entry (tile i, 128-blocks kb ..)
-        if (kb == 0) {
+        if (kb == part.kb0) {
           t = tile_of(p, s.tiles, i, kTileRows, kTileCols, lane);
           t.m0 += rank * kRows;
           t.rows -= rank * kRows;
@@ -461,8 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++use;
         }
         kb += kScaleKb;
-        if (kb >= p.kbs) {
-          kb = 0;
+        if (kb >= part.kb1) {
+          kb = part.kb0;
           i += groups;
         }
         if (i < tiles) load();
@@ -525,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait32(h0);
       }
 #pragma unroll 1
-      for (int32_t left = p.kbs; left > 0; --left) {
+      for (int32_t left = part.kb1 - part.kb0; left > 0; --left) {
         const uint32_t tacc = tmem0 + b * kCols;
         if (mine) {
           tmem_ld_32x32b_x32(tacc + col(1), h1);
@@ -584,18 +589,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       if (!mine) continue;
-      const int part = lane & 3;
+      if constexpr (kSplit) {
+        // the stages are free: all MMAs of the block are complete
+        const uint32_t own = smem_addr(s.stage) + (warp * (kChunks * kChunk / 4) * 32 + lane) * 16;
+        if (!part.mine(q)) {
+#pragma unroll
+          for (int k = 0; k < kChunks * kChunk; k += 4) {
+            const float* v = &acc[k / kChunk][k % kChunk];
+            sts128(own + k / 4 * 512, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                                 __float_as_uint(v[2]), __float_as_uint(v[3])));
+          }
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        joined = true;
+        if (!part.mine(q)) continue;
+        // its own sums first, then the other blocks' in their order; eight words
+        // are under way at a time
+#pragma unroll 1
+        for (int32_t j = 1; j < part.parts; ++j) {
+          const uint32_t from = map_cluster(own, (part.rank + j) & (part.parts - 1));
+#pragma unroll
+          for (int k0 = 0; k0 < kChunks * kChunk; k0 += kChunk) {
+            uint4 v[kChunk / 4];
+#pragma unroll
+            for (int k = 0; k < kChunk / 4; ++k) v[k] = ld_cluster_128(from + (k0 / 4 + k) * 512);
+#pragma unroll
+            for (int k = 0; k < kChunk / 4; ++k) {
+              float* const o = &acc[k0 / kChunk][4 * k];
+              o[0] += __uint_as_float(v[k].x);
+              o[1] += __uint_as_float(v[k].y);
+              o[2] += __uint_as_float(v[k].z);
+              o[3] += __uint_as_float(v[k].w);
+            }
+          }
+        }
+      }
+      const int col8 = lane & 3;
       const int64_t row = row0 + (lane & ~3);
       if constexpr (kForm != kGated) {
-        uint16_t* const orow = p.out + row * p.outer + c + part * 8;
+        uint16_t* const orow = p.out + row * p.outer + c + col8 * 8;
 #pragma unroll
         for (int ch = 0; ch < kChunks; ++ch)
           store_bf16(acc[ch], orow + ch * kChunk, p.outer, rows,
-                     c + ch * kChunk + part * 8 < p.outer, lane);  // outer % 16 == 0
+                     c + ch * kChunk + col8 * 8 < p.outer, lane);  // outer % 16 == 0
       } else {
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
-          const int32_t at = c + ch * kChunk + part * 8;
+          const int32_t at = c + ch * kChunk + col8 * 8;
           const bool in = at < p.outer;  // outer % 16 == 0
           if (p.pre != nullptr) {  // the projections, as they are
             uint16_t* const prow = p.pre + row * 2 * p.outer + at;
@@ -633,12 +675,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* v = &acc[w >> 1][(w & 1) * 16 + 4 * j];
             x[w][j] = quant4f(make_float4(v[0], v[1], v[2], v[3]), sc);
           }
-        store_parts(x, p.q + row * p.outer + c + part * 16, p.outer, rows, c + part * 16 < p.outer, lane);
+        store_parts(x, p.q + row * p.outer + c + col8 * 16, p.outer, rows, c + col8 * 16 < p.outer, lane);
         if (hc == 0 && lane < rows)
           p.scales[static_cast<int64_t>(row0 + lane) * ((p.outer + kBlock - 1) / kBlock) + c / kBlock] = sc;
       }
     }
     tc_fence_before();
+  }
+  if (kSplit) {
+    // Every thread meets the cluster's barrier twice: with the sums written, and
+    // with them read, before a block that holds some may leave.
+    __syncwarp();
+    if (!joined) {
+      cluster_arrive();
+      cluster_wait();
+    }
+    cluster_arrive();
+    cluster_wait();
   }
 
   __syncthreads();
@@ -675,13 +728,21 @@ constexpr int kFewRows = 48, kFewRowsGated = 16;
 constexpr int kPairRows = 96;
 constexpr int kPairTiles = 3;  // per SM
 
+// Blocks share a tile of the gated forms where there are few tiles and more than
+// this many 128-blocks: joining the sums takes 4 us, a 128-block 0.45.  In us, one
+// block / as many as parts_of gives, 128-blocks in brackets: 128 rows of one
+// expert, 2 x 2048 x 4096, gated 17.1/12.6 (32), its grad_input 16.6/12.0 (32); 100 of
+// one, 2 x 768 x 7168, 25.6/14.9 (56) and 8.6/10.3 (12); 256 of four, 2 x 1024 x 4096,
+// 17.6/15.5 (32); 128 of two, 2 x 1408 x 2048, 10.7/11.0 (16) and 12.2/11.1 (22).
+constexpr int kSplitKbs = 20;
+
 }  // namespace
 
 namespace {
 
-template <int kForm, int kBlocks>
+template <int kForm, int kBlocks, bool kSplit>
 gq_status setup_kernel() {
-  const auto kernel = product_kernel<kForm, kBlocks>;
+  const auto kernel = product_kernel<kForm, kBlocks, kSplit>;
   gq_status st = check_cuda(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(smem_bytes<kBlocks>())),
                             "grouped_mm: shared memory size");
@@ -697,8 +758,11 @@ gq_status setup_kernel() {
 
 template <int kForm>
 gq_status setup_form() {
-  const gq_status st = setup_kernel<kForm, 1>();
-  return st != GQ_OK ? st : setup_kernel<kForm, 2>();
+  gq_status st = setup_kernel<kForm, 1, false>();
+  if (st == GQ_OK) st = setup_kernel<kForm, 2, false>();
+  if constexpr (may_split(kForm))
+    if (st == GQ_OK) st = setup_kernel<kForm, 1, true>();
+  return st;
 }
 
 }  // namespace
@@ -719,7 +783,7 @@ gq_status setup(DeviceInfo& info) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   const gq_status st = check_cuda(
-      cudaOccupancyMaxActiveClusters(&info.mm_pairs, product_kernel<kForward, 2>, &cfg),
+      cudaOccupancyMaxActiveClusters(&info.mm_pairs, product_kernel<kForward, 2, false>, &cfg),
       "grouped_mm: resident block pairs");
   if (st != GQ_OK) return st;
   if (info.mm_pairs < 1) info.mm_pairs = 1;
@@ -765,8 +829,8 @@ gq_status launch_many(const DeviceInfo& info, Params& p, const void* qa, const v
                       int32_t K, cudaStream_t stream) {
   constexpr int kTileCols = kForm == kGated ? kCols / 2 : kCols;
   p.tiles_c = (p.outer + kTileCols - 1) / kTileCols;
-  const int64_t most =
-      (static_cast<int64_t>(p.M) / (kBlocks * kRows) + (p.E < p.M ? p.E : p.M)) * p.tiles_c;
+  const int64_t filled = p.E < p.M ? p.E : p.M;  // groups that have rows, at most
+  const int64_t most = (p.M + filled * (kBlocks * kRows - 1)) / (kBlocks * kRows) * p.tiles_c;
   if (most > INT32_MAX)  // tiles of any offsets
     return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: %lld tiles", static_cast<long long>(most));
   CUtensorMap amap, amap32, wmap;
@@ -777,9 +841,16 @@ gq_status launch_many(const DeviceInfo& info, Params& p, const void* qa, const v
   }
   st = encode_weights(&wmap, p, qb, N, K);
   if (st != GQ_OK) return st;
+  if constexpr (kBlocks == 1 && may_split(kForm)) {
+    const int32_t parts = p.kbs > kSplitKbs ? parts_of(info, p, most, kMostParts) : 1;
+    if (parts > 1)
+      return launch_chained("grouped_mm: launch", product_kernel<kForm, 1, true>,
+                            dim3(static_cast<unsigned>(most * parts)), kThreads, smem_bytes<1>(),
+                            stream, parts, amap, amap32, wmap, p);
+  }
   const int resident = kBlocks == 2 ? info.mm_pairs : info.sm_count;
   const unsigned grid = kBlocks * static_cast<unsigned>(most < resident ? most : resident);
-  return launch_chained("grouped_mm: launch", product_kernel<kForm, kBlocks>, dim3(grid), kThreads,
+  return launch_chained("grouped_mm: launch", product_kernel<kForm, kBlocks, false>, dim3(grid), kThreads,
                         smem_bytes<kBlocks>(), stream, kBlocks, amap, amap32, wmap, p);
 }
 

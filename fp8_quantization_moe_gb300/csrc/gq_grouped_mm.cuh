@@ -14,6 +14,7 @@ namespace gmm {
 
 constexpr int kBlock = 128;  // contraction columns per scale, and per stage
 constexpr int kSubK = 32;    // contraction columns per MMA (kind::f8f6f4)
+constexpr int kScaleKb = 4;  // 128-blocks per entry of the kernels' factor rings
 
 // The products, W[g] being a group's matrix (N, K) or its two, W0 and W1.
 enum Form {
@@ -114,6 +115,30 @@ __device__ __forceinline__ int32_t column_of(const Params& p, int32_t kb) {
   return (kb - (half_of<kForm>(p, kb) ? p.kb_half : 0)) * kBlock;
 }
 
+// Where the tiles are too few for the SMs, `parts` blocks, a cluster, share one:
+// each forms the sum of a run of the contraction's 128-blocks and leaves it in its
+// shared memory; then each adds and writes a part of the tile, the sums in the
+// blocks' order.  (One tile a cluster: the launch sees to it.)
+struct Split {
+  int32_t rank, parts;
+  int32_t kb0, kb1;  // this block's 128-blocks, from a whole entry of the factor ring on
+  // whether part i of a tile is this block's to write
+  __device__ __forceinline__ bool mine(int32_t i) const { return (i & (parts - 1)) == rank; }
+};
+
+template <bool kSplit>
+__device__ __forceinline__ Split split_of(const Params& p) {
+  Split v = {0, 1, 0, p.kbs};
+  if (kSplit) {
+    v.rank = static_cast<int32_t>(cluster_rank());
+    v.parts = static_cast<int32_t>(cluster_size());
+    const int32_t entries = (p.kbs + kScaleKb - 1) / kScaleKb;
+    v.kb0 = entries * v.rank / v.parts * kScaleKb;
+    v.kb1 = min(p.kbs, entries * (v.rank + 1) / v.parts * kScaleKb);
+  }
+  return v;
+}
+
 struct Tile {
   int32_t g, c0, m0, rows;  // group, first column, first row, rows of the group from there
 };
@@ -135,6 +160,19 @@ __device__ __forceinline__ Tile tile_of(const Params& p, const TileTable& s, int
   t.m0 = (g > 0 ? s.ends[g - 1] : 0) + (r - c * row_tiles) * rows;
   t.rows = s.ends[g] - t.m0;
   return t;
+}
+
+// The gated forms share tiles; the plain products add their 128-blocks in one
+// order, whatever the sizes, as they always have.
+constexpr bool may_split(int form) { return form == kGated || form == kGatedGrad; }
+
+// Blocks per tile, up to `at_most`: as many as are resident at once if there are
+// `tiles` of them, each with an entry of the factor ring at least.
+inline int32_t parts_of(const DeviceInfo& info, const Params& p, int64_t tiles, int32_t at_most) {
+  const int32_t entries = (p.kbs + kScaleKb - 1) / kScaleKb;
+  int32_t n = 0;
+  while ((2 << n) <= at_most && tiles <= info.mm_split[n + 1] && (2 << n) <= entries) ++n;
+  return 1 << n;
 }
 
 // The product of many rows per group (gq_grouped_mm.cu) and of few

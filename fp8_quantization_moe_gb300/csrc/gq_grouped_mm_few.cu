@@ -35,7 +35,6 @@ namespace {
 constexpr int kCols = 128;     // output columns of a tile (the MMA's M)
 constexpr int kUnit = 16;      // rows of a tile come in units
 constexpr int kWBytes = kCols * kBlock;   // 16 KB
-constexpr int kScaleKb = 4;    // 128-blocks per entry of the factor ring
 constexpr int kScaleRing = 4;
 constexpr int kMostParts = 8;  // blocks that share a tile, at most
 constexpr int kEpiWarps = 8;
@@ -87,32 +86,6 @@ __device__ __forceinline__ int32_t units_of(const Tile& t) {
   return (min(t.rows, Sizes<kForm>::kTok) + kUnit - 1) / kUnit;
 }
 
-// Where the tiles are too few for the SMs, `parts` blocks, a cluster, share one:
-// each forms the sum of a run of the contraction's 128-blocks and leaves it in its
-// shared memory; then each adds and writes every parts-th four rows, the sums in
-// the blocks' order.  (One tile a cluster: the launch sees to it.)
-struct Split {
-  int32_t rank, parts;
-  int32_t kb0, kb1;  // this block's 128-blocks, from a whole entry of the factor ring on
-  // whether the four rows from `row` of a tile on are this block's to write
-  __device__ __forceinline__ bool mine(int32_t row) const {
-    return ((row >> 2) & (parts - 1)) == rank;
-  }
-};
-
-template <bool kSplit>
-__device__ __forceinline__ Split split_of(const Params& p) {
-  Split v = {0, 1, 0, p.kbs};
-  if (kSplit) {
-    v.rank = static_cast<int32_t>(cluster_rank());
-    v.parts = static_cast<int32_t>(cluster_size());
-    const int32_t entries = (p.kbs + kScaleKb - 1) / kScaleKb;
-    v.kb0 = entries * v.rank / v.parts * kScaleKb;
-    v.kb1 = min(p.kbs, entries * (v.rank + 1) / v.parts * kScaleKb);
-  }
-  return v;
-}
-
 // Positions in the rings, common to a tile's steps.
 struct Rings {
   uint32_t b = 0;              // accumulator
@@ -135,7 +108,7 @@ __device__ __forceinline__ void store_bf16(const float (&v)[kN][kUnit], uint16_t
   for (int u = 0; u < kN; ++u)
 #pragma unroll
     for (int j = 0; j < kUnit; j += 2) {
-      if (u * kUnit + j >= rows || !part.mine(u * kUnit + j)) continue;  // rows may end early
+      if (u * kUnit + j >= rows || !part.mine((u * kUnit + j) / 4)) continue;  // rows may end early
       const float give = odd ? v[u][j] : v[u][j + 1];
       const float got = __shfl_xor_sync(0xffffffffu, give, 1);
       const uint32_t w = odd ? bf16x2_of(got, v[u][j + 1]) : bf16x2_of(v[u][j], got);
@@ -172,7 +145,7 @@ __device__ __forceinline__ bool gated_store(const Params& p, const Split& part, 
     float m = 0.0f;  // of row `lane & 15`
 #pragma unroll
     for (int j = 0; j < kUnit; ++j) {
-      if (a * kUnit + j >= rows || !part.mine(a * kUnit + j)) continue;
+      if (a * kUnit + j >= rows || !part.mine((a * kUnit + j) / 4)) continue;
       float v = c < p.outer ? fmaxf(fabsf(x[a][j]), 0.0f) : 0.0f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -189,7 +162,7 @@ __device__ __forceinline__ bool gated_store(const Params& p, const Split& part, 
   for (int a = 0; a < kN; ++a)
 #pragma unroll
     for (int j = 0; j < kUnit; j += 4) {
-      if (a * kUnit + j >= rows || !part.mine(a * kUnit + j)) continue;
+      if (a * kUnit + j >= rows || !part.mine((a * kUnit + j) / 4)) continue;
       // four rows: a lane's bytes of its column, then by two exchanges of bytes the
       // bytes of four columns of one row, lane & 3
       uint32_t w = 0;
@@ -289,7 +262,7 @@ __device__ __forceinline__ bool tile_body(const Params& p, const Split& part, Sm
     constexpr uint32_t kQuad = kCols * 16, kMat = Z::kTok / 4 * kQuad;
 #pragma unroll
     for (int a = 0; a < kU * kUnit; a += 4)
-      if (j0 + a < t.rows && !part.mine(a))
+      if (j0 + a < t.rows && !part.mine(a / 4))
 #pragma unroll
         for (int i = 0; i < Z::kMats; ++i) {
           const float* v = &acc[i][a / kUnit][a % kUnit];
@@ -306,7 +279,7 @@ __device__ __forceinline__ bool tile_body(const Params& p, const Split& part, Sm
     for (int r = 0; r < kMostParts; ++r) from[r] = map_cluster(own, min(r, part.parts - 1));
 #pragma unroll
     for (int a = 0; a < kU * kUnit; a += 4) {
-      if (j0 + a >= t.rows || !part.mine(a)) continue;
+      if (j0 + a >= t.rows || !part.mine(a / 4)) continue;
 #pragma unroll
       for (int i = 0; i < Z::kMats; ++i) {
         // of every block at once (of a missing one the last one's again), added in order
@@ -598,10 +571,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-// The gated forms share tiles; the plain products add their 128-blocks in one
-// order, whatever the sizes, as they always have.
-constexpr bool may_split(int form) { return form == kGated || form == kGatedGrad; }
-
 template <int kForm, bool kSplit>
 gq_status setup_kernel() {
   return check_cuda(cudaFuncSetAttribute(few_kernel<kForm, kSplit>,
@@ -618,9 +587,7 @@ gq_status setup_form() {
   return st;
 }
 
-// Blocks per tile, at most a portable cluster's: as many as are resident at once
-// if every group has rows, each with an entry of the factor ring at least.  In
-// us, one block / as many as this gives:
+// What sharing tiles gives, in us, one block / as many as parts_of gives:
 //   one token to 8 of 128, gated, 2 x 768 x 2048     10.9 / 10.2
 //   to 2 of 8, 2 x 2048 x 4096                       16.4 / 11.0
 //   to one of 16, 2 x 1024 x 8192                    27.8 / 9.0
@@ -629,13 +596,6 @@ gq_status setup_form() {
 //   16 rows of one expert, gated, 2 x 2048 x 4096    18.3 / 11.1
 // (With two entries each at least the fourth takes 8.0, with four each 10.1;
 // with the sums added and written by the first block alone the last takes 12.9.)
-int32_t parts_of(const DeviceInfo& info, const Params& p, int64_t most) {
-  const int32_t entries = (p.kbs + kScaleKb - 1) / kScaleKb;
-  int32_t n = 0;
-  while (n < 3 && most <= info.mm_split[n + 1] && (2 << n) <= entries) ++n;
-  return 1 << n;
-}
-
 template <int kForm>
 gq_status launch_form(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,
                       int32_t K, cudaStream_t stream) {
@@ -651,7 +611,7 @@ gq_status launch_form(const DeviceInfo& info, Params& p, const void* qa, const v
   if (most > INT32_MAX)
     return fail(GQ_ERR_UNSUPPORTED, "grouped_mm: %lld tiles", static_cast<long long>(most));
   if constexpr (may_split(kForm)) {
-    const int32_t parts = parts_of(info, p, most);
+    const int32_t parts = parts_of(info, p, most, kMostParts);
     if (parts > 1)
       return launch_chained("grouped_mm: launch", few_kernel<kForm, true>,
                             dim3(static_cast<unsigned>(most * parts)), kThreads,

@@ -449,9 +449,9 @@ gq_status gq_grouped_mm(const void* qa, const float* sa, int64_t M, const void* 
  *     x[m][n] = sum over k of A[m][k] * W[g][0][n][k]
  *     u[m][n] = sum over k of A[m][k] * W[g][1][n][k]
  *     h[m][n] = act(x[m][n]) * u[m][n]
- * x, u and h are formed in fp32 as in gq_grouped_mm (where there are few rows and
- * few columns, runs of 128-blocks are summed apart and then added, in one order
- * for a call's sizes); act(x) = x * sigma(z), sigma
+ * x, u and h are formed in fp32 as in gq_grouped_mm (where there are few
+ * tiles, runs of 128-blocks are summed apart and then added, in an order that the
+ * call's sizes give); act(x) = x * sigma(z), sigma
  * the logistic function, with
  *     GQ_ACT_SILU   z = x
  *     GQ_ACT_GELU   z = 2 sqrt(2 / pi) (x + 0.044715 x^3), the tanh form of gelu

@@ -357,6 +357,11 @@ SPLIT = [
     (40, 4096, 16, [9, 40]),
     (30, 2000, 1040, [10, 28]),       # rows behind the last end
     (16, 6160, 400, [16, 3, 16, 20]),
+    # more rows: the kernel for many, two and four blocks
+    (128, 4096, 1040, [128]),
+    (300, 2704, 272, [1, 300]),
+    (700, 2800, 528, [257, 300, 300, 650]),
+    (129, 7184, 48, [129]),
 ]
 
 
@@ -573,7 +578,8 @@ def test_streams_and_graphs(gq, M, N, K, offs):
 
 
 @pytest.mark.parametrize("M,N,K,offs", [(12, 5008, 656, [4, 12]), (600, 48, 400, [300, 600]),
-                                         (6200, 2576, 144, [3000, 6200]), (5, 4112, 4112, [5])])
+                                         (6200, 2576, 144, [3000, 6200]), (5, 4112, 4112, [5]),
+                                         (129, 4112, 4112, [129])])
 def test_timeouts_are_reported_not_hung(gq, M, N, K, offs):
     """A withheld accumulator release: every role leaves its loop after the
     (shortened) limit, the call reports GQ_ERR_TIMEOUT, the next call is fine.
