@@ -97,23 +97,28 @@ struct Rings {
 };
 
 // Rows of 128-columns' values in TMEM lanes (a lane is a column c) to bf16 rows:
-// two rows at a time, neighbouring lanes swap one value each, so that even lanes
-// hold two columns of the first row and odd lanes of the second; a store covers
-// 64 bytes of both.  `out` points at column (c & ~1) of row (lane & 1).
+// four rows at a time; two exchanges among four neighbouring lanes leave each with
+// four columns of one of the rows, so that a store covers 64 bytes of all four.
+// `out` points at column (c & ~3) of row (lane & 3).
 template <int kN>
 __device__ __forceinline__ void store_bf16(const float (&v)[kN][kUnit], uint16_t* out, int64_t pitch,
                                            int32_t rows, bool c_ok, const Split& part, int lane) {
-  const int32_t odd = lane & 1;
+  const bool high = lane & 2, odd = lane & 1;
 #pragma unroll
   for (int u = 0; u < kN; ++u)
 #pragma unroll
-    for (int j = 0; j < kUnit; j += 2) {
+    for (int j = 0; j < kUnit; j += 4) {
       if (u * kUnit + j >= rows || !part.mine((u * kUnit + j) / 4)) continue;  // rows may end early
-      const float give = odd ? v[u][j] : v[u][j + 1];
-      const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-      const uint32_t w = odd ? bf16x2_of(got, v[u][j + 1]) : bf16x2_of(v[u][j], got);
-      if (u * kUnit + j + odd < rows && c_ok)
-        *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(u * kUnit + j) * pitch) = w;
+      const uint32_t w0 = bf16x2_of(v[u][j], v[u][j + 1]), w1 = bf16x2_of(v[u][j + 2], v[u][j + 3]);
+      // two of the rows, of columns c and c ^ 2, then one of columns c and c ^ 2, c ^ 1 and c ^ 3
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w0 : w1, 2);
+      const uint32_t lo = high ? got : w0, hi = high ? w1 : got;  // columns 0 or 1, and 2 or 3
+      const uint32_t keep = __byte_perm(lo, hi, odd ? 0x7632 : 0x5410);
+      const uint32_t back = __shfl_xor_sync(0xffffffffu, __byte_perm(lo, hi, odd ? 0x5410 : 0x7632), 1);
+      const uint32_t even = odd ? back : keep, other = odd ? keep : back;  // columns 0 and 2, 1 and 3
+      if (u * kUnit + j + (lane & 3) < rows && c_ok)
+        *reinterpret_cast<uint2*>(out + static_cast<int64_t>(u * kUnit + j) * pitch) =
+            make_uint2(__byte_perm(even, other, 0x5410), __byte_perm(even, other, 0x7632));
     }
 }
 
@@ -124,17 +129,17 @@ __device__ __forceinline__ bool gated_store(const Params& p, const Split& part, 
                                             float (&x)[kN][kUnit], float (&u)[kN][kUnit], int32_t j0,
                                             int q, int lane, uint64_t wait_ns) {
   const int32_t rows = t.rows - j0;
-  const int32_t c = t.c0 + 32 * q + lane, pair = c & ~1, odd = lane & 1;
-  const bool c_ok = pair < p.outer;  // outer % 16 == 0
+  const int32_t c = t.c0 + 32 * q + lane, four = c & ~3, of_four = lane & 3;
+  const bool c_ok = four < p.outer;  // outer % 16 == 0
   const int64_t row = t.m0 + j0, n = p.outer;
   if (p.pre != nullptr) {
-    uint16_t* const to = p.pre + (row + odd) * 2 * n + pair;
+    uint16_t* const to = p.pre + (row + of_four) * 2 * n + four;
     store_bf16(x, to, 2 * n, rows, c_ok, part, lane);
     store_bf16(u, to + n, 2 * n, rows, c_ok, part, lane);
   }
 #pragma unroll
   for (int a = 0; a < kN; ++a) gated::gate(p.act, x[a], u[a]);
-  if (p.out != nullptr) store_bf16(x, p.out + (row + odd) * n + pair, n, rows, c_ok, part, lane);
+  if (p.out != nullptr) store_bf16(x, p.out + (row + of_four) * n + four, n, rows, c_ok, part, lane);
   if (p.q == nullptr) return true;
   // the maximum of a row over this warp's 32 columns, then over the four warps
   // that hold its 128 (a NaN does not count; columns past the last hold anything)
@@ -142,16 +147,18 @@ __device__ __forceinline__ bool gated_store(const Params& p, const Split& part, 
   float(*const most)[4] = s.most[r.shares & 1][g];
 #pragma unroll
   for (int a = 0; a < kN; ++a) {
-    float m = 0.0f;  // of row `lane & 15`
+    uint32_t m = 0;  // of row `lane & 15`, bits: of values that are not negative in their order
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) {
+    for (int j = 0; j < kUnit; j += 4) {
       if (a * kUnit + j >= rows || !part.mine((a * kUnit + j) / 4)) continue;
-      float v = c < p.outer ? fmaxf(fabsf(x[a][j]), 0.0f) : 0.0f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-      if ((lane & 15) == j) m = v;
+      for (int k = 0; k < 4; ++k) {
+        const float v = c < p.outer ? fmaxf(fabsf(x[a][j + k]), 0.0f) : 0.0f;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v));
+        if ((lane & 15) == j + k) m = top;
+      }
     }
-    if (lane < kUnit) sts32(smem_addr(&most[a * kUnit + lane][q]), m);
+    if (lane < kUnit) sts32(smem_addr(&most[a * kUnit + lane][q]), __uint_as_float(m));
   }
   __syncwarp();
   if (lane == 0) mbar_arrive(&s.pair[g]);
@@ -159,7 +166,14 @@ __device__ __forceinline__ bool gated_store(const Params& p, const Split& part, 
   ++r.shares;
   const int32_t nb = (p.outer + kBlock - 1) / kBlock;
 #pragma unroll
-  for (int a = 0; a < kN; ++a)
+  for (int a = 0; a < kN; ++a) {
+    if (a * kUnit >= rows) continue;
+    // a row's scale is formed by one lane, which holds it for the others
+    const int32_t own = lane & (kUnit - 1);
+    const uint4 m = lds128_ordered(smem_addr(most[a * kUnit + own]));
+    const float sc = scale_from_amax_bits(max(max(m.x, m.y), max(m.z, m.w)), p.pow2);
+    if (q == 0 && lane < kUnit && a * kUnit + own < rows && part.mine((a * kUnit + own) / 4))
+      p.scales[(row + a * kUnit + own) * nb + t.c0 / kBlock] = sc;
 #pragma unroll
     for (int j = 0; j < kUnit; j += 4) {
       if (a * kUnit + j >= rows || !part.mine((a * kUnit + j) / 4)) continue;
@@ -168,23 +182,18 @@ __device__ __forceinline__ bool gated_store(const Params& p, const Split& part, 
       uint32_t w = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint4 m = lds128_ordered(smem_addr(most[a * kUnit + j + k]));
-        const float top = fmaxf(fmaxf(__uint_as_float(m.x), __uint_as_float(m.y)),
-                                fmaxf(__uint_as_float(m.z), __uint_as_float(m.w)));
-        const float sc = scale_from_amax_bits(__float_as_uint(top), p.pow2);
         const float v = x[a][j + k];
-        w |= (quant4f(make_float4(v, v, v, v), sc) & 0xFFu) << (8 * k);
-        if (q == 0 && lane == 0 && a * kUnit + j + k < rows)
-          p.scales[(row + a * kUnit + j + k) * nb + t.c0 / kBlock] = sc;
+        const float of = __shfl_sync(0xffffffffu, sc, j + k);
+        w |= (quant4f(make_float4(v, v, v, v), of) & 0xFFu) << (8 * k);
       }
       uint32_t o = __shfl_xor_sync(0xffffffffu, w, 1);
       w = lane & 1 ? __byte_perm(w, o, 0x3715) : __byte_perm(w, o, 0x6240);
       o = __shfl_xor_sync(0xffffffffu, w, 2);
       w = lane & 2 ? __byte_perm(w, o, 0x3276) : __byte_perm(w, o, 0x5410);
-      const int32_t at = a * kUnit + j + (lane & 3);
-      if (at < rows && (c & ~3) < p.outer)
-        *reinterpret_cast<uint32_t*>(p.q + (row + at) * n + (c & ~3)) = w;
+      const int32_t at = a * kUnit + j + of_four;
+      if (at < rows && c_ok) *reinterpret_cast<uint32_t*>(p.q + (row + at) * n + four) = w;
     }
+  }
   return true;
 }
 
@@ -307,8 +316,8 @@ __device__ __forceinline__ bool tile_body(const Params& p, const Split& part, Sm
   } else if constexpr (kForm == kGated) {
     return gated_store<kU>(p, part, s, t, x, acc[0], acc[1], j0, q, lane, wait_ns);
   } else {
-    const int32_t c = t.c0 + 32 * q + (lane & ~1);
-    store_bf16<kU>(acc[0], p.out + static_cast<int64_t>(t.m0 + j0 + (lane & 1)) * p.outer + c, p.outer,
+    const int32_t c = t.c0 + 32 * q + (lane & ~3);
+    store_bf16<kU>(acc[0], p.out + static_cast<int64_t>(t.m0 + j0 + (lane & 3)) * p.outer + c, p.outer,
                    t.rows - j0, c < p.outer, part, lane);
     return true;
   }
