@@ -709,10 +709,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   16 of 4096 x 4096           48/49 50/50 52/50 56/52   46/44 47/45 49/46 54/47
 //   8 of 8192 x 2048            25/27 26/27 28/28 33/29   22/31 23/32 25/32 28/33
 //   8 of 2048 x 8192            22/32 23/33 25/34 28/34   25/26 26/26 28/27 33/28
-// The gated form has half as many rows in a tile there: 64 pairs of 1024 x
-// 2048 at 16, 32 and 48 rows 53/50 55/51 63/52, of 1424 x 2064 69/69 80/73 87/76.
+// The gated form has half as many rows in a tile there: fp8 rows, at 16, 24, 32 and 48
+//   64 pairs of 1024 x 2048     48/49 47/49 47/50 52/49
+//   64 of 1424 x 2064           66/69 68/71 70/72 77/78, all outputs 73/73 78/75 85/78 96/86
+//   16 of 2048 x 4096           45/48 47/48 47/49 54/49
+//   8 of 768 x 2048             11/11 13/12 14/12 13/12
+//   one of 2048 x 4096          9.9/11.6 11.6/11.6 12.1/11.6 14.0/11.8
 // The rows are those of the buffer, also behind the last group's end.
-constexpr int kFewRows = 48, kFewRowsGated = 16;
+constexpr int kFewRows = 48, kFewRowsGated = 24;
 
 // Block pairs where rows of an operand begin anywhere in a 128-byte line (their
 // length is no multiple of 64 bytes): nearly each 128 bytes of a box are then two
