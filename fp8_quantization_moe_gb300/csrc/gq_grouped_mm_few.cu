@@ -6,8 +6,9 @@
 // rest the launch, the first loads and the last tile.
 //
 // In the gated form a tile has 128 columns of both projections and up to 64 rows:
-// one token to eight of 64 experts, 2 x 2048 x 4096, 134 MB: 24.6 us, of which the
-// loads take 21.4; 512 rows of 64 experts, 2 x 1424 x 2064: 58.3 us, 6.5 TB/s.
+// one token to eight of 64 experts, 2 x 2048 x 4096, 134 MB: 24.3 us, of which the
+// loads take 21.4; 512 rows of 64 experts, 2 x 1424 x 2064: 58.3 us, 6.5 TB/s (fp8
+// 60).
 //
 // Here the weights are the MMA's M operand (128 output columns) and the rows
 // its N operand, up to 128 of them in steps of 16: an MMA costs as many cycles
@@ -16,7 +17,8 @@
 // an output column and needs every row's factor 1/sa * 1/sb; with few rows
 // those shared loads are cheap.
 //
-// One persistent block per SM; its warps:
+// One persistent block per SM -- or, where the gated forms have few tiles, a cluster
+// per tile (see Split) -- whose warps are:
 //   0-7   epilogue: TMEM lane quarter w % 4 (32 output columns), rows
 //         64 (w / 4) and on;
 //   8     TMA loads (one lane);
@@ -141,8 +143,10 @@ __device__ __forceinline__ bool gated_store(const Params& p, const Split& part, 
   for (int a = 0; a < kN; ++a) gated::gate(p.act, x[a], u[a]);
   if (p.out != nullptr) store_bf16(x, p.out + (row + of_four) * n + four, n, rows, c_ok, part, lane);
   if (p.q == nullptr) return true;
-  // the maximum of a row over this warp's 32 columns, then over the four warps
-  // that hold its 128 (a NaN does not count; columns past the last hold anything)
+  // the maximum of a row over this warp's 32 columns, then over the four warps that
+  // hold its 128 (a NaN does not count; columns past the last hold anything); with
+  // five exchanges a row, and its scale formed by every lane, 1024 rows of 64
+  // experts, 2 x 1024 x 2048, took 58 us, this way 48
   const int g = j0 / Sizes<kGated>::kWarpTok;
   float(*const most)[4] = s.most[r.shares & 1][g];
 #pragma unroll
@@ -597,14 +601,15 @@ gq_status setup_form() {
 }
 
 // What sharing tiles gives, in us, one block / as many as parts_of gives:
-//   one token to 8 of 128, gated, 2 x 768 x 2048     10.9 / 10.2
-//   to 2 of 8, 2 x 2048 x 4096                       16.4 / 11.0
-//   to one of 16, 2 x 1024 x 8192                    27.8 / 9.0
-//   to 2 of 8, 2 x 768 x 2048                        10.1 / 6.9
-//   to 2 of 8, grad_input, 2 x 4096 x 2048           20.9 / 9.7
-//   16 rows of one expert, gated, 2 x 2048 x 4096    18.3 / 11.1
-// (With two entries each at least the fourth takes 8.0, with four each 10.1;
-// with the sums added and written by the first block alone the last takes 12.9.)
+//   one token to 8 of 128, gated, 2 x 768 x 2048     10.6 / 10.1
+//   to 2 of 8, 2 x 2048 x 4096                       16.1 / 10.7
+//   to one of 16, 2 x 1024 x 8192                    27.3 / 8.8
+//   to 2 of 8, 2 x 768 x 2048                        9.8 / 6.6
+//   to 2 of 8, grad_input, 2 x 4096 x 2048           21.1 / 9.6
+//   16 rows of one expert, gated, 2 x 2048 x 4096    15.9 / 9.8
+// (With two entries each at least the fourth takes 1 us more, with four each 3;
+// with the sums added and written by the first block alone the last takes 2 more.
+// Clusters of three, five, six and seven blocks, where they fit: no faster.)
 template <int kForm>
 gq_status launch_form(const DeviceInfo& info, Params& p, const void* qa, const void* qb, int32_t N,
                       int32_t K, cudaStream_t stream) {
