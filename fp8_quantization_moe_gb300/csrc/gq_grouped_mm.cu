@@ -605,23 +605,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         cluster_wait();
         joined = true;
         if (!part.mine(q)) continue;
-        // its own sums first, then the other blocks' in their order; eight words
-        // are under way at a time
-#pragma unroll 1
-        for (int32_t j = 1; j < part.parts; ++j) {
-          const uint32_t from = map_cluster(own, (part.rank + j) & (part.parts - 1));
+        // (a0 + a1) + (a2 + a3), a_i the sums of block i: each addition commutes, so that
+        // a row has the same bits whichever block adds it up, wherever in the tile it
+        // is.  Eight words are under way at a time.
+        static_assert(kMostParts <= 4, "two rounds of pairs");
+        const uint32_t other = map_cluster(own, part.rank ^ 1);
 #pragma unroll
-          for (int k0 = 0; k0 < kChunks * kChunk; k0 += kChunk) {
-            uint4 v[kChunk / 4];
+        for (int k0 = 0; k0 < kChunks * kChunk; k0 += 32) {
+          uint4 v[8];
 #pragma unroll
-            for (int k = 0; k < kChunk / 4; ++k) v[k] = ld_cluster_128(from + (k0 / 4 + k) * 512);
+          for (int k = 0; k < 8; ++k) v[k] = ld_cluster_128(other + (k0 / 4 + k) * 512);
 #pragma unroll
-            for (int k = 0; k < kChunk / 4; ++k) {
-              float* const o = &acc[k0 / kChunk][4 * k];
-              o[0] += __uint_as_float(v[k].x);
-              o[1] += __uint_as_float(v[k].y);
-              o[2] += __uint_as_float(v[k].z);
-              o[3] += __uint_as_float(v[k].w);
+          for (int k = 0; k < 8; ++k) {
+            float* const o = &acc[k0 / kChunk][4 * k];
+            o[0] += __uint_as_float(v[k].x);
+            o[1] += __uint_as_float(v[k].y);
+            o[2] += __uint_as_float(v[k].z);
+            o[3] += __uint_as_float(v[k].w);
+          }
+        }
+        if (part.parts > 2) {
+          const uint32_t two = map_cluster(own, part.rank ^ 2), three = map_cluster(own, part.rank ^ 3);
+#pragma unroll
+          for (int k0 = 0; k0 < kChunks * kChunk; k0 += 16) {
+            uint4 v[4], w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[k] = ld_cluster_128(two + (k0 / 4 + k) * 512);
+              w[k] = ld_cluster_128(three + (k0 / 4 + k) * 512);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float* const o = &acc[k0 / kChunk][k0 % kChunk + 4 * k];
+              o[0] += __uint_as_float(v[k].x) + __uint_as_float(w[k].x);
+              o[1] += __uint_as_float(v[k].y) + __uint_as_float(w[k].y);
+              o[2] += __uint_as_float(v[k].z) + __uint_as_float(w[k].z);
+              o[3] += __uint_as_float(v[k].w) + __uint_as_float(w[k].w);
             }
           }
         }

@@ -117,8 +117,9 @@ __device__ __forceinline__ int32_t column_of(const Params& p, int32_t kb) {
 
 // Where the tiles are too few for the SMs, `parts` blocks, a cluster, share one:
 // each forms the sum of a run of the contraction's 128-blocks and leaves it in its
-// shared memory; then each adds and writes a part of the tile, the sums in the
-// blocks' order.  (One tile a cluster: the launch sees to it.)
+// shared memory; then each adds and writes a part of the tile, in an order that goes
+// by the number of blocks alone: all rows of a call are added up alike.  (One tile a
+// cluster: the launch sees to it.)
 struct Split {
   int32_t rank, parts;
   int32_t kb0, kb1;  // this block's 128-blocks, from a whole entry of the factor ring on
