@@ -233,28 +233,48 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 
-template <int kSize>
-__device__ __forceinline__ uint4 scale_vec(uint4 v, float f) {
+// What the tensors are multiplied by.  Below fp32's normal values a factor would have
+// lost bits that the products need not lose (1e38 clipped to 1e-7): there it is
+// `wide`, else that is 0.
+struct Factor {
+  float f;
+  double wide;
+};
+
+// A NaN is not below the limit: it becomes the factor.
+__device__ __forceinline__ Factor factor_of(double norm, float most) {
+  if (norm <= most) return {1.0f, 0.0};
+  const double q = most / norm;
+  return {static_cast<float>(q), q < 0x1p-126 ? q : 0.0};
+}
+
+template <bool kWide>
+__device__ __forceinline__ float times(float x, const Factor& f) {
+  return kWide ? static_cast<float>(x * f.wide) : x * f.f;
+}
+
+template <int kSize, bool kWide>
+__device__ __forceinline__ uint4 scale_vec(uint4 v, const Factor& f) {
   constexpr int kVec = 16 / kSize;
   float x[kVec];
   widen<kSize>(x, v);
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k)
-    w[k] = kSize == 4 ? __float_as_uint(x[k] * f)
-                      : bf16x2_of(x[(2 * k) % kVec] * f, x[(2 * k + 1) % kVec] * f);
+    w[k] = kSize == 4 ? __float_as_uint(times<kWide>(x[k], f))
+                      : bf16x2_of(times<kWide>(x[(2 * k) % kVec], f), times<kWide>(x[(2 * k + 1) % kVec], f));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int kSize>
-__device__ __forceinline__ void store_part(const Part& t, const Chunk& k, float f) {
+template <int kSize, bool kWide>
+__device__ __forceinline__ void store_part(const Part& t, const Chunk& k, const Factor& f) {
   uint8_t* const to = k.out + k.head * kSize;
   const bool vectors = (reinterpret_cast<uintptr_t>(to) & 15) == 0;
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int32_t i = threadIdx.x + j * kThreads;
     if (i >= k.vecs) continue;
-    const uint4 v = scale_vec<kSize>(t.v[j], f);
+    const uint4 v = scale_vec<kSize, kWide>(t.v[j], f);
     if (vectors) {
       __stcs(reinterpret_cast<uint4*>(to) + i, v);
     } else {  // the tensor and its output lie differently in their 16 bytes
@@ -269,7 +289,20 @@ __device__ __forceinline__ void store_part(const Part& t, const Chunk& k, float 
     }
   }
   const int32_t at = single_of(k);
-  if (at >= 0) store_one(k.out + at, kSize, t.one * f);
+  if (at >= 0) store_one(k.out + at, kSize, times<kWide>(t.one, f));
+}
+
+__device__ __forceinline__ void scale_part(const Part& t, const Chunk& k, const Factor& f) {
+  if (f.wide != 0.0) {
+    if (k.size == 4)
+      store_part<4, true>(t, k, f);
+    else
+      store_part<2, true>(t, k, f);
+  } else if (k.size == 4) {
+    store_part<4, false>(t, k, f);
+  } else {
+    store_part<2, false>(t, k, f);
+  }
 }
 
 struct ClipParams {
@@ -294,9 +327,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   const double norm = p.given != nullptr ? static_cast<double>(__ldg(p.given))
                                          : norm_of(p.partial, p.partials, red);
   if (p.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
-  // a NaN is not below the limit: it becomes the factor
-  const float f = norm <= p.most ? 1.0f : static_cast<float>(p.most / norm);
-  if (f == 1.0f && p.in_place) return;
+  const Factor f = factor_of(norm, p.most);
+  if (f.f == 1.0f && p.in_place) return;
   while (true) {
     const Chunk last = k;
     const bool more = c >= step;
@@ -306,10 +338,7 @@ __global__ void __launch_bounds__(kThreads, 4)
       k = chunk_of(tab, c);
       load_part(next, k);
     }
-    if (last.size == 4)
-      store_part<4>(t, last, f);
-    else
-      store_part<2>(t, last, f);
+    scale_part(t, last, f);
     if (!more) break;
     t = next;
   }
@@ -344,15 +373,12 @@ __global__ void __launch_bounds__(kThreads)
   cluster_arrive();  // waited for below: a block's sum is read until then
   const double norm = sqrt(total);
   if (first == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
-  const float f = norm <= p.most ? 1.0f : static_cast<float>(p.most / norm);
-  if (write && !(f == 1.0f && p.in_place)) {
+  const Factor f = factor_of(norm, p.most);
+  if (write && !(f.f == 1.0f && p.in_place)) {
     for (int32_t c = first; c < chunks; c += step) {
       const Chunk k = chunk_of(tab, c);
       if (chunks > step) load_part(t, k);  // else t still holds the only one
-      if (k.size == 4)
-        store_part<4>(t, k, f);
-      else
-        store_part<2>(t, k, f);
+      scale_part(t, k, f);
     }
   }
   cluster_wait();

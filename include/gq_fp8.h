@@ -548,7 +548,8 @@ gq_status gq_grad_norm(const void* const* grads, const int64_t* sizes, const int
 /*
  * The tensors scaled to a norm of at most max_norm:
  *     y = x * (norm <= max_norm ? 1 : max_norm / norm)
- * in fp32, rounded once to the tensor's type.  A NaN norm makes every element
+ * in fp32, rounded once to the tensor's type (a factor below fp32's normal values is
+ * not rounded to one of fp32 before).  A NaN norm makes every element
  * a NaN; an infinite one makes the finite elements zeros.  In place, a factor
  * of 1 writes nothing.
  *
