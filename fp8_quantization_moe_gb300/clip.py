@@ -111,7 +111,8 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *,
     (each its own gradient, or memory of no other); by default the gradients
     themselves, which are then left alone where nothing is to be scaled.
     Returns the norm.  A NaN norm makes every element a NaN, an infinite one
-    every finite element zero.
+    (also of finite elements, past 3.4e38) every finite element zero.
+    ``norm=grad_norm(grads)`` gives the same bits as none.
     """
     name = "clip_grads"
     max_norm = float(max_norm)

@@ -218,19 +218,24 @@ __global__ void __launch_bounds__(kThreads, 4)
   if (threadIdx.x == 0) partial[blockIdx.x] = sum;
 }
 
+// The norm from the sum of all squares.  What scales the tensors is this fp32 value,
+// not the fp64 root: the same norm handed back as a given one has to give the same
+// result, zeros past fp32's range among them.
+__device__ __forceinline__ float root_of(double sum) { return static_cast<float>(sqrt(sum)); }
+
 // The norm from all partial sums, in one order.
-__device__ __forceinline__ double norm_of(const double* partial, int32_t partials, double* red) {
+__device__ __forceinline__ float norm_of(const double* partial, int32_t partials, double* red) {
   double sum = 0.0;
   for (int32_t i = threadIdx.x; i < partials; i += kThreads) sum += __ldg(partial + i);
-  return sqrt(block_sum(sum, red));
+  return root_of(block_sum(sum, red));
 }
 
 __global__ void __launch_bounds__(kThreads)
     norm_kernel(const double* partial, int32_t partials, float* norm) {
   __shared__ double red[kWarps];
   grid_wait();
-  const double v = norm_of(partial, partials, red);
-  if (threadIdx.x == 0) *norm = static_cast<float>(v);
+  const float v = norm_of(partial, partials, red);
+  if (threadIdx.x == 0) *norm = v;
 }
 
 // What the tensors are multiplied by.  Below fp32's normal values a factor would have
@@ -242,9 +247,9 @@ struct Factor {
 };
 
 // A NaN is not below the limit: it becomes the factor.
-__device__ __forceinline__ Factor factor_of(double norm, float most) {
+__device__ __forceinline__ Factor factor_of(float norm, float most) {
   if (norm <= most) return {1.0f, 0.0};
-  const double q = most / norm;
+  const double q = static_cast<double>(most) / norm;
   return {static_cast<float>(q), q < 0x1p-126 ? q : 0.0};
 }
 
@@ -324,9 +329,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   grid_wait();
   Part t;
   load_part(t, k);
-  const double norm = p.given != nullptr ? static_cast<double>(__ldg(p.given))
-                                         : norm_of(p.partial, p.partials, red);
-  if (p.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
+  const float norm = p.given != nullptr ? __ldg(p.given) : norm_of(p.partial, p.partials, red);
+  if (p.norm != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = norm;
   const Factor f = factor_of(norm, p.most);
   if (f.f == 1.0f && p.in_place) return;
   while (true) {
@@ -371,8 +375,8 @@ __global__ void __launch_bounds__(kThreads)
   double total = 0.0;
   for (int32_t b = 0; b < step; ++b) total += ld_cluster_f64(map_cluster(smem_addr(&mine), b));
   cluster_arrive();  // waited for below: a block's sum is read until then
-  const double norm = sqrt(total);
-  if (first == 0 && threadIdx.x == 0) *p.norm = static_cast<float>(norm);
+  const float norm = root_of(total);
+  if (first == 0 && threadIdx.x == 0) *p.norm = norm;
   const Factor f = factor_of(norm, p.most);
   if (write && !(f.f == 1.0f && p.in_place)) {
     for (int32_t c = first; c < chunks; c += step) {

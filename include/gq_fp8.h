@@ -549,9 +549,11 @@ gq_status gq_grad_norm(const void* const* grads, const int64_t* sizes, const int
  * The tensors scaled to a norm of at most max_norm:
  *     y = x * (norm <= max_norm ? 1 : max_norm / norm)
  * in fp32, rounded once to the tensor's type (a factor below fp32's normal values is
- * not rounded to one of fp32 before).  A NaN norm makes every element
- * a NaN; an infinite one makes the finite elements zeros.  In place, a factor
- * of 1 writes nothing.
+ * not rounded to one of fp32 before).  norm is the fp32 value that is written, or
+ * given: the tensors' norm from gq_grad_norm handed in as given_norm gives the same
+ * bits.  A NaN norm makes every element a NaN; an infinite one (also of finite
+ * elements, past 3.4e38) makes the finite elements zeros.  In place, a factor of 1
+ * writes nothing.
  *
  *   grads, sizes, dtypes, count   as in gq_grad_norm.              (input)
  *   outs     device pointers, each aligned to its elements, or NULL: in place.

@@ -67,3 +67,24 @@ def test_factors_below_fp32(gq, dtype, long, scale, most):
     placed = [t.clone() for t in ts]
     gq.clip_grads(placed, most)
     check_scaled(placed, ts, most, norm)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("long", [False, True])
+@pytest.mark.parametrize("scale,most", [(1.0, 0.5), (1e-20, 3e-22), (1e38, 1e-8), (1e30, 2e29), (2.2e38, 1.0), (2.2e38, 1e38), (1.0, 1e9)])
+def test_one_meaning_of_the_norm(gq, dtype, long, scale, most):
+    """The tensors' own norm and the same norm handed in: the same bits, also where
+    the norm of finite elements is past fp32 (2.2e38: 3.8e38 and more)."""
+    ts = tensors(dtype, scale, long)
+    norm = gq.grad_norm(ts)
+    a, b = ([torch.full_like(t, 7.0) for t in ts] for _ in range(2))
+    assert torch.equal(gq.clip_grads(ts, most, out=a), norm)
+    gq.clip_grads(ts, most, norm=norm, out=b)
+    placed = [t.clone() for t in ts]
+    gq.clip_grads(placed, most, norm=norm)
+    for x, y, z in zip(a, b, placed):
+        assert torch.equal(x, y) and torch.equal(x, z)
+    past = norm64(ts) > torch.finfo(torch.float32).max * (1 + 2.0 ** -20)
+    assert past == (scale > 2e38) and bool(torch.isinf(norm)) == past
+    if past:
+        assert all(bool((x == 0).all()) for x in a)
