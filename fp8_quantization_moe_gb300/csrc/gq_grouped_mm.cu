@@ -600,7 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                  __float_as_uint(v[2]), __float_as_uint(v[3])));
           }
         }
-        __syncwarp();
         cluster_arrive();
         cluster_wait();
         joined = true;
@@ -704,7 +703,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (kSplit) {
     // Every thread meets the cluster's barrier twice: with the sums written, and
     // with them read, before a block that holds some may leave.
-    __syncwarp();
     if (!joined) {
       cluster_arrive();
       cluster_wait();

@@ -283,7 +283,6 @@ __device__ __forceinline__ bool tile_body(const Params& p, const Split& part, Sm
                  make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
                             __float_as_uint(v[3])));
         }
-    __syncwarp();
     cluster_arrive();
     cluster_wait();
     x.joined = true;
@@ -564,7 +563,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (kSplit) {
     // Every thread meets the cluster's barrier twice: with the sums written, and
     // with them read, before a block that holds some may leave.
-    __syncwarp();
     if (!joined) {
       cluster_arrive();
       cluster_wait();
