@@ -107,9 +107,10 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *,
 
     grads: as in ``grad_norm``, each tensor once.  norm: a float32 scalar on
     the device to use instead of the tensors' own norm (that of more tensors
-    than these, say).  out: tensors to write, of the same types and sizes
-    (each its own gradient, or memory of no other); by default the gradients
-    themselves, which are then left alone where nothing is to be scaled.
+    than these, say), no element of a tensor that is written.  out: tensors to
+    write, of the same types and sizes (each its own gradient, or memory of no
+    other); by default the gradients themselves, which are then left alone
+    where nothing is to be scaled.
     Returns the norm.  A NaN norm makes every element a NaN, an infinite one
     (also of finite elements, past 3.4e38) every finite element zero.
     ``norm=grad_norm(grads)`` gives the same bits as none.

@@ -899,7 +899,7 @@ gq_status gq_clip_grads(const void* const* grads, void* const* outs, const int64
     st = validate_ws(workspace, workspace_bytes, gq_grad_norm_workspace_bytes(sizes, dtypes, count), name);
     if (st != GQ_OK) return st;
   }
-  st = clip::check_overlap(grads, outs, sizes, dtypes, count);
+  st = clip::check_overlap(grads, outs, sizes, dtypes, count, given_norm, norm);
   if (st != GQ_OK) return st;
   const DeviceInfo* info = nullptr;
   st = current_device(&info);

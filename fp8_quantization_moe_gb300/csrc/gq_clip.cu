@@ -480,10 +480,12 @@ size_t workspace_bytes(const int64_t* sizes, const int32_t* dtypes, int32_t coun
 }
 
 // Whether an element would be written twice, or written through one pointer
-// and read through another: outputs that overlap, or an input that overlaps
-// an output other than its own.
+// and read through another: outputs that overlap, an input that overlaps an output
+// other than its own, a norm that is read inside an output, or one that is written
+// inside any tensor.
 gq_status check_overlap(const void* const* in, void* const* out, const int64_t* sizes,
-                        const int32_t* dtypes, int32_t count) {
+                        const int32_t* dtypes, int32_t count, const float* given,
+                        const float* norm) {
   std::unique_ptr<Range[]> r(new (std::nothrow) Range[count > 0 ? count : 1]);
   if (!r) return fail(GQ_ERR_UNSUPPORTED, "gq_clip_grads: no host memory for %d tensors", count);
   int32_t n = 0;
@@ -497,14 +499,22 @@ gq_status check_overlap(const void* const* in, void* const* out, const int64_t* 
   for (int32_t i = 1; i < n; ++i)
     if (r[i].from < r[i - 1].to)
       return fail(GQ_ERR_INVALID_ARG, "gq_clip_grads: two outputs overlap");
-  if (out == nullptr) return GQ_OK;
-  for (int32_t i = 0; i < count; ++i) {
-    if (sizes[i] == 0 || in[i] == out[i]) continue;
-    const Range a = range(in[i], i);
+  auto hits_output = [&](const Range& a) {
     // the first output that ends behind a's start
     const Range* const b = std::upper_bound(
         r.get(), r.get() + n, a.from, [](uintptr_t v, const Range& x) { return v < x.to; });
-    if (b != r.get() + n && b->from < a.to)
+    return b != r.get() + n && b->from < a.to;
+  };
+  const float* const value = given != nullptr ? given : norm;
+  const Range at = {reinterpret_cast<uintptr_t>(value), reinterpret_cast<uintptr_t>(value + 1)};
+  if (hits_output(at)) return fail(GQ_ERR_INVALID_ARG, "gq_clip_grads: the norm overlaps an output");
+  if (out == nullptr) return GQ_OK;
+  for (int32_t i = 0; i < count; ++i) {
+    if (sizes[i] == 0) continue;
+    const Range a = range(in[i], i);
+    if (given == nullptr && a.from < at.to && at.from < a.to)
+      return fail(GQ_ERR_INVALID_ARG, "gq_clip_grads: the norm overlaps tensor %d", i);
+    if (in[i] != out[i] && hits_output(a))
       return fail(GQ_ERR_INVALID_ARG, "gq_clip_grads: tensor %d overlaps an output", i);
   }
   return GQ_OK;

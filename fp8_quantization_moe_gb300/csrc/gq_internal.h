@@ -177,7 +177,8 @@ gq_status launch_backward(const void* g, const void* pre, bool f32, int64_t rows
 namespace clip {
 size_t workspace_bytes(const int64_t* sizes, const int32_t* dtypes, int32_t count);
 gq_status check_overlap(const void* const* in, void* const* out, const int64_t* sizes,
-                        const int32_t* dtypes, int32_t count);
+                        const int32_t* dtypes, int32_t count, const float* given,
+                        const float* norm);
 // The norm of the tensors, unless `given`, to `norm`, unless nullptr; with
 // `write` the tensors scaled to `most`, into `out` or in place.
 gq_status launch(const DeviceInfo& info, const void* const* in, void* const* out, bool write,

@@ -557,8 +557,9 @@ gq_status gq_grad_norm(const void* const* grads, const int64_t* sizes, const int
  *
  *   grads, sizes, dtypes, count   as in gq_grad_norm.              (input)
  *   outs     device pointers, each aligned to its elements, or NULL: in place.
- *            An output may be its own tensor; overlaps between outputs, or of
- *            an output with another tensor, are refused.          (output)
+ *            An output may be its own tensor; overlaps between outputs, of an
+ *            output with another tensor, of an output with given_norm, or of
+ *            norm with any tensor are refused.                    (output)
  *   max_norm at least 0.
  *   given_norm  fp32, device, or NULL: a norm to use instead of the tensors'
  *            own (of more tensors than these, say); norm and workspace are

@@ -88,3 +88,19 @@ def test_one_meaning_of_the_norm(gq, dtype, long, scale, most):
     assert past == (scale > 2e38) and bool(torch.isinf(norm)) == past
     if past:
         assert all(bool((x == 0).all()) for x in a)
+
+
+def test_given_norm_and_the_tensors(gq):
+    """A given norm may lie in a tensor that is only read, and right beside one
+    that is written; in one that is written it is refused."""
+    t = torch.arange(1.0, 1001.0, device=DEV)
+    out = torch.zeros_like(t)
+    gq.clip_grads([t], 50.0, norm=t[99], out=[out])  # 100
+    assert torch.equal(out, t * 0.5)
+    u = t.clone()
+    gq.clip_grads([u[:99], u[100:]], 50.0, norm=u[99])
+    assert torch.equal(u[:99], t[:99] * 0.5) and torch.equal(u[100:], t[100:] * 0.5) and float(u[99]) == 100.0
+    for grads, out in (([u], None), ([u[99:]], None), ([t], [u])):
+        with pytest.raises(gq.GQError, match="overlap"):
+            gq.clip_grads(grads, 50.0, norm=u[99], out=out)
+    assert float(u[99]) == 100.0
