@@ -306,6 +306,21 @@ gq_status validate_operands(const void* qa, const float* sa, const void* qb, con
   return GQ_OK;
 }
 
+// Memory that a call reads or writes: `rows` runs of `width` bytes, `pitch` apart.
+struct Span {
+  const void* p;
+  int64_t width, rows = 1, pitch = 0;
+};
+
+// Whether any byte of `a` lies in `b`, one run; not where one of them is missing.
+bool overlaps(const Span& a, const Span& b) {
+  if (a.p == nullptr || b.p == nullptr || a.width <= 0 || b.width <= 0) return false;
+  const intptr_t from = reinterpret_cast<intptr_t>(a.p), lo = reinterpret_cast<intptr_t>(b.p);
+  // the first run of `a` that ends behind b's start
+  const int64_t i = from + a.width > lo ? 0 : a.rows > 1 ? (lo - from - a.width) / a.pitch + 1 : 1;
+  return i < a.rows && from + i * a.pitch < lo + b.width;
+}
+
 constexpr int32_t kMaxTensors = 1 << 20;
 constexpr int64_t kMaxElements = int64_t(1) << 42;  // of all tensors
 
@@ -844,6 +859,15 @@ gq_status gq_gated_backward(const void* g, const void* pre, int dtype, int64_t r
       !aligned(scales, 4))
     return fail(GQ_ERR_INVALID_ARG,
                 "%s: inputs and outputs must be 16-byte aligned, scales 4-byte aligned", name);
+  const Span gs = {g, N * size, rows, ld * size}, ps = {pre, rows * 2 * N * size};
+  const Span os = {out, rows * 2 * N * size}, qs = {q, rows * 2 * N};
+  const Span ss = {q != nullptr ? scales : nullptr, rows * 2 * ((N + 127) / 128) * 4};
+  // out may be pre itself: a lane reads its columns of both halves before it writes them
+  if (overlaps(gs, os) || (out != pre && overlaps(ps, os)) || overlaps(gs, qs) || overlaps(ps, qs) ||
+      overlaps(gs, ss) || overlaps(ps, ss))
+    return fail(GQ_ERR_INVALID_ARG, "%s: an output overlaps an input", name);
+  if (overlaps(os, qs) || overlaps(os, ss) || overlaps(qs, ss))
+    return fail(GQ_ERR_INVALID_ARG, "%s: two outputs overlap", name);
   const DeviceInfo* info = nullptr;
   st = current_device(&info);
   if (st != GQ_OK) return st;

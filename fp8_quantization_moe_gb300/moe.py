@@ -374,9 +374,10 @@ def gated_backward(g: torch.Tensor, pre: torch.Tensor, *, activation: str = "sil
     """The gradients of the two projections of ``grouped_gated_mm``: g (M, N),
     possibly with a pitch, is the gradient of its rows, pre (M, 2, N) the
     projections, both bf16 or both float32.  Returns GatedRows: out (M, 2, N)
-    of g's type (``plain`` or ``out``, which may be ``pre`` itself), q e4m3
-    (M, 2, N) and scales float32 (M, 2, ceil(N / 128)) for
-    ``grouped_gated_grad`` (``fp8``, ``q`` or ``scales``)."""
+    of g's type (``plain`` or ``out``, which may be ``pre`` itself, but no
+    output may overlap an input otherwise), q e4m3 (M, 2, N) and scales float32
+    (M, 2, ceil(N / 128)) for ``grouped_gated_grad`` (``fp8``, ``q`` or
+    ``scales``)."""
     name = "gated_backward"
     _need(g, name + ": g", 2, _FLOAT, contiguous=False)
     M, N = g.shape

@@ -491,8 +491,8 @@ gq_status gq_grouped_gated_mm(const void* qa, const float* sa, int64_t M, const 
  *   pre      g's type [rows, 2, N], 16-byte aligned: x and u.      (input)
  *   rows, N  N % 16 == 0, N <= 2^22; rows * ceil(N / 128) < 2^31.
  *   out      g's type [rows, 2, N], 16-byte aligned, or NULL: dx and du.  It
- *            may be pre itself, but no output overlaps an input otherwise.
- *                                                                 (output)
+ *            may be pre itself; an output that overlaps an input otherwise, or
+ *            another output, is refused.                          (output)
  *   q, scales   e4m3 [rows, 2, N], 16-byte aligned, and fp32 [rows, 2,
  *            ceil(N / 128)], or NULL: dx and du quantized as
  *            gq_fp8_block_rows does it, from the fp32 values.  One of out and
