@@ -321,6 +321,21 @@ bool overlaps(const Span& a, const Span& b) {
   return i < a.rows && from + i * a.pitch < lo + b.width;
 }
 
+// Refuses `n` outputs that overlap one of `m` inputs, or one another.
+gq_status validate_apart(const Span* out, int n, const Span* in, int m, const char* name) {
+  for (int i = 0; i < n; ++i) {
+    for (int j = 0; j < m; ++j)
+      if (overlaps(in[j], out[i]))
+        return fail(GQ_ERR_INVALID_ARG, "%s: an output overlaps an input", name);
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[j], out[i]))
+        return fail(GQ_ERR_INVALID_ARG, "%s: two outputs overlap", name);
+  }
+  return GQ_OK;
+}
+
+int64_t blocks_of(int64_t n) { return (n + 127) / 128; }
+
 constexpr int32_t kMaxTensors = 1 << 20;
 constexpr int64_t kMaxElements = int64_t(1) << 42;  // of all tensors
 
@@ -801,13 +816,22 @@ gq_status gq_grouped_gated_mm(const void* qa, const float* sa, int64_t M, const 
   if (K == 0) return fail(GQ_ERR_UNSUPPORTED, "%s: the contraction has no columns", name);
   st = validate_operands(qa, sa, qb, sb, name);
   if (st != GQ_OK) return st;
+  const int64_t mats = 2 * int64_t(n_groups);
+  const Span in[] = {{qa, M * K},
+                     {sa, M * blocks_of(K) * 4},
+                     {qb, mats * N * K},
+                     {sb, mats * blocks_of(N) * blocks_of(K) * 4},
+                     {offs, int64_t(n_groups) * 4}};
+  const Span written[] = {
+      {out, M * N * 2}, {q, M * N}, {q != nullptr ? scales : nullptr, M * blocks_of(N) * 4}, {pre, M * N * 4}};
+  st = validate_apart(written, 4, in, 5, name);
+  if (st != GQ_OK) return st;
   const DeviceInfo* info = nullptr;
   st = current_device(&info);
   if (st != GQ_OK) return st;
   return gmm::launch_gated(*info, g_dbg, qa, sa, M, qb, sb, static_cast<int32_t>(N),
-                               static_cast<int32_t>(K), activation, offs, n_groups, out, q, scales,
-                               pre, (flags & GQ_SCALE_POW2) != 0,
-                               reinterpret_cast<cudaStream_t>(stream));
+                           static_cast<int32_t>(K), activation, offs, n_groups, out, q, scales, pre,
+                           (flags & GQ_SCALE_POW2) != 0, reinterpret_cast<cudaStream_t>(stream));
 }
 
 gq_status gq_grouped_gated_grad(const void* qd, const float* sd, int64_t M, const void* qb,
@@ -823,6 +847,15 @@ gq_status gq_grouped_gated_grad(const void* qd, const float* sd, int64_t M, cons
     return fail(GQ_ERR_INVALID_ARG, "%s: misaligned offsets or output", name);
   if (N == 0) return fail(GQ_ERR_UNSUPPORTED, "%s: the contraction has no columns", name);
   st = validate_operands(qd, sd, qb, sb, name);
+  if (st != GQ_OK) return st;
+  const int64_t mats = 2 * int64_t(n_groups);
+  const Span in[] = {{qd, M * 2 * N},
+                     {sd, M * 2 * blocks_of(N) * 4},
+                     {qb, mats * N * K},
+                     {sb, mats * blocks_of(N) * blocks_of(K) * 4},
+                     {offs, int64_t(n_groups) * 4}};
+  const Span written = {out, M * K * 2};
+  st = validate_apart(&written, 1, in, 5, name);
   if (st != GQ_OK) return st;
   const DeviceInfo* info = nullptr;
   st = current_device(&info);
@@ -861,13 +894,11 @@ gq_status gq_gated_backward(const void* g, const void* pre, int dtype, int64_t r
                 "%s: inputs and outputs must be 16-byte aligned, scales 4-byte aligned", name);
   const Span gs = {g, N * size, rows, ld * size}, ps = {pre, rows * 2 * N * size};
   const Span os = {out, rows * 2 * N * size}, qs = {q, rows * 2 * N};
-  const Span ss = {q != nullptr ? scales : nullptr, rows * 2 * ((N + 127) / 128) * 4};
+  const Span ss = {q != nullptr ? scales : nullptr, rows * 2 * blocks_of(N) * 4};
   // out may be pre itself: a lane reads its columns of both halves before it writes them
-  if (overlaps(gs, os) || (out != pre && overlaps(ps, os)) || overlaps(gs, qs) || overlaps(ps, qs) ||
-      overlaps(gs, ss) || overlaps(ps, ss))
-    return fail(GQ_ERR_INVALID_ARG, "%s: an output overlaps an input", name);
-  if (overlaps(os, qs) || overlaps(os, ss) || overlaps(qs, ss))
-    return fail(GQ_ERR_INVALID_ARG, "%s: two outputs overlap", name);
+  const Span in[] = {gs, out == pre ? Span{nullptr, 0} : ps}, written[] = {os, qs, ss};
+  st = validate_apart(written, 3, in, 2, name);
+  if (st != GQ_OK) return st;
   const DeviceInfo* info = nullptr;
   st = current_device(&info);
   if (st != GQ_OK) return st;

@@ -471,7 +471,8 @@ gq_status gq_grouped_mm(const void* qa, const float* sa, int64_t M, const void* 
  *            gq_gated_backward.                                   (output)
  *   flags    0 or GQ_SCALE_POW2.
  *   stream   the CUDA stream to run on.  No workspace.
- * Rows behind the last end are left untouched in every output.
+ * Rows behind the last end are left untouched in every output.  An output that
+ * overlaps an input or another output is refused.
  */
 #define GQ_ACT_SILU 0
 #define GQ_ACT_GELU 1
@@ -514,7 +515,7 @@ gq_status gq_gated_backward(const void* g, const void* pre, int dtype, int64_t r
  *   sd       fp32 [M, 2, ceil(N / 128)].                           (input)
  *   qb, sb, offs, n_groups   as in gq_grouped_gated_mm; N at least 16.
  *   out      bf16 [M, K], 16-byte aligned; rows behind the last end are left
- *            untouched.                                           (output)
+ *            untouched.  One that overlaps an input is refused.   (output)
  *   stream   the CUDA stream to run on.  No workspace.
  */
 gq_status gq_grouped_gated_grad(const void* qd, const float* sd, int64_t M, const void* qb,

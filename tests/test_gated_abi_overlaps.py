@@ -100,3 +100,46 @@ def test_gated_backward_takes_what_does_not_overlap(gq):
                dict(out=lambda p, s: p["g"] - s["out"])):
         status = backward(gq, **kw)
         assert status not in (0, INVALID), kw
+
+
+def product(gq, form, M=5, N=144, K=272, E=3, **at):
+    n, k = -(-N // 128), -(-K // 128)
+    weights = dict(qb=E * 2 * N * K, sb=E * 2 * n * k * 4, offs=E * 4 + 4)
+    if form == "mm":
+        sizes = dict(qa=M * K, sa=M * k * 4 + 4, **weights, out=M * N * 2, q=M * N, scales=M * n * 4, pre=M * 2 * N * 2)
+    else:
+        sizes = dict(qa=M * 2 * N, sa=M * 2 * n * 4, **weights, out=M * K * 2)
+    sizes = {name: -(-size // 16) * 16 for name, size in sizes.items()}
+    p, _ = spread(sizes)
+    p.update({name: v(p, sizes) if callable(v) else v for name, v in at.items()})
+    a = p["qa"], p["sa"], M, p["qb"], p["sb"], N, K
+    if form == "mm":
+        return gq.lib().gq_grouped_gated_mm(*a, 0, p["offs"], E, p["out"], p["q"], p["scales"], p["pre"], 0, None)
+    return gq.lib().gq_grouped_gated_grad(*a, p["offs"], E, p["out"], None)
+
+
+@pytest.mark.parametrize("which", ["qa", "sa", "qb", "sb", "offs"])
+def test_products_refuse_outputs_over_inputs(gq, which):
+    for form in ("mm", "grad"):
+        for name in ("out", "q", "scales", "pre") if form == "mm" else ("out",):
+            refused(gq, product(gq, form, **{name: lambda p, s: p[which]}))
+            refused(gq, product(gq, form, **{name: lambda p, s: p[which] - s[name] + 16}))
+
+
+def test_products_refuse_outputs_over_outputs(gq):
+    names = ("out", "q", "scales", "pre")
+    for a in names:
+        for b in names:
+            if a != b:
+                refused(gq, product(gq, "mm", **{a: lambda p, s: p[b]}))
+                refused(gq, product(gq, "mm", **{a: lambda p, s: p[b] + s[b] // 32 * 16}))
+
+
+def test_products_take_what_does_not_overlap(gq):
+    import torch
+
+    if torch.cuda.is_available():
+        pytest.skip("addresses are made up")
+    for form, kw in (("mm", {}), ("grad", {}), ("mm", dict(out=None)), ("mm", dict(pre=None)),
+                     ("mm", dict(q=None, scales=lambda p, s: p["out"]))):  # scales of no rows are not written
+        assert product(gq, form, **kw) not in (0, INVALID)
