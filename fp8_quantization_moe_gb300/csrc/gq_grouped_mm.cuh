@@ -46,6 +46,9 @@ struct Params {
   uint16_t* pre;
   gated::Act act;
   bool pow2;
+  // Of two launches one works (see kPairRows): with more than pairs_over rows that in
+  // pairs of blocks (pairs_only 1), else the other (-1).  0: the only launch.
+  int32_t pairs_only, pairs_over;
   uint64_t timeout_ns;
   int32_t skip_arrival;  // test hook: block 0 never frees its first accumulator
 };
