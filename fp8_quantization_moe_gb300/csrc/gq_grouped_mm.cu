@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   grid_wait();
-  if (p.pairs_only != 0) {  // the rows that there are: the highest end, up to M (above pairs_over)
+  if (may_choose(kForm) && p.pairs_only != 0) {
     bool past = false;
     for (int32_t g = threadIdx.x; g < p.E; g += kThreads) past |= __ldg(p.offs + g) > p.pairs_over;
     if ((__syncthreads_or(past) != 0) != (p.pairs_only > 0)) return;
@@ -752,14 +752,16 @@ constexpr int kFewRows = 48, kFewRowsGated = 24;
 //   forward 92/85 97/105 103/121 130/159 274/354, transposed 90/78 92/96 104/113 118/144 234/330
 // With rows of whole lines (64 of 1024 x 2048, gated): 64/51 64/57 71/57 86/71
 // (200 rows) 127/120 (400), at 1040 rows of 16 x 2048 x 4096 232/238.
-// The rows are those in front of the last end.  The host knows the buffer's alone, of
-// which a layer with a part of the experts may fill little: where these are enough for
-// pairs, it launches both kernels, and the blocks of the one that the ends do not want
-// leave again, 1.5 us in a call.  Chosen by the buffer, 64 groups as above in a buffer
-// of 16 times their rows took, at 16, 32 and 64 rows each, pairs / single blocks /
-// both launched
+// For the plain products the rows are those in front of the last end.  The host knows
+// the buffer's alone, of which a layer with a part of the experts may fill little:
+// where these are enough for pairs, it launches both kernels, and the blocks of the
+// one that the ends do not want leave again: 1.5 us in a call, up to 4 % where the
+// groups have many rows.  64 groups as above in a buffer of 16 times their rows, at 16,
+// 32 and 64 rows each, pairs / single blocks / both launched
 //   forward 50/39/40 51/40/42 54/45/47, transposed 49/41/42 50/42/42 53/47/48
-//   gated 99/73/79 98/74/82 101/79/87, grad_input of it 84/75/75 86/79/79 90/86/87
+// The gated forms go by the buffer's rows: gated 99/73/79 98/74/82 101/79/87 there,
+// grad_input of it 84/75/75 86/79/79 90/86/87, but 40 groups of 614 rows in a buffer of
+// four times as many, gated to fp8, 186/-/190 in a run of nothing but this call.
 constexpr int kPairRows = 96;
 constexpr int kPairTiles = 3;  // per SM
 
@@ -901,7 +903,7 @@ gq_status launch_form(const DeviceInfo& info, Params& p, const void* qa, const v
     p.pairs_over = kPairRows * p.E;
     p.pairs_only = 1;
     const gq_status st = launch_many<kForm, 2>(info, p, qa, qb, N, K, stream);
-    if (st != GQ_OK) return st;
+    if (st != GQ_OK || !may_choose(kForm)) return st;
     p.pairs_only = -1;
   }
   return launch_many<kForm, 1>(info, p, qa, qb, N, K, stream);

@@ -46,8 +46,9 @@ struct Params {
   uint16_t* pre;
   gated::Act act;
   bool pow2;
-  // Of two launches one works (see kPairRows): with more than pairs_over rows that in
-  // pairs of blocks (pairs_only 1), else the other (-1).  0: the only launch.
+  // Plain products: of two launches one works (see kPairRows), with more than
+  // pairs_over rows that in pairs of blocks (pairs_only 1), else the other (-1); 0: the
+  // only launch.
   int32_t pairs_only, pairs_over;
   uint64_t timeout_ns;
   int32_t skip_arrival;  // test hook: block 0 never frees its first accumulator
@@ -169,6 +170,9 @@ __device__ __forceinline__ Tile tile_of(const Params& p, const TileTable& s, int
 // The gated forms share tiles; the plain products add their 128-blocks in one
 // order, whatever the sizes, as they always have.
 constexpr bool may_split(int form) { return form == kGated || form == kGatedGrad; }
+
+// The plain products choose between pairs and single blocks on the device.
+__host__ __device__ constexpr bool may_choose(int form) { return form == kForward || form == kTransposed; }
 
 // Blocks per tile, up to `at_most`: as many as are resident at once if there are
 // `tiles` of them, each with an entry of the factor ring at least.
