@@ -768,9 +768,11 @@ constexpr int kPairTiles = 3;  // per SM
 // Blocks share a tile of the gated forms where there are few tiles and more than
 // this many 128-blocks: joining the sums takes 4 us, a 128-block 0.45.  In us, one
 // block / as many as parts_of gives, 128-blocks in brackets: 128 rows of one
-// expert, 2 x 2048 x 4096, gated 17.1/12.6 (32), its grad_input 16.6/12.0 (32); 100 of
-// one, 2 x 768 x 7168, 25.6/14.9 (56) and 8.6/10.3 (12); 256 of four, 2 x 1024 x 4096,
-// 17.6/15.5 (32); 128 of two, 2 x 1408 x 2048, 10.7/11.0 (16) and 12.2/11.1 (22).
+// expert, 2 x 2048 x 4096, gated 17.3/13.7 (32), its grad_input 16.8/12.2 (32); 100 of
+// one, 2 x 768 x 7168, 25.6/16.1 (56) and 9.1/11.1 (12); 256 of four, 2 x 1024 x 4096,
+// 17.3/15.3 (32); 128 of two, 2 x 1408 x 2048, 11.3/12.1 (16) and 12.8/12.1 (22).
+// (Each block's own sum first, whichever it is, 0.7 us less where four share a tile;
+// but then a row's last bits go by its place in the tile.)
 constexpr int kSplitKbs = 20;
 
 }  // namespace
